@@ -54,11 +54,13 @@ typedef enum {
     KDA_ERR_TOO_LARGE = 8,         /* sizes exceed what the library indexes              */
     KDA_ERR_TIMEOUT = 9,           /* a kernel gave up on a bounded wait (see kda_device_error) */
     KDA_ERR_NOALLOC_LIMIT = 10,    /* kda_fwd_noalloc: more (sequence, head) pairs than its scratch holds */
-    KDA_ERR_STATE_OVERLAP = 11,    /* kda_decode: distinct state_in and state_out buffers overlap */
+    KDA_ERR_STATE_OVERLAP = 11,    /* distinct state buffers in and out overlap            */
     KDA_ERR_BAD_CU_SEQLENS = 12,   /* (kda_device_error) cu_seqlens was not 0, ..., seq_len non-decreasing */
     KDA_ERR_INTERNAL = 13,         /* (kda_device_error) a kernel ran where its scratch has no slot for it */
-    KDA_ERR_BAD_OPTION = 14,       /* kda_fwd_ex: unknown gate kind or flag bit */
-    KDA_ERR_WORKSPACE = 15         /* kda_fwd_segmented: workspace smaller than it needs */
+    KDA_ERR_BAD_OPTION = 14,       /* unknown gate kind, norm kind or flag bit, bad eps    */
+    KDA_ERR_WORKSPACE = 15,        /* the workspace is smaller than the call needs         */
+    KDA_ERR_OVERLAP = 16,          /* kda_conv_*, kda_qk_*, kda_scan_*: an output overlaps an input or another output */
+    KDA_ERR_DTYPE = 17             /* kda_conv_*, kda_qk_*: a dtype code the call does not take */
 } kda_status;
 
 typedef enum { KDA_DTYPE_NONE = 0, KDA_DTYPE_BF16 = 1, KDA_DTYPE_FP32 = 2 } kda_dtype;
@@ -300,6 +302,184 @@ kda_status kda_decode(const void *q, const void *k, const void *v, const float *
                       const float *beta, float scale, int32_t batch, int32_t num_heads,
                       int32_t head_dim_k, int32_t head_dim_v, const void *state_in,
                       void *state_out, kda_dtype state_dtype, void *out, kda_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Operators around the recurrence. A layer of this kind convolves q, k and v over a few tokens
+ * before it mixes them, norms (and where its model asks for it rotates) the heads of q and k, and
+ * a hybrid model has layers with the simpler sibling of the recurrence, the selective state space scan.
+ *
+ * Rules common to kda_conv_*, kda_qk_* and kda_scan_*, besides those at the top of this file:
+ *  - Token rows may be strided: row r (token t of batch row b is row b * seq_len + t) starts at
+ *    r * stride elements, so a slice of one wider tensor's columns is taken as it is. Strides are
+ *    in elements, at least the row's width and a multiple of 16 bytes; channels and heads within a
+ *    row are contiguous. All tensors of 16-bit elements, states and fp32 x, out, dx and dout are 16-byte
+ *    aligned, other fp32 and int32 tensors 4-byte (kda_conv_*: weight 16-byte), workspaces 256-byte.
+ *  - Sequences are as in kda_fwd (cu_seqlens NULL: `batch` rows of seq_len tokens; else batch == 1 and
+ *    num_seqs + 1 device offsets), except that a packed batch may end before seq_len:
+ *    cu_seqlens[num_seqs] <= seq_len, and rows behind the last sequence are neither used nor written
+ *    (outputs keep what they held there). A malformed table raises KDA_ERR_BAD_CU_SEQLENS in the device
+ *    error word; nothing is accessed out of bounds, and results are then unspecified.
+ *  - Outputs may not overlap inputs or one another (KDA_ERR_OVERLAP), but for the buffers that a call names
+ *    as usable in place. Nothing is allocated; a workspace's contents on entry do not matter, and calls that
+ *    may run at the same time need one each. All results repeat bit for bit.
+ */
+
+/*
+ * kda_conv_fwd -- short causal depthwise convolution over a batch of sequences, with SiLU.
+ *
+ * With e the rows of a sequence behind the taps - 1 rows of its initial state:
+ *     pre_t = bias + sum_{k < taps} weight[:, k] e_(t - taps + 1 + k),    out_t = pre_t sigmoid(pre_t),
+ * or out_t = pre_t without KDA_FLAG_CONV_SILU.
+ *
+ *   x, out         : dtype [batch, seq_len, channels] (rows strided)
+ *   weight, bias   : fp32 [channels, taps], fp32 [channels] or NULL
+ *   initial_state  : dtype [num_seqs_eff, taps - 1, channels], oldest row first, or NULL (zeros)
+ *   final_state    : the same shape, written, or NULL: the last taps - 1 rows of e, which the next call
+ *                    or kda_conv_decode takes. Not usable in place of initial_state.
+ * dtype is KDA_DTYPE_BF16 or KDA_DTYPE_FP32; channels a multiple of 8, taps 2 to 4. Sums are fp32.
+ */
+#define KDA_FLAG_CONV_SILU 1u
+kda_status kda_conv_fwd(const void *x, kda_dtype dtype, int64_t x_stride, const float *weight, const float *bias,
+                        uint32_t flags, const int32_t *cu_seqlens, int32_t num_seqs, int32_t batch, int64_t seq_len,
+                        int32_t channels, int32_t taps, const void *initial_state, void *final_state, void *out,
+                        int64_t out_stride, kda_stream_t stream);
+
+/*
+ * kda_conv_bwd -- gradients of sum(dout . out) + sum(dfinal_state . final_state) of kda_conv_fwd.
+ *
+ * Inputs are kda_conv_fwd's, plus dout [batch, seq_len, channels] (rows strided; fp32, or bf16 where x is
+ * bf16) and dfinal_state (dtype, shape of final_state) or NULL. Written: dx (dtype, rows strided), dweight
+ * fp32 [channels, taps], dbias fp32 [channels] and dinitial_state (dtype), each of the last three or NULL.
+ * workspace: kda_conv_bwd_workspace(batch * seq_len, channels, taps) bytes (0 for sizes it does not take).
+ */
+size_t kda_conv_bwd_workspace(int64_t total_tokens, int32_t channels, int32_t taps);
+kda_status kda_conv_bwd(const void *x, kda_dtype dtype, int64_t x_stride, const float *weight, const float *bias,
+                        uint32_t flags, const int32_t *cu_seqlens, int32_t num_seqs, int32_t batch, int64_t seq_len,
+                        int32_t channels, int32_t taps, const void *initial_state, const void *dout,
+                        kda_dtype dout_dtype, int64_t dout_stride, const void *dfinal_state, void *dx,
+                        int64_t dx_stride, float *dweight, float *dbias, void *dinitial_state, void *workspace,
+                        size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_conv_decode -- kda_conv_fwd for one new token of each of `batch` requests.
+ *
+ *   x, out              : dtype [batch, channels] (rows strided)
+ *   state_in, state_out : dtype [batch, taps - 1, channels]; state_in NULL means zeros, state_out NULL
+ *                         that the new state is not written; they may be the same pointer (in place).
+ */
+kda_status kda_conv_decode(const void *x, kda_dtype dtype, int64_t x_stride, const float *weight, const float *bias,
+                           uint32_t flags, int32_t batch, int32_t channels, int32_t taps, const void *state_in,
+                           void *state_out, void *out, int64_t out_stride, kda_stream_t stream);
+
+/*
+ * kda_qk_fwd -- the norm of each head of q and k and its position rotation, in one pass.
+ *
+ * For every token and head, with x its head_dim channels:
+ *     z = x r w,   r = (sum x^2 + eps)^(-1/2)   KDA_NORM_L2 (KDA's own norm, as KDA_FLAG_L2NORM_QK takes it),
+ *                  r = (mean x^2 + eps)^(-1/2)  KDA_NORM_RMS,     r = 1   KDA_NORM_NONE,
+ *     pairs (z_a, z_b) of the first rot_dim channels -> factor (z_a cos - z_b sin, z_b cos + z_a sin),
+ * pair i being channels (2 i, 2 i + 1) if `interleaved`, else (i, i + rot_dim / 2), and its angle
+ * positions[row] * inv_freq[i], formed and reduced in 64 bits. Any scaling for long contexts is in the caller's
+ * inv_freq and factor. A zero vector with eps == 0 stays zero.
+ *
+ *   q, q_out : bf16 [rows, q_heads, head_dim] (rows strided); k, k_out: [rows, k_heads, head_dim] (k_heads may
+ *              be 0). q_out may be q, and k_out k, with the same stride (in place).
+ *   q_weight, k_weight : fp32 [head_dim] or NULL (ones)
+ *   positions : int32 [rows], inv_freq: fp32 [rot_dim / 2] (both unused, may be NULL, when rot_dim is 0)
+ * head_dim is 64, 128 or 256; rot_dim a multiple of 16, at most head_dim. eps >= 0.
+ */
+#define KDA_NORM_NONE 0
+#define KDA_NORM_L2 1
+#define KDA_NORM_RMS 2
+kda_status kda_qk_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride, int64_t rows, int32_t q_heads,
+                      int32_t k_heads, int32_t head_dim, int32_t norm, float eps, const float *q_weight,
+                      const float *k_weight, const int32_t *positions, const float *inv_freq, int32_t rot_dim,
+                      int32_t interleaved, float factor, void *q_out, int64_t q_out_stride, void *k_out,
+                      int64_t k_out_stride, kda_stream_t stream);
+
+/*
+ * kda_qk_bwd -- gradients of sum(dq_out . q_out) + sum(dk_out . k_out) of kda_qk_fwd.
+ *
+ * Inputs are kda_qk_fwd's (q, k as they were before it) plus dq_out, dk_out (rows strided, both of
+ * dout_dtype: bf16, or fp32 as kda_bwd gives them). Written: dq, dk bf16 (rows strided), dq_weight,
+ * dk_weight fp32 [head_dim] or NULL. workspace: kda_qk_bwd_workspace(...) bytes, unless both weights'
+ * gradients are NULL.
+ */
+size_t kda_qk_bwd_workspace(int64_t rows, int32_t q_heads, int32_t k_heads, int32_t head_dim);
+kda_status kda_qk_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride, int64_t rows, int32_t q_heads,
+                      int32_t k_heads, int32_t head_dim, int32_t norm, float eps, const float *q_weight,
+                      const float *k_weight, const int32_t *positions, const float *inv_freq, int32_t rot_dim,
+                      int32_t interleaved, float factor, const void *dq_out, int64_t dq_out_stride,
+                      const void *dk_out, int64_t dk_out_stride, kda_dtype dout_dtype, void *dq, int64_t dq_stride,
+                      void *dk, int64_t dk_stride, float *dq_weight, float *dk_weight, void *workspace,
+                      size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_scan_fwd -- selective state space scan over a batch of sequences.
+ *
+ * Per sequence and head, with a state S of state_dim x head_dim and one decay per token:
+ *     d_t = dt_t + dt_bias,  or softplus(dt_t + dt_bias) with KDA_FLAG_SCAN_SOFTPLUS
+ *     S_t = exp(d_t A) S_(t-1) + d_t B_t x_t^T,       out_t = S_t^T C_t + D x_t.
+ *
+ *   x, out : bf16 [batch, seq_len, num_heads, head_dim] (rows strided)
+ *   dt     : fp32 [batch, seq_len, num_heads]
+ *   A      : fp32 [num_heads], negative (d_t A is the log decay);  D, dt_bias: fp32 [num_heads] or NULL (0)
+ *   B, C   : bf16 [batch, seq_len, num_groups, state_dim] (rows strided); head h takes group
+ *            h / (num_heads / num_groups)
+ *   initial_state, final_state : [num_seqs_eff, num_heads, state_dim, head_dim], head channel fastest, bf16 or
+ *            fp32 (the same when both are given) or NULL, as in kda_fwd. final_state may be
+ *            initial_state (in place).
+ * head_dim and state_dim are 64 or 128; num_heads a multiple of num_groups. States are carried in fp32. The
+ * tokens are taken 64 at a time: a NaN or infinity in x, B or C can reach outputs up to 63 tokens before
+ * its own, of the same sequence and head.
+ *
+ * Long sequences of few heads are cut into pieces that run at once (as in kda_fwd_segmented, but a
+ * scalar decay needs no second run for a transition matrix); their states go to `workspace`,
+ * kda_scan_fwd_workspace(...) bytes, which is 0 where nothing is cut.
+ */
+#define KDA_FLAG_SCAN_SOFTPLUS 1u
+size_t kda_scan_fwd_workspace(int64_t total_tokens, int32_t num_seqs, int32_t num_heads, int32_t head_dim,
+                              int32_t state_dim);
+kda_status kda_scan_fwd(const void *x, int64_t x_stride, const float *dt, const float *A, const void *B,
+                        int64_t b_stride, const void *C, int64_t c_stride, const float *D, const float *dt_bias,
+                        uint32_t flags, const int32_t *cu_seqlens, int32_t num_seqs, int32_t batch, int64_t seq_len,
+                        int32_t num_heads, int32_t num_groups, int32_t head_dim, int32_t state_dim,
+                        const void *initial_state, kda_dtype initial_dtype, void *final_state, kda_dtype final_dtype,
+                        void *out, int64_t out_stride, void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_scan_bwd -- gradients of sum(dout . out) + sum(dfinal_state . final_state) of kda_scan_fwd.
+ *
+ * Inputs are kda_scan_fwd's, plus dout bf16 [batch, seq_len, num_heads, head_dim] (rows strided) and
+ * dfinal_state fp32 [num_seqs_eff, num_heads, state_dim, head_dim] or NULL. Written: dx bf16, dB, dC bf16
+ * (summed over a group's heads; all three rows strided), ddt fp32 [batch, seq_len, num_heads], dA fp32
+ * [num_heads], and, each or NULL, dD, ddt_bias fp32 [num_heads], dinitial_state fp32 (shape of the states).
+ * workspace: kda_scan_bwd_workspace(...) bytes (two fp32 states per 64 tokens and head are its bulk).
+ */
+size_t kda_scan_bwd_workspace(int64_t total_tokens, int32_t num_seqs, int32_t num_heads, int32_t num_groups,
+                              int32_t head_dim, int32_t state_dim);
+kda_status kda_scan_bwd(const void *x, int64_t x_stride, const float *dt, const float *A, const void *B,
+                        int64_t b_stride, const void *C, int64_t c_stride, const float *D, const float *dt_bias,
+                        uint32_t flags, const int32_t *cu_seqlens, int32_t num_seqs, int32_t batch, int64_t seq_len,
+                        int32_t num_heads, int32_t num_groups, int32_t head_dim, int32_t state_dim,
+                        const void *initial_state, kda_dtype initial_dtype, const void *dout, int64_t dout_stride,
+                        const float *dfinal_state, void *dx, int64_t dx_stride, float *ddt, float *dA, void *dB,
+                        int64_t db_stride, void *dC, int64_t dc_stride, float *dD, float *ddt_bias,
+                        float *dinitial_state, void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_scan_decode -- kda_scan_fwd for one new token of each of `batch` requests.
+ *
+ *   x [batch, num_heads, head_dim], B, C [batch, num_groups, state_dim] bf16 (rows strided), dt fp32
+ *   [batch, num_heads], out bf16 [batch, num_heads, head_dim] contiguous; state_in, state_out [batch,
+ *   num_heads, state_dim, head_dim] of state_dtype, with kda_decode's rules (NULL, in place).
+ */
+kda_status kda_scan_decode(const void *x, int64_t x_stride, const float *dt, const float *A, const void *B,
+                           int64_t b_stride, const void *C, int64_t c_stride, const float *D, const float *dt_bias,
+                           uint32_t flags, int32_t batch, int32_t num_heads, int32_t num_groups, int32_t head_dim,
+                           int32_t state_dim, const void *state_in, void *state_out, kda_dtype state_dtype, void *out,
+                           kda_stream_t stream);
 
 /*
  * kda_device_error -- synchronise the current device, then read and clear the

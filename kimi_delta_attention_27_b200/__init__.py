@@ -1,4 +1,5 @@
-"""B200 (sm_100a) Kimi Delta Attention library (prefill forward and decode step): Python binding.
+"""B200 (sm_100a) Kimi Delta Attention library (prefill, backward, decode, and the operators around the
+recurrence: short convolution, q/k norm and rotation, selective scan): Python binding.
 
 The work happens in ``libkda.so`` (hand-written CUDA kernels behind the C ABI
 declared in ``include/kda.h``). This module only marshals torch tensors into
@@ -16,13 +17,19 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libkda.so")
 
 # entry points declared in include/kda.h
-EXPORTS = ("kda_bwd", "kda_bwd_workspace", "kda_decode", "kda_device_error", "kda_fwd", "kda_fwd_ex",
-           "kda_fwd_noalloc", "kda_fwd_segmented", "kda_fwd_segmented_workspace", "kda_status_string",
-           "kda_version")
+EXPORTS = ("kda_bwd", "kda_bwd_workspace", "kda_conv_bwd", "kda_conv_bwd_workspace", "kda_conv_decode",
+           "kda_conv_fwd", "kda_decode", "kda_device_error", "kda_fwd", "kda_fwd_ex", "kda_fwd_noalloc",
+           "kda_fwd_segmented", "kda_fwd_segmented_workspace", "kda_qk_bwd", "kda_qk_bwd_workspace", "kda_qk_fwd",
+           "kda_scan_bwd", "kda_scan_bwd_workspace", "kda_scan_decode", "kda_scan_fwd", "kda_scan_fwd_workspace",
+           "kda_status_string", "kda_version")
 
 # kda_fwd_ex gate kinds and flags (include/kda.h)
 KDA_GATE_FP32, KDA_GATE_BF16, KDA_GATE_SCALAR_FP32 = 0, 1, 2
 KDA_FLAG_L2NORM_QK, KDA_FLAG_GATE_LOGSIGMOID = 1, 2
+
+# kda_conv_*, kda_scan_* flags and kda_qk_* norm kinds (include/kda.h)
+KDA_FLAG_CONV_SILU, KDA_FLAG_SCAN_SOFTPLUS = 1, 1
+NORM_KINDS = {"none": 0, "l2": 1, "rms": 2}
 
 # (sequence, head) pairs per kda_fwd_noalloc call (KDA_NOALLOC_MAX_UNITS in include/kda.h)
 NOALLOC_MAX_UNITS = 32
@@ -73,6 +80,32 @@ def load_library(path: str | None = None):
         lib.kda_bwd_workspace.argtypes = [i64, i32, i32]
         lib.kda_decode.restype = ctypes.c_int
         lib.kda_decode.argtypes = [P, P, P, P, P, ctypes.c_float, i32, i32, i32, i32, P, P, ctypes.c_int, P, P]
+        f32, u32, sz, dt = ctypes.c_float, ctypes.c_uint32, ctypes.c_size_t, ctypes.c_int
+        conv = [P, dt, i64, P, P, u32]
+        seqs = [P, i32, i32, i64]
+        qk = [P, i64, P, i64, i64, i32, i32, i32, i32, f32, P, P, P, P, i32, i32, f32]
+        scan = [P, i64, P, P, P, i64, P, i64, P, P, u32]
+        for name, args in {
+            "kda_conv_fwd": conv + seqs + [i32, i32, P, P, P, i64, P],
+            "kda_conv_bwd": conv + seqs + [i32, i32, P, P, dt, i64, P, P, i64, P, P, P, P, sz, P],
+            "kda_conv_decode": conv + [i32, i32, i32, P, P, P, i64, P],
+            "kda_qk_fwd": qk + [P, i64, P, i64, P],
+            "kda_qk_bwd": qk + [P, i64, P, i64, dt, P, i64, P, i64, P, P, P, sz, P],
+            "kda_scan_fwd": scan + seqs + [i32, i32, i32, i32, P, dt, P, dt, P, i64, P, sz, P],
+            "kda_scan_bwd": scan + seqs + [i32, i32, i32, i32, P, dt, P, i64, P, P, i64, P, P, P, i64, P, i64, P, P,
+                                           P, P, sz, P],
+            "kda_scan_decode": scan + [i32, i32, i32, i32, i32, P, P, dt, P, P],
+        }.items():
+            getattr(lib, name).restype = ctypes.c_int
+            getattr(lib, name).argtypes = args
+        for name, args in {
+            "kda_conv_bwd_workspace": [i64, i32, i32],
+            "kda_qk_bwd_workspace": [i64, i32, i32, i32],
+            "kda_scan_fwd_workspace": [i64, i32, i32, i32, i32],
+            "kda_scan_bwd_workspace": [i64, i32, i32, i32, i32, i32],
+        }.items():
+            getattr(lib, name).restype = sz
+            getattr(lib, name).argtypes = args
         lib.kda_status_string.restype = ctypes.c_char_p
         lib.kda_status_string.argtypes = [ctypes.c_int]
         lib.kda_version.restype = ctypes.c_int32
@@ -402,4 +435,429 @@ def kda_decode(q, k, v, g, beta, state_in=None, state_out=None, scale: float | N
                             _ptr(out), ctypes.c_void_p(int(stream)))
     if st != 0:
         raise KdaError(st, lib.kda_status_string(st).decode())
+    return out, state_out
+
+
+# ---------------------------------------------------------------- operators around the recurrence
+
+def _check_rows(name, t, dtypes, shape, lead):
+    """Validate a tensor whose token rows may be strided: the first ``lead`` dims are the rows, the others
+    contiguous within one. Returns the row stride in elements."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    width = 1
+    for n, st in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
+        if n > 1 and t.numel() and st != width:
+            raise ValueError(f"{name} must be contiguous within a row")
+        width *= n
+    stride, below = width, 1
+    if t.numel():
+        for n, st in zip(reversed(t.shape[:lead]), reversed(t.stride()[:lead])):
+            if n > 1 and below == 1:
+                stride = st
+            elif n > 1 and st != stride * below:
+                raise ValueError(f"{name}'s rows must be evenly spaced")
+            below *= n
+    if stride < width:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return stride
+
+
+class _Stream:
+    """``with _Stream(dev, stream) as handle``: the device is current, and so is the stream, so that what is
+    allocated inside belongs to the stream the kernels run on."""
+
+    def __init__(self, dev, stream):
+        import torch
+        self.dev = torch.cuda.device(dev)
+        here = torch.cuda.current_stream(dev)
+        self.handle = here.cuda_stream if stream is None else int(stream)
+        self.stream = None
+        if self.handle != here.cuda_stream:
+            self.stream = torch.cuda.stream(torch.cuda.ExternalStream(self.handle, device=dev))
+
+    def __enter__(self):
+        self.dev.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return ctypes.c_void_p(self.handle)
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        return self.dev.__exit__(*exc)
+
+
+def _raise(lib, st):
+    if st != 0:
+        raise KdaError(st, lib.kda_status_string(st).decode())
+
+
+def _scratch(need, given, dev):
+    import torch
+    if given is not None:
+        _check("workspace", given, torch.uint8, 1)
+        return given
+    return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+
+
+def _size(t):
+    return 0 if t is None else int(t.numel())
+
+
+def _num_seqs(cu_seqlens, B):
+    import torch
+    if cu_seqlens is None:
+        return B
+    _check("cu_seqlens", cu_seqlens, torch.int32, 1)
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must have at least one entry")
+    return cu_seqlens.numel() - 1
+
+
+def _conv_args(x, weight, bias, lead):
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dim() != lead + 1:
+        raise ValueError(f"x must have {lead + 1} dims")
+    C = x.shape[-1]
+    xs = _check_rows("x", x, (torch.bfloat16, torch.float32), x.shape, lead)
+    _check("weight", weight, torch.float32, 2)
+    W = weight.shape[1]
+    _check("weight", weight, torch.float32, shape=(C, W))
+    if bias is not None:
+        _check("bias", bias, torch.float32, shape=(C,))
+    return C, W, xs
+
+
+def kda_conv_fwd(x, weight, bias=None, silu: bool = True, cu_seqlens=None, initial_state=None, final_state=None,
+                 out=None, want_final_state: bool = False, stream=None):
+    """Short causal depthwise convolution with SiLU over a batch of sequences (see include/kda.h, kda_conv_fwd).
+
+    x: bf16 or fp32 [B, T, C] (token rows may be strided); weight: fp32 [C, W], W 2 to 4; bias: fp32 [C] or
+    None; cu_seqlens: int32 [N + 1] on the device (then B == 1) or None; initial_state: [N, W - 1, C] of x's
+    type or None (zeros). ``final_state`` may be passed preallocated, or is allocated when
+    ``want_final_state``. Returns (out, final_state or None)."""
+    import torch
+    C, W, xs = _conv_args(x, weight, bias, 2)
+    B, T = x.shape[:2]
+    N = _num_seqs(cu_seqlens, B)
+    for name, t in (("initial_state", initial_state), ("final_state", final_state)):
+        if t is not None:
+            _check(name, t, x.dtype, shape=(N, W - 1, C))
+    if out is not None:
+        _check_rows("out", out, (x.dtype,), x.shape, 2)
+    dev = _check_devices(x=x, weight=weight, bias=bias, cu_seqlens=cu_seqlens, initial_state=initial_state,
+                         final_state=final_state, out=out)
+    lib = load_library()
+    with _Stream(dev, stream) as handle:
+        if out is None:
+            out = torch.empty((B, T, C), dtype=x.dtype, device=dev)
+        if final_state is None and want_final_state:
+            final_state = torch.empty((N, W - 1, C), dtype=x.dtype, device=dev)
+        _raise(lib, lib.kda_conv_fwd(_ptr(x), _dtype_code(x), xs, _ptr(weight), _ptr(bias),
+                                     KDA_FLAG_CONV_SILU if silu else 0, _ptr(cu_seqlens), N, B, T, C, W,
+                                     _ptr(initial_state), _ptr(final_state), _ptr(out),
+                                     _check_rows("out", out, (x.dtype,), x.shape, 2), handle))
+    return out, final_state
+
+
+def kda_conv_bwd(x, weight, dout, bias=None, silu: bool = True, cu_seqlens=None, initial_state=None,
+                 dfinal_state=None, want_dinitial_state: bool = False, dx=None, workspace=None, stream=None):
+    """Gradients of sum(dout * out) + sum(dfinal_state * final_state) of ``kda_conv_fwd`` (see include/kda.h,
+    kda_conv_bwd). Inputs as for it, plus dout [B, T, C] (x's type, or fp32) and dfinal_state [N, W - 1, C] or
+    None. Returns a dict: dx [B, T, C] (x's type), dweight fp32 [C, W], dbias fp32 [C] (None without a bias),
+    dinitial_state [N, W - 1, C] (None unless asked). ``dx`` may be passed preallocated (strided)."""
+    import torch
+    C, W, xs = _conv_args(x, weight, bias, 2)
+    B, T = x.shape[:2]
+    N = _num_seqs(cu_seqlens, B)
+    ds = _check_rows("dout", dout, (x.dtype, torch.float32), x.shape, 2)
+    for name, t in (("initial_state", initial_state), ("dfinal_state", dfinal_state)):
+        if t is not None:
+            _check(name, t, x.dtype, shape=(N, W - 1, C))
+    if dx is not None:
+        _check_rows("dx", dx, (x.dtype,), x.shape, 2)
+    dev = _check_devices(x=x, weight=weight, bias=bias, cu_seqlens=cu_seqlens, initial_state=initial_state,
+                         dout=dout, dfinal_state=dfinal_state, dx=dx, workspace=workspace)
+    lib = load_library()
+    with _Stream(dev, stream) as handle:
+        if dx is None:
+            dx = torch.empty((B, T, C), dtype=x.dtype, device=dev)
+        dweight = torch.empty((C, W), dtype=torch.float32, device=dev)
+        dbias = torch.empty(C, dtype=torch.float32, device=dev) if bias is not None else None
+        dinit = torch.empty((N, W - 1, C), dtype=x.dtype, device=dev) if want_dinitial_state else None
+        ws = _scratch(int(lib.kda_conv_bwd_workspace(B * T, C, W)), workspace, dev)
+        _raise(lib, lib.kda_conv_bwd(_ptr(x), _dtype_code(x), xs, _ptr(weight), _ptr(bias),
+                                     KDA_FLAG_CONV_SILU if silu else 0, _ptr(cu_seqlens), N, B, T, C, W,
+                                     _ptr(initial_state), _ptr(dout), _dtype_code(dout), ds, _ptr(dfinal_state),
+                                     _ptr(dx), _check_rows("dx", dx, (x.dtype,), x.shape, 2), _ptr(dweight),
+                                     _ptr(dbias), _ptr(dinit), _ptr(ws), _size(ws), handle))
+    return dict(dx=dx, dweight=dweight, dbias=dbias, dinitial_state=dinit)
+
+
+def kda_conv_decode(x, weight, state_in=None, state_out=None, bias=None, silu: bool = True, out=None, stream=None):
+    """``kda_conv_fwd`` for one new token per request (see include/kda.h, kda_conv_decode).
+
+    x: [B, C] (rows may be strided); states [B, W - 1, C] of x's type: ``state_in`` None means zeros,
+    ``state_out`` may be ``state_in`` itself (in place) or None (not written). Returns (out, state_out)."""
+    import torch
+    C, W, xs = _conv_args(x, weight, bias, 1)
+    B = x.shape[0]
+    for name, t in (("state_in", state_in), ("state_out", state_out)):
+        if t is not None:
+            _check(name, t, x.dtype, shape=(B, W - 1, C))
+    if out is not None:
+        _check_rows("out", out, (x.dtype,), x.shape, 1)
+    dev = _check_devices(x=x, weight=weight, bias=bias, state_in=state_in, state_out=state_out, out=out)
+    lib = load_library()
+    with _Stream(dev, stream) as handle:
+        if out is None:
+            out = torch.empty((B, C), dtype=x.dtype, device=dev)
+        _raise(lib, lib.kda_conv_decode(_ptr(x), _dtype_code(x), xs, _ptr(weight), _ptr(bias),
+                                        KDA_FLAG_CONV_SILU if silu else 0, B, C, W, _ptr(state_in), _ptr(state_out),
+                                        _ptr(out), _check_rows("out", out, (x.dtype,), x.shape, 1), handle))
+    return out, state_out
+
+
+def _qk_args(q, k, norm, q_weight, k_weight, positions, inv_freq):
+    import torch
+    if norm not in NORM_KINDS:
+        raise ValueError(f"norm must be one of {', '.join(NORM_KINDS)}, got {norm!r}")
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or (k is not None and (
+            not isinstance(k, torch.Tensor) or k.dim() != 4)):
+        raise ValueError("q and k must have 4 dims")
+    B, T, Hq, D = q.shape
+    qs = _check_rows("q", q, (torch.bfloat16,), q.shape, 2)
+    Hk = 0 if k is None else k.shape[2]
+    ks = 0 if k is None else _check_rows("k", k, (torch.bfloat16,), (B, T, Hk, D), 2)
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None:
+            _check(name, t, torch.float32, shape=(D,))
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq come together")
+    rot = 0
+    if positions is not None:
+        _check("positions", positions, torch.int32, shape=(B, T))
+        _check("inv_freq", inv_freq, torch.float32, 1)
+        rot = 2 * inv_freq.numel()
+    return B, T, Hq, Hk, D, qs, ks, rot
+
+
+def kda_qk_fwd(q, k=None, norm: str = "l2", q_weight=None, k_weight=None, eps: float = 1e-6, positions=None,
+               inv_freq=None, interleaved: bool = False, factor: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Norm of each head of q and k and its position rotation in one pass (see include/kda.h, kda_qk_fwd).
+
+    q: bf16 [B, T, Hq, D], k: bf16 [B, T, Hk, D] or None (token rows may be strided), D 64, 128 or 256; norm:
+    "l2", "rms" or "none"; weights: fp32 [D] or None; positions: int32 [B, T] and inv_freq: fp32
+    [rot_dim / 2] rotate the first rot_dim channels (both None: no rotation), in pairs (2i, 2i + 1) if
+    ``interleaved``, else (i, i + rot_dim / 2); ``factor`` multiplies cos and sin. ``q_out``/``k_out`` may be q and
+    k themselves. Returns (q_out, k_out)."""
+    import torch
+    B, T, Hq, Hk, D, qs, ks, rot = _qk_args(q, k, norm, q_weight, k_weight, positions, inv_freq)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    bf = (torch.bfloat16,)
+    if q_out is not None:
+        _check_rows("q_out", q_out, bf, q.shape, 2)
+    if k_out is not None:
+        _check_rows("k_out", k_out, bf, k.shape, 2)
+    dev = _check_devices(q=q, k=k, q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq,
+                         q_out=q_out, k_out=k_out)
+    lib = load_library()
+    with _Stream(dev, stream) as handle:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        if k_out is None and k is not None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        _raise(lib, lib.kda_qk_fwd(_ptr(q), qs, _ptr(k), ks, B * T, Hq, Hk, D, NORM_KINDS[norm], float(eps),
+                                   _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), rot,
+                                   int(bool(interleaved)), float(factor),
+                                   _ptr(q_out), _check_rows("q_out", q_out, bf, q.shape, 2),
+                                   _ptr(k_out), _check_rows("k_out", k_out, bf, k.shape, 2) if Hk else 0, handle))
+    return q_out, k_out
+
+
+def kda_qk_bwd(q, k, dq_out, dk_out, norm: str = "l2", q_weight=None, k_weight=None, eps: float = 1e-6,
+               positions=None, inv_freq=None, interleaved: bool = False, factor: float = 1.0, workspace=None,
+               stream=None):
+    """Gradients of sum(dq_out * q_out) + sum(dk_out * k_out) of ``kda_qk_fwd`` (see include/kda.h, kda_qk_bwd).
+
+    q, k and the options as it took them (k and dk_out None together); dq_out, dk_out both bf16 or both fp32 (as
+    ``kda_bwd`` gives them). Returns a dict: dq, dk bf16, dq_weight, dk_weight fp32 [D] (None without that
+    weight)."""
+    import torch
+    B, T, Hq, Hk, D, qs, ks, rot = _qk_args(q, k, norm, q_weight, k_weight, positions, inv_freq)
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out come together")
+    if k is None and k_weight is not None:
+        raise ValueError("k_weight without k")
+    dqs = _check_rows("dq_out", dq_out, (torch.bfloat16, torch.float32), q.shape, 2)
+    dks = 0 if k is None else _check_rows("dk_out", dk_out, (dq_out.dtype,), k.shape, 2)
+    dev = _check_devices(q=q, k=k, q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq,
+                         dq_out=dq_out, dk_out=dk_out, workspace=workspace)
+    lib = load_library()
+    with _Stream(dev, stream) as handle:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        dk = torch.empty(k.shape, dtype=k.dtype, device=dev) if k is not None else None
+        dqw = torch.empty(D, dtype=torch.float32, device=dev) if q_weight is not None else None
+        dkw = torch.empty(D, dtype=torch.float32, device=dev) if k_weight is not None else None
+        need = 0
+        if dqw is not None or dkw is not None:
+            need = int(lib.kda_qk_bwd_workspace(B * T, Hq, Hk, D))
+        ws = _scratch(need, workspace, dev)
+        _raise(lib, lib.kda_qk_bwd(_ptr(q), qs, _ptr(k), ks, B * T, Hq, Hk, D, NORM_KINDS[norm], float(eps),
+                                   _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), rot,
+                                   int(bool(interleaved)), float(factor), _ptr(dq_out), dqs, _ptr(dk_out), dks,
+                                   _dtype_code(dq_out), _ptr(dq), Hq * D, _ptr(dk), Hk * D, _ptr(dqw), _ptr(dkw),
+                                   _ptr(ws), _size(ws), handle))
+    return dict(dq=dq, dk=dk, dq_weight=dqw, dk_weight=dkw)
+
+
+def _scan_args(x, dt, A, B, C, D, dt_bias, lead):
+    import torch
+    bf = (torch.bfloat16,)
+    for name, t in (("x", x), ("B", B)):
+        if not isinstance(t, torch.Tensor) or t.dim() != lead + 2:
+            raise ValueError(f"{name} must have {lead + 2} dims")
+    H, P = x.shape[lead:]
+    G, N = B.shape[lead:]
+    rows = tuple(x.shape[:lead])
+    strides = (_check_rows("x", x, bf, x.shape, lead), _check_rows("B", B, bf, rows + (G, N), lead),
+               _check_rows("C", C, bf, rows + (G, N), lead))
+    _check("dt", dt, torch.float32, shape=rows + (H,))
+    _check("A", A, torch.float32, shape=(H,))
+    for name, t in (("D", D), ("dt_bias", dt_bias)):
+        if t is not None:
+            _check(name, t, torch.float32, shape=(H,))
+    return H, P, G, N, strides
+
+
+def kda_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus: bool = False, cu_seqlens=None,
+                 initial_state=None, final_state=None, out=None, final_state_dtype=None, workspace=None, stream=None):
+    """Selective state space scan over a batch of sequences (see include/kda.h, kda_scan_fwd).
+
+    x: bf16 [B, T, H, P]; dt: fp32 [B, T, H]; A: fp32 [H] (negative); B, C: bf16 [B, T, G, N], H a multiple of
+    G (token rows of x, B, C may be strided: slices of one projection); D, dt_bias: fp32 [H] or None; the step is
+    dt + dt_bias, or its softplus. States [N_seqs, H, N, P] bf16 or fp32; ``final_state`` may be
+    ``initial_state`` (in place), or is allocated when ``final_state_dtype`` is given. P and N are 64 or 128.
+    ``workspace`` (uint8, at least ``scan_workspace_bytes(...)``) is allocated when needed and not given.
+    Returns (out, final_state or None)."""
+    import torch
+    H, P, G, N, (xs, bs, cs) = _scan_args(x, dt, A, B, C, D, dt_bias, 2)
+    Bn, T = x.shape[:2]
+    n = _num_seqs(cu_seqlens, Bn)
+    for name, t in (("initial_state", initial_state), ("final_state", final_state)):
+        if t is not None:
+            _check(name, t, None, shape=(n, H, N, P))
+    bf = (torch.bfloat16,)
+    if out is not None:
+        _check_rows("out", out, bf, x.shape, 2)
+    dev = _check_devices(x=x, dt=dt, A=A, B=B, C=C, D=D, dt_bias=dt_bias, cu_seqlens=cu_seqlens,
+                         initial_state=initial_state, final_state=final_state, out=out, workspace=workspace)
+    lib = load_library()
+    with _Stream(dev, stream) as handle:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        if final_state is None and final_state_dtype is not None:
+            final_state = torch.empty((n, H, N, P), dtype=final_state_dtype, device=dev)
+        ws = _scratch(int(lib.kda_scan_fwd_workspace(Bn * T, n, H, P, N)), workspace, dev)
+        ic, fc = _dtype_code(initial_state), _dtype_code(final_state)
+        _raise(lib, lib.kda_scan_fwd(_ptr(x), xs, _ptr(dt), _ptr(A), _ptr(B), bs, _ptr(C), cs, _ptr(D), _ptr(dt_bias),
+                                     KDA_FLAG_SCAN_SOFTPLUS if dt_softplus else 0, _ptr(cu_seqlens), n, Bn, T, H, G,
+                                     P, N, _ptr(initial_state), ic if ic >= 0 else 99, _ptr(final_state),
+                                     fc if fc >= 0 else 99, _ptr(out), _check_rows("out", out, bf, x.shape, 2),
+                                     _ptr(ws), _size(ws), handle))
+    return out, final_state
+
+
+def kda_scan_bwd(x, dt, A, B, C, dout, D=None, dt_bias=None, dt_softplus: bool = False, cu_seqlens=None,
+                 initial_state=None, dfinal_state=None, want_dinitial_state: bool = True, dx=None, dB=None, dC=None,
+                 workspace=None, stream=None):
+    """Gradients of sum(dout * out) + sum(dfinal_state * final_state) of ``kda_scan_fwd`` (see include/kda.h,
+    kda_scan_bwd). Inputs as for it, plus dout bf16 [B, T, H, P] and dfinal_state fp32 [N_seqs, H, N, P] or None.
+    Returns a dict: dx, dB, dC bf16 (shapes of x, B, C; each may be passed preallocated, strided), ddt, dA, dD,
+    ddt_bias fp32 (the last two None without D or dt_bias) and dh0 fp32 [N_seqs, H, N, P] (None unless asked)."""
+    import torch
+    H, P, G, N, (xs, bs, cs) = _scan_args(x, dt, A, B, C, D, dt_bias, 2)
+    Bn, T = x.shape[:2]
+    n = _num_seqs(cu_seqlens, Bn)
+    bf = (torch.bfloat16,)
+    ds = _check_rows("dout", dout, bf, x.shape, 2)
+    if initial_state is not None:
+        _check("initial_state", initial_state, None, shape=(n, H, N, P))
+    if dfinal_state is not None:
+        _check("dfinal_state", dfinal_state, torch.float32, shape=(n, H, N, P))
+    for name, t, like in (("dx", dx, x), ("dB", dB, B), ("dC", dC, C)):
+        if t is not None:
+            _check_rows(name, t, bf, like.shape, 2)
+    dev = _check_devices(x=x, dt=dt, A=A, B=B, C=C, D=D, dt_bias=dt_bias, dout=dout, cu_seqlens=cu_seqlens,
+                         initial_state=initial_state, dfinal_state=dfinal_state, dx=dx, dB=dB, dC=dC,
+                         workspace=workspace)
+    lib = load_library()
+    with _Stream(dev, stream) as handle:
+        empty = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+        f32 = torch.float32
+        dx = empty(x.shape, x.dtype) if dx is None else dx
+        dB = empty(B.shape, B.dtype) if dB is None else dB
+        dC = empty(C.shape, C.dtype) if dC is None else dC
+        out = dict(dx=dx, dB=dB, dC=dC, ddt=empty(dt.shape, f32), dA=empty((H,), f32),
+                   dD=empty((H,), f32) if D is not None else None,
+                   ddt_bias=empty((H,), f32) if dt_bias is not None else None,
+                   dh0=empty((n, H, N, P), f32) if want_dinitial_state else None)
+        ws = _scratch(int(lib.kda_scan_bwd_workspace(Bn * T, n, H, G, P, N)), workspace, dev)
+        ic = _dtype_code(initial_state)
+        _raise(lib, lib.kda_scan_bwd(_ptr(x), xs, _ptr(dt), _ptr(A), _ptr(B), bs, _ptr(C), cs, _ptr(D), _ptr(dt_bias),
+                                     KDA_FLAG_SCAN_SOFTPLUS if dt_softplus else 0, _ptr(cu_seqlens), n, Bn, T, H, G,
+                                     P, N, _ptr(initial_state), ic if ic >= 0 else 99, _ptr(dout), ds,
+                                     _ptr(dfinal_state), _ptr(dx), _check_rows("dx", dx, bf, x.shape, 2),
+                                     _ptr(out["ddt"]), _ptr(out["dA"]), _ptr(dB),
+                                     _check_rows("dB", dB, bf, B.shape, 2), _ptr(dC),
+                                     _check_rows("dC", dC, bf, C.shape, 2), _ptr(out["dD"]), _ptr(out["ddt_bias"]),
+                                     _ptr(out["dh0"]), _ptr(ws), _size(ws), handle))
+    return out
+
+
+def scan_workspace_bytes(total_tokens: int, num_seqs: int, num_heads: int, head_dim: int, state_dim: int) -> int:
+    """Bytes of workspace kda_scan_fwd needs (0 where it cuts no sequence)."""
+    return int(load_library().kda_scan_fwd_workspace(int(total_tokens), int(num_seqs), int(num_heads), int(head_dim),
+                                                     int(state_dim)))
+
+
+def kda_scan_decode(x, dt, A, B, C, state_in=None, state_out=None, D=None, dt_bias=None, dt_softplus: bool = False,
+                    out=None, state_dtype=None, stream=None):
+    """``kda_scan_fwd`` for one new token per request (see include/kda.h, kda_scan_decode).
+
+    x: bf16 [B, H, P], B, C: bf16 [B, G, N] (rows may be strided), dt: fp32 [B, H]; states [B, H, N, P] with
+    ``kda_decode``'s rules: ``state_in`` None means zeros, ``state_out`` may be ``state_in`` itself, and is
+    allocated when it is None and ``state_dtype`` is given. Returns (out, state_out or None)."""
+    import torch
+    H, P, G, N, (xs, bs, cs) = _scan_args(x, dt, A, B, C, D, dt_bias, 1)
+    n = x.shape[0]
+    for name, t in (("state_in", state_in), ("state_out", state_out)):
+        if t is not None:
+            _check(name, t, None, shape=(n, H, N, P))
+    if state_in is not None and state_out is not None and state_in.dtype != state_out.dtype:
+        raise ValueError("state_in and state_out must have the same dtype")
+    if state_in is not None and state_out is None and state_dtype not in (None, state_in.dtype):
+        raise ValueError("state_dtype must be state_in's")
+    if out is not None:
+        _check("out", out, torch.bfloat16, shape=x.shape)
+    dev = _check_devices(x=x, dt=dt, A=A, B=B, C=C, D=D, dt_bias=dt_bias, state_in=state_in, state_out=state_out,
+                         out=out)
+    lib = load_library()
+    with _Stream(dev, stream) as handle:
+        if state_out is None and state_dtype is not None:
+            state_out = torch.empty((n, H, N, P), dtype=state_dtype, device=dev)
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        code = _dtype_code(state_in if state_in is not None else state_out)
+        _raise(lib, lib.kda_scan_decode(_ptr(x), xs, _ptr(dt), _ptr(A), _ptr(B), bs, _ptr(C), cs, _ptr(D),
+                                        _ptr(dt_bias), KDA_FLAG_SCAN_SOFTPLUS if dt_softplus else 0, n, H, G, P, N,
+                                        _ptr(state_in), _ptr(state_out), code if code >= 0 else 99, _ptr(out),
+                                        handle))
     return out, state_out

@@ -4,6 +4,8 @@
 #include "../../include/kda.h"
 #include "kda_internal.h"
 #include "kda_decode.h"
+#include "kda_conv.h"
+#include "kda_scan.h"
 
 static_assert(kda::kNoAllocMaxUnits == KDA_NOALLOC_MAX_UNITS, "scratch limit of kda_fwd_noalloc");
 
@@ -93,7 +95,7 @@ const char *kda_status_string(kda_status s) {
     switch (s) {
         case KDA_OK: return "KDA_OK";
         case KDA_ERR_NULL_PTR: return "KDA_ERR_NULL_PTR: a required pointer is NULL";
-        case KDA_ERR_BAD_SHAPE: return "KDA_ERR_BAD_SHAPE: head dims must be 128 and sizes non-negative";
+        case KDA_ERR_BAD_SHAPE: return "KDA_ERR_BAD_SHAPE: a size the call does not take (kda_fwd, kda_decode: head dims must be 128)";
         case KDA_ERR_VARLEN_BATCH: return "KDA_ERR_VARLEN_BATCH: cu_seqlens requires batch == 1";
         case KDA_ERR_STATE_DTYPE: return "KDA_ERR_STATE_DTYPE: states must be bf16 or fp32 and match";
         case KDA_ERR_CUDA: return "KDA_ERR_CUDA: a CUDA call failed";
@@ -104,20 +106,24 @@ const char *kda_status_string(kda_status s) {
         case KDA_ERR_NOALLOC_LIMIT:
             return "KDA_ERR_NOALLOC_LIMIT: kda_fwd_noalloc takes at most 32 (sequence, head) pairs per call";
         case KDA_ERR_STATE_OVERLAP:
-            return "KDA_ERR_STATE_OVERLAP: kda_decode state_in and state_out overlap without being the same buffer";
+            return "KDA_ERR_STATE_OVERLAP: the states in and out overlap without being the same buffer";
         case KDA_ERR_BAD_CU_SEQLENS:
             return "KDA_ERR_BAD_CU_SEQLENS: cu_seqlens must run 0, ..., seq_len without decreasing";
         case KDA_ERR_INTERNAL:
             return "KDA_ERR_INTERNAL: a kernel ran on an SM beyond its scratch pool and stopped";
         case KDA_ERR_BAD_OPTION:
-            return "KDA_ERR_BAD_OPTION: unknown gate kind or flag";
+            return "KDA_ERR_BAD_OPTION: unknown gate kind, norm kind or flag, or a bad eps";
         case KDA_ERR_WORKSPACE:
-            return "KDA_ERR_WORKSPACE: the workspace is smaller than kda_fwd_segmented_workspace() asks";
+            return "KDA_ERR_WORKSPACE: the workspace is smaller than the entry point's _workspace() asks";
+        case KDA_ERR_OVERLAP:
+            return "KDA_ERR_OVERLAP: an output overlaps an input or another output";
+        case KDA_ERR_DTYPE:
+            return "KDA_ERR_DTYPE: a tensor's type is not one the call takes";
     }
     return "KDA_ERR_UNKNOWN";
 }
 
-int32_t kda_version(void) { return (1 << 16) | 3; }
+int32_t kda_version(void) { return (1 << 16) | 4; }
 
 kda_status kda_fwd(const void *q, const void *k, const void *v, const float *g,
                    const float *beta, float scale, const int32_t *cu_seqlens,
@@ -339,8 +345,11 @@ kda_status kda_decode(const void *q, const void *k, const void *v, const float *
 
 kda_status kda_device_error(void) {
     if (cudaDeviceSynchronize() != cudaSuccess) return KDA_ERR_CUDA;
-    unsigned int v = 0;
-    if (kda::read_and_clear_device_error(&v) != cudaSuccess) return KDA_ERR_CUDA;
+    unsigned int v = 0, conv = 0, scan = 0;
+    if (kda::read_and_clear_device_error(&v) != cudaSuccess || kda::read_and_clear_conv_error(&conv) != cudaSuccess ||
+        kda::read_and_clear_scan_error(&scan) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    v |= conv | scan;
     if (v & kda::kErrCuSeqlens) return KDA_ERR_BAD_CU_SEQLENS;
     if (v & kda::kErrTimeout) return KDA_ERR_TIMEOUT;
     if (v & kda::kErrRingIndex) return KDA_ERR_INTERNAL;

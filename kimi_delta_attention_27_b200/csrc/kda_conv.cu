@@ -1,0 +1,520 @@
+// kda_conv.cu -- short causal depthwise convolution with SiLU: prompts, gradients, single tokens. sm_100a.
+//
+// For every sequence, with e = [initial_state rows, x rows] (row -(W-1) .. -1 the state's):
+//
+//   pre_t = bias + sum_{k < W} w_k e_{t-W+1+k},   out_t = pre_t sigmoid(pre_t)  (or pre_t)
+//
+// All three kernels are bound by HBM: 2 W operations and one sigmoid per element against 4 bytes
+// (bf16, forward). A thread owns 8 channels (4 in the backward) and walks a run of tokens with the
+// last W - 1 inputs in registers, so x is read once but for the W - 1 rows before each run, which
+// the neighbouring warp has just read. The loads of the next tokens are issued together, before any
+// of them is used. Sums are fp32; each output is rounded once.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "kda_conv.h"
+
+namespace kda {
+namespace conv {
+
+__device__ unsigned int g_conv_error = 0;
+
+constexpr int V = 8;              // channels per thread, forward and decode
+constexpr int FW = 4;             // warps per CTA, forward
+constexpr int U = 4;              // tokens whose loads are issued together
+
+__device__ __forceinline__ float sigmoidf(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+template <int W, int N>
+__device__ __forceinline__ void load_taps(const ConvParams &p, int ch, float (&w)[W][N], float (&b)[N]) {
+    // weight is [C, W]: the N channels' taps are N * W consecutive floats
+    float flat[N * W];
+    const float4 *src = reinterpret_cast<const float4 *>(p.weight + static_cast<int64_t>(ch) * W);
+#pragma unroll
+    for (int i = 0; i < N * W / 4; ++i) {
+        const float4 f = src[i];
+        flat[4 * i] = f.x;
+        flat[4 * i + 1] = f.y;
+        flat[4 * i + 2] = f.z;
+        flat[4 * i + 3] = f.w;
+    }
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+#pragma unroll
+        for (int c = 0; c < N; ++c) w[k][c] = flat[c * W + k];
+#pragma unroll
+    for (int c = 0; c < N; ++c) b[c] = p.bias ? p.bias[ch + c] : 0.f;
+}
+
+// the row `back` tokens before row t of sequence i (which begins at b): of x, or of the initial state
+template <class T, int W, int N>
+__device__ __forceinline__ void load_before(const ConvParams &p, int32_t i, int64_t b, int64_t t, int back, int ch,
+                                            float (&e)[N]) {
+    Vec<T, N> raw;
+    const int64_t pos = t - back - b;
+    if (pos >= 0)
+        raw.load(p.x, (t - back) * p.x_stride + ch);
+    else if (p.init)
+        raw.load(p.init, (static_cast<int64_t>(i) * (W - 1) + (W - 1) + pos) * p.C + ch);
+    else
+        raw.zero();
+    raw.get(e);
+}
+
+// grid (token blocks + sequence blocks, channel blocks of 256). Token blocks: warp w walks `run` tokens.
+// Sequence blocks: warp w copies the final state of one sequence.
+template <class T, int W, bool kSilu>
+__global__ void __launch_bounds__(32 * FW) conv_fwd_kernel(ConvParams p, int run, int64_t token_blocks) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ch = blockIdx.y * (32 * V) + lane * V;
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seqs, &g_conv_error);
+    if (blockIdx.x >= token_blocks) {
+        const int64_t i64 = (static_cast<int64_t>(blockIdx.x) - token_blocks) * FW + warp;
+        if (i64 >= p.seqs.n || ch >= p.C) return;
+        const int32_t i = static_cast<int32_t>(i64);
+        const int64_t b = p.seqs.begin(i), e = p.seqs.end(i);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            float f[V];
+            load_before<T, W, V>(p, i, b, e, W - 1 - k, ch, f);
+            Vec<T, V>::store(p.final_state, (i64 * (W - 1) + k) * p.C + ch, f);
+        }
+        return;
+    }
+    int64_t t = (static_cast<int64_t>(blockIdx.x) * FW + warp) * run;
+    if (t >= p.rows) return;
+    const int64_t t1 = t + run < p.rows ? t + run : p.rows;
+    int32_t i = warp_upper(p.seqs.n, t, [&](int32_t j) { return p.seqs.begin(j); });
+    int64_t b = p.seqs.begin(i), e = p.seqs.end(i);
+    if (ch >= p.C) return;
+    float w[W][V], bias[V], win[W - 1][V];
+    load_taps<W, V>(p, ch, w, bias);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) load_before<T, W, V>(p, i, b, t, W - 1 - k, ch, win[k]);
+    while (t < t1) {
+        Vec<T, V> raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t + u < t1) raw[u].load(p.x, (t + u) * p.x_stride + ch);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t + u >= t1) break;
+            if (t + u >= e) {
+                // the next sequence with tokens; behind the last one nothing is written
+                do {
+                    if (++i >= p.seqs.n) return;
+                    b = p.seqs.begin(i);
+                    e = p.seqs.end(i);
+                } while (t + u >= e);
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) load_before<T, W, V>(p, i, b, t + u, W - 1 - k, ch, win[k]);
+            }
+            float x[V], y[V];
+            raw[u].get(x);
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+                float a = fmaf(w[W - 1][c], x[c], bias[c]);
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) a = fmaf(w[k][c], win[k][c], a);
+                y[c] = kSilu ? a * sigmoidf(a) : a;
+#pragma unroll
+                for (int k = 0; k < W - 2; ++k) win[k][c] = win[k + 1][c];
+                win[W - 2][c] = x[c];
+            }
+            Vec<T, V>::store(p.out, (t + u) * p.out_stride + ch, y);
+        }
+        t += U;
+    }
+}
+
+// ---------------------------------------------------------------- single tokens
+
+template <class T, int W, bool kSilu>
+__global__ void __launch_bounds__(128) conv_decode_kernel(ConvDecodeParams p) {
+    const int per = p.C / V;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (id >= p.batch * per) return;
+    const int64_t r = id / per;
+    const int ch = static_cast<int>(id - r * per) * V;
+    Vec<T, V> x, s[W - 1];
+    x.load(p.x, r * p.x_stride + ch);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+        if (p.state_in)
+            s[k].load(p.state_in, (r * (W - 1) + k) * p.C + ch);
+        else
+            s[k].zero();
+    }
+    ConvParams tp;
+    tp.weight = p.weight;
+    tp.bias = p.bias;
+    float w[W][V], bias[V], f[V], y[V];
+    load_taps<W, V>(tp, ch, w, bias);
+    x.get(f);
+#pragma unroll
+    for (int c = 0; c < V; ++c) y[c] = fmaf(w[W - 1][c], f[c], bias[c]);
+    if (p.state_out) Vec<T, V>::store(p.state_out, (r * (W - 1) + W - 2) * p.C + ch, f);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+        s[k].get(f);
+#pragma unroll
+        for (int c = 0; c < V; ++c) y[c] = fmaf(w[k][c], f[c], y[c]);
+        // in place: row k was read above, before any row is written
+        if (k > 0 && p.state_out) Vec<T, V>::store(p.state_out, (r * (W - 1) + k - 1) * p.C + ch, f);
+    }
+    if (kSilu)
+#pragma unroll
+        for (int c = 0; c < V; ++c) y[c] *= sigmoidf(y[c]);
+    Vec<T, V>::store(p.out, r * p.out_stride + ch, y);
+}
+
+// ---------------------------------------------------------------- gradients
+//
+//   dpre_t = dout_t act'(pre_t)  with pre recomputed from x,
+//   de_j = sum_k w_k dpre_{j+W-1-k} (outputs of the same sequence) + dfinal_state,
+//   dw_k = sum_t dpre_t e_{t-W+1+k},  dbias = sum_t dpre_t.
+//
+// A warp walks `kRun` tokens and the W - 1 behind them (whose dpre it needs for its last dx). 4 channels
+// per thread keep the taps, their gradients and both windows within 128 registers. Each CTA adds its
+// warps' tap gradients in shared memory and writes one partial row; conv_reduce_kernel adds the rows
+// in a fixed order, so a run repeats bit for bit.
+
+constexpr int BV = 4;             // channels per thread
+constexpr int BW = 8;             // warps per CTA
+constexpr int kRun = 32;          // tokens per warp and step
+
+template <class T>
+struct Vec4;
+template <>
+struct Vec4<float> : Vec<float, 4> {};
+template <>
+struct Vec4<__nv_bfloat16> {
+    uint2 raw;
+    __device__ __forceinline__ void load(const void *p, int64_t at) {
+        raw = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + at);
+    }
+    __device__ __forceinline__ void zero() { raw = make_uint2(0u, 0u); }
+    __device__ __forceinline__ void get(float (&x)[4]) const {
+        x[0] = bf_low(raw.x);
+        x[1] = bf_high(raw.x);
+        x[2] = bf_low(raw.y);
+        x[3] = bf_high(raw.y);
+    }
+    static __device__ __forceinline__ void store(void *p, int64_t at, const float (&x)[4]) {
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p) + at) =
+            make_uint2(bf_pair(x[0], x[1]), bf_pair(x[2], x[3]));
+    }
+};
+
+template <class T, int W>
+__device__ __forceinline__ void load_before4(const ConvParams &p, int32_t i, int64_t b, int64_t t, int back, int ch,
+                                             float (&e)[BV]) {
+    Vec4<T> raw;
+    const int64_t pos = t - back - b;
+    if (pos >= 0)
+        raw.load(p.x, (t - back) * p.x_stride + ch);
+    else if (p.init)
+        raw.load(p.init, (static_cast<int64_t>(i) * (W - 1) + (W - 1) + pos) * p.C + ch);
+    else
+        raw.zero();
+    raw.get(e);
+}
+
+template <int W, bool kSilu>
+__device__ __forceinline__ void dpre_of(const float (&w)[W][BV], const float (&bias)[BV], const float (&win)[W - 1][BV],
+                                        const float (&x)[BV], const float (&dy)[BV], float (&d)[BV]) {
+#pragma unroll
+    for (int c = 0; c < BV; ++c) {
+        d[c] = dy[c];
+        if (kSilu) {
+            float a = fmaf(w[W - 1][c], x[c], bias[c]);
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) a = fmaf(w[k][c], win[k][c], a);
+            const float g = sigmoidf(a);
+            d[c] *= g * fmaf(a, 1.f - g, 1.f);
+        }
+    }
+}
+
+// grid (token blocks + sequence blocks, channel blocks of 128). Sequence blocks write dinit: warp w one
+// sequence.
+template <class T, class TD, int W, bool kSilu>
+__global__ void __launch_bounds__(32 * BW, 2) conv_bwd_kernel(ConvParams p, int token_blocks) {
+    __shared__ float part[BW][W + 1][32 * BV];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ch = blockIdx.y * (32 * BV) + lane * BV;
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seqs, &g_conv_error);
+    float w[W][BV], bias[BV];
+    if (ch < p.C) load_taps<W, BV>(p, ch, w, bias);
+    if (blockIdx.x >= token_blocks) {
+        // de_j for the rows before the sequence: its first W - 1 outputs, and what a sequence shorter
+        // than the state passes on from the final state's gradient
+        const int64_t i64 = (static_cast<int64_t>(blockIdx.x) - token_blocks) * BW + warp;
+        if (i64 >= p.seqs.n || ch >= p.C) return;
+        const int32_t i = static_cast<int32_t>(i64);
+        const int64_t b = p.seqs.begin(i), e = p.seqs.end(i);
+        float de[W - 1][BV], win[W - 1][BV];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            load_before4<T, W>(p, i, b, b, W - 1 - j, ch, win[j]);
+            const int64_t slot = j - (e - b);
+            if (p.dfinal && slot >= 0) {
+                Vec4<T> r;
+                r.load(p.dfinal, (i64 * (W - 1) + slot) * p.C + ch);
+                r.get(de[j]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < BV; ++c) de[j][c] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < W - 1; ++u) {
+            if (b + u < e) {
+                Vec4<T> rx;
+                Vec4<TD> rd;
+                float x[BV], dy[BV], d[BV];
+                rx.load(p.x, (b + u) * p.x_stride + ch);
+                rd.load(p.dout, (b + u) * p.dout_stride + ch);
+                rx.get(x);
+                rd.get(dy);
+                dpre_of<W, kSilu>(w, bias, win, x, dy, d);
+                // output u reads row j of the state (place j - (W - 1)) with tap j - u
+#pragma unroll
+                for (int j = u; j < W - 1; ++j)
+#pragma unroll
+                    for (int c = 0; c < BV; ++c) de[j][c] = fmaf(w[j - u][c], d[c], de[j][c]);
+#pragma unroll
+                for (int c = 0; c < BV; ++c) {
+#pragma unroll
+                    for (int k = 0; k < W - 2; ++k) win[k][c] = win[k + 1][c];
+                    win[W - 2][c] = x[c];
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) Vec4<T>::store(p.dinit, (i64 * (W - 1) + j) * p.C + ch, de[j]);
+        return;
+    }
+    float dw[W + 1][BV];
+#pragma unroll
+    for (int k = 0; k <= W; ++k)
+#pragma unroll
+        for (int c = 0; c < BV; ++c) dw[k][c] = 0.f;
+    const int64_t step = static_cast<int64_t>(token_blocks) * BW * kRun;
+    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * BW + warp) * kRun; t0 < p.rows; t0 += step) {
+        const int64_t t1 = t0 + kRun < p.rows ? t0 + kRun : p.rows;
+        int32_t i = warp_upper(p.seqs.n, t0, [&](int32_t j) { return p.seqs.begin(j); });
+        if (ch >= p.C) continue;
+        int64_t a = t0;
+        while (a < t1) {
+            // the part [a, z) of the run that belongs to sequence i = [b, e)
+            int64_t b = p.seqs.begin(i), e = p.seqs.end(i);
+            while (a >= e && i + 1 < p.seqs.n) {
+                ++i;
+                b = p.seqs.begin(i);
+                e = p.seqs.end(i);
+            }
+            if (a >= e) break;   // rows behind the last sequence
+            const int64_t z = t1 < e ? t1 : e;
+            float win[W - 1][BV], dp[W - 1][BV];
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) {
+                load_before4<T, W>(p, i, b, a, W - 1 - k, ch, win[k]);
+#pragma unroll
+                for (int c = 0; c < BV; ++c) dp[k][c] = 0.f;
+            }
+            const int64_t last = z + W - 1;
+            for (int64_t t = a; t < last; t += U) {
+                Vec4<T> rx[U];
+                Vec4<TD> rd[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (t + u < last && t + u < e) {
+                        rx[u].load(p.x, (t + u) * p.x_stride + ch);
+                        rd[u].load(p.dout, (t + u) * p.dout_stride + ch);
+                    } else {
+                        rx[u].zero();
+                        rd[u].zero();
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t tt = t + u;
+                    if (tt >= last) break;
+                    float x[BV], dy[BV], d[BV];
+                    rx[u].get(x);
+                    rd[u].get(dy);
+                    // behind the sequence's end dy is zero, and with it d
+                    dpre_of<W, kSilu>(w, bias, win, x, dy, d);
+                    if (tt >= e)
+#pragma unroll
+                        for (int c = 0; c < BV; ++c) d[c] = 0.f;   // also where pre is not finite
+                    const int64_t o = tt - (W - 1);
+                    if (o >= a) {
+                        float g[BV];
+#pragma unroll
+                        for (int c = 0; c < BV; ++c) {
+                            g[c] = w[0][c] * d[c];
+#pragma unroll
+                            for (int k = 1; k < W; ++k) g[c] = fmaf(w[k][c], dp[W - 1 - k][c], g[c]);
+                        }
+                        const int64_t slot = o - (e - (W - 1));
+                        if (p.dfinal && slot >= 0) {
+                            Vec4<T> r;
+                            float f[BV];
+                            r.load(p.dfinal, (static_cast<int64_t>(i) * (W - 1) + slot) * p.C + ch);
+                            r.get(f);
+#pragma unroll
+                            for (int c = 0; c < BV; ++c) g[c] += f[c];
+                        }
+                        Vec4<T>::store(p.dx, o * p.dx_stride + ch, g);
+                    }
+                    if (tt < z) {
+#pragma unroll
+                        for (int c = 0; c < BV; ++c) {
+#pragma unroll
+                            for (int k = 0; k < W - 1; ++k) dw[k][c] = fmaf(d[c], win[k][c], dw[k][c]);
+                            dw[W - 1][c] = fmaf(d[c], x[c], dw[W - 1][c]);
+                            dw[W][c] += d[c];
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < BV; ++c) {
+#pragma unroll
+                        for (int k = 0; k < W - 2; ++k) {
+                            win[k][c] = win[k + 1][c];
+                            dp[k][c] = dp[k + 1][c];
+                        }
+                        win[W - 2][c] = x[c];
+                        dp[W - 2][c] = d[c];
+                    }
+                }
+            }
+            a = z;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k <= W; ++k)
+#pragma unroll
+        for (int c = 0; c < BV; ++c) part[warp][k][lane * BV + c] = dw[k][c];
+    __syncthreads();
+    for (int j = threadIdx.x; j < (W + 1) * 32 * BV; j += 32 * BW) {
+        const int k = j / (32 * BV), c = j % (32 * BV), gc = blockIdx.y * (32 * BV) + c;
+        if (gc >= p.C) continue;
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < BW; ++q) s += part[q][k][c];
+        p.partial[(static_cast<int64_t>(blockIdx.x) * (W + 1) + k) * p.C + gc] = s;
+    }
+}
+
+template <int W>
+__global__ void __launch_bounds__(128) conv_reduce_kernel(ConvParams p, int blocks) {
+    const int c = blockIdx.x * 128 + threadIdx.x, k = blockIdx.y;
+    if (c >= p.C) return;
+    float s = 0.f;
+#pragma unroll 4
+    for (int b = 0; b < blocks; ++b) s += p.partial[(static_cast<int64_t>(b) * (W + 1) + k) * p.C + c];
+    if (k < W) {
+        if (p.dweight) p.dweight[static_cast<int64_t>(c) * W + k] = s;
+    } else if (p.dbias) {
+        p.dbias[c] = s;
+    }
+}
+
+template <class F>
+cudaError_t by_taps(int W, F f) {
+    switch (W) {
+        case 2: return f(std::integral_constant<int, 2>());
+        case 3: return f(std::integral_constant<int, 3>());
+        default: return f(std::integral_constant<int, 4>());
+    }
+}
+
+template <class T, int W>
+cudaError_t fwd(const ConvParams &p, cudaStream_t s) {
+    // Long runs re-read fewer rows (W - 1 of every `run`); short ones make enough warps of few tokens.
+    const int64_t cblocks = (p.C + 32 * V - 1) / (32 * V);
+    int run = 16;
+    while (run > U && (p.rows + run - 1) / run * cblocks < 148 * 16) run /= 2;
+    const int64_t tb = (p.rows + FW * run - 1) / (FW * run);
+    const int64_t sb = p.final_state ? (p.seqs.n + FW - 1) / FW : 0;
+    if (tb + sb == 0) return cudaSuccess;
+    if (tb + sb > 0x7fffffffLL || cblocks > 65535) return cudaErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(tb + sb), static_cast<unsigned>(cblocks));
+    if (p.silu)
+        conv_fwd_kernel<T, W, true><<<grid, 32 * FW, 0, s>>>(p, run, tb);
+    else
+        conv_fwd_kernel<T, W, false><<<grid, 32 * FW, 0, s>>>(p, run, tb);
+    return cudaGetLastError();
+}
+
+template <class T, class TD, int W>
+cudaError_t bwd(const ConvParams &p, cudaStream_t s) {
+    const int32_t tb = conv_bwd_blocks(p.rows, p.C);
+    const int64_t cblocks = (p.C + 32 * BV - 1) / (32 * BV);
+    const int64_t sb = p.dinit ? (p.seqs.n + BW - 1) / BW : 0;
+    if (tb + sb > 0x7fffffffLL || cblocks > 65535) return cudaErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(tb + sb), static_cast<unsigned>(cblocks));
+    if (p.silu)
+        conv_bwd_kernel<T, TD, W, true><<<grid, 32 * BW, 0, s>>>(p, tb);
+    else
+        conv_bwd_kernel<T, TD, W, false><<<grid, 32 * BW, 0, s>>>(p, tb);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess || (!p.dweight && !p.dbias)) return err;
+    conv_reduce_kernel<W><<<dim3((p.C + 127) / 128, W + 1), 128, 0, s>>>(p, tb);
+    return cudaGetLastError();
+}
+
+template <class T, int W>
+cudaError_t decode(const ConvDecodeParams &p, cudaStream_t s) {
+    const int64_t blocks = (p.batch * (p.C / V) + 127) / 128;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (p.silu)
+        conv_decode_kernel<T, W, true><<<static_cast<unsigned>(blocks), 128, 0, s>>>(p);
+    else
+        conv_decode_kernel<T, W, false><<<static_cast<unsigned>(blocks), 128, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace conv
+
+int32_t conv_bwd_blocks(int64_t rows, int32_t C) {
+    // about four CTAs for each SM over all channel blocks: each writes one row of partial sums
+    const int64_t cblocks = (static_cast<int64_t>(C) + 32 * conv::BV - 1) / (32 * conv::BV);
+    const int64_t most = (rows + conv::BW * conv::kRun - 1) / (conv::BW * conv::kRun);
+    const int64_t want = (4 * 148 + cblocks - 1) / cblocks;
+    const int64_t n = most < want ? most : want;
+    return static_cast<int32_t>(n < 1 ? 1 : n);
+}
+
+cudaError_t launch_conv_fwd(const ConvParams &p, cudaStream_t s) {
+    return conv::by_taps(p.W, [&](auto w) {
+        constexpr int W = decltype(w)::value;
+        return p.fp32 ? conv::fwd<float, W>(p, s) : conv::fwd<__nv_bfloat16, W>(p, s);
+    });
+}
+
+cudaError_t launch_conv_bwd(const ConvParams &p, cudaStream_t s) {
+    return conv::by_taps(p.W, [&](auto w) {
+        constexpr int W = decltype(w)::value;
+        if (p.fp32) return conv::bwd<float, float, W>(p, s);
+        return p.dout_fp32 ? conv::bwd<__nv_bfloat16, float, W>(p, s) : conv::bwd<__nv_bfloat16, __nv_bfloat16, W>(p, s);
+    });
+}
+
+cudaError_t launch_conv_decode(const ConvDecodeParams &p, cudaStream_t s) {
+    return conv::by_taps(p.W, [&](auto w) {
+        constexpr int W = decltype(w)::value;
+        return p.fp32 ? conv::decode<float, W>(p, s) : conv::decode<__nv_bfloat16, W>(p, s);
+    });
+}
+
+cudaError_t read_and_clear_conv_error(unsigned int *value) {
+    cudaError_t err = cudaMemcpyFromSymbol(value, conv::g_conv_error, sizeof(*value));
+    if (err != cudaSuccess || *value == 0) return err;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(conv::g_conv_error, &zero, sizeof(zero));
+}
+
+}  // namespace kda

@@ -1,0 +1,71 @@
+// Internal interface of the selective state space scan kernels (see include/kda.h, kda_scan_*).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_seq.cuh"
+
+namespace kda {
+
+struct ScanParams {
+    Seqs seqs;
+    int64_t rows;                 // tokens in all
+    int32_t H, G, P, N;           // heads, groups of B and C, head channels (64 or 128), state size (64 or 128)
+    const uint16_t *x;            // bf16, row r, head h at x + r * x_stride + h * P
+    int64_t x_stride;
+    const float *dt;              // [rows, H]
+    const float *A;               // [H]
+    const uint16_t *B, *C;        // bf16, row r, group g at B + r * b_stride + g * N
+    int64_t b_stride, c_stride;
+    const float *D, *dt_bias;     // [H] or nullptr
+    int32_t softplus;
+    const void *h0;               // [n, H, N, P] or nullptr
+    int32_t h0_fp32;
+    void *hT;                     // [n, H, N, P] or nullptr
+    int32_t hT_fp32;
+    uint16_t *out;                // bf16, row r, head h at out + r * out_stride + h * P
+    int64_t out_stride;
+    float *ws;                    // scan_fwd_workspace_bytes
+    // backward
+    const uint16_t *dout;         // bf16, row r, head h at dout + r * dout_stride + h * P
+    int64_t dout_stride;
+    const float *dhT;             // [n, H, N, P] or nullptr
+    uint16_t *dx, *dB, *dC;       // bf16, strided as x, B, C are
+    int64_t dx_stride, db_stride, dc_stride;
+    float *ddt;                   // [rows, H]
+    float *dA, *dD, *ddt_bias;    // [H] (dD, ddt_bias or nullptr)
+    float *dh0;                   // [n, H, N, P] or nullptr
+};
+
+struct ScanDecodeParams {
+    int64_t batch;
+    int32_t H, G, P, N;
+    const uint16_t *x, *B, *C;
+    int64_t x_stride, b_stride, c_stride;
+    const float *dt, *A, *D, *dt_bias;
+    int32_t softplus;
+    const void *state_in;         // [batch, H, N, P] or nullptr (zeros)
+    void *state_out;              // or nullptr
+    int32_t state_fp32;
+    uint16_t *out;                // [batch, H, P]
+};
+
+size_t scan_fwd_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N);
+size_t scan_bwd_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t G, int32_t P, int32_t N);
+cudaError_t launch_scan_fwd(const ScanParams &p, cudaStream_t stream);
+cudaError_t launch_scan_bwd(const ScanParams &p, cudaStream_t stream);
+cudaError_t launch_scan_decode(const ScanDecodeParams &p, cudaStream_t stream);
+cudaError_t read_and_clear_scan_error(unsigned int *value);
+
+// Steps of the forward that the backward takes too (kda_scan_fwd.cu): the states entering every
+// 64-token cell of every sequence, or, with `reverse`, the gradients of the states leaving them.
+// Cells lie on the global grid of 64 tokens; sequence i's cell c has slot i + c of `states`
+// [slots, H, N, P]. `ws` as for the forward. Reverse: end_state receives what reaches the start (dh0).
+cudaError_t launch_scan_states(const ScanParams &p, bool reverse, float *states, float *ws, cudaStream_t stream);
+
+constexpr int kScanTile = 64;     // tokens per tile
+// slots of the 64-token cells of n sequences over `rows` tokens
+inline int64_t scan_cells(int64_t rows, int64_t n) { return rows / kScanTile + n; }
+
+}  // namespace kda
