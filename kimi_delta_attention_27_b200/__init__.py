@@ -9,7 +9,9 @@ device, the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 import threading
 
@@ -36,6 +38,7 @@ NOALLOC_MAX_UNITS = 32
 
 KDA_DTYPE_NONE, KDA_DTYPE_BF16, KDA_DTYPE_FP32 = 0, 1, 2
 
+_HERE = contextlib.nullcontext()
 _lock = threading.Lock()
 _lib = None
 
@@ -448,49 +451,60 @@ def _check_rows(name, t, dtypes, shape, lead):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    width = 1
+    width = math.prod(shape[lead:])
+    if t.is_contiguous() or not t.numel():
+        return width
+    inner = 1
     for n, st in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
-        if n > 1 and t.numel() and st != width:
+        if n > 1 and st != inner:
             raise ValueError(f"{name} must be contiguous within a row")
-        width *= n
+        inner *= n
     stride, below = width, 1
-    if t.numel():
-        for n, st in zip(reversed(t.shape[:lead]), reversed(t.stride()[:lead])):
-            if n > 1 and below == 1:
-                stride = st
-            elif n > 1 and st != stride * below:
-                raise ValueError(f"{name}'s rows must be evenly spaced")
-            below *= n
+    for n, st in zip(reversed(t.shape[:lead]), reversed(t.stride()[:lead])):
+        if n > 1 and below == 1:
+            stride = st
+        elif n > 1 and st != stride * below:
+            raise ValueError(f"{name}'s rows must be evenly spaced")
+        below *= n
     if stride < width:
         raise ValueError(f"{name}'s rows must not overlap")
     return stride
 
 
-class _Stream:
-    """``with _Stream(dev, stream) as handle``: the device is current, and so is the stream, so that what is
-    allocated inside belongs to the stream the kernels run on."""
-
-    def __init__(self, dev, stream):
+def _check_param(name, t, shape):
+    """Validate an optional contiguous fp32 tensor."""
+    if t is not None:
         import torch
-        self.dev = torch.cuda.device(dev)
-        here = torch.cuda.current_stream(dev)
-        self.handle = here.cuda_stream if stream is None else int(stream)
-        self.stream = None
-        if self.handle != here.cuda_stream:
-            self.stream = torch.cuda.stream(torch.cuda.ExternalStream(self.handle, device=dev))
+        _check(name, t, torch.float32, shape=shape)
 
-    def __enter__(self):
-        self.dev.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
-        return ctypes.c_void_p(self.handle)
 
-    def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        return self.dev.__exit__(*exc)
+def _one_device(first, *others):
+    """``first``'s device, which must be a CUDA device that the others (or None) are on too."""
+    at = first.get_device()
+    if at < 0:
+        raise ValueError("tensors must be on a CUDA device (no CPU path exists)")
+    for t in others:
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"all tensors must be on {first.device}, got {t.device}")
+    return first.device
+
+
+def _stream_of(dev, stream):
+    """(the handle to launch on, a context in which ``dev`` is the current device and the handle's stream the
+    current stream): what is allocated in it belongs to the stream the kernels run on."""
+    import torch
+    here = torch.cuda.current_stream(dev).cuda_stream
+    handle = here if stream is None else int(stream)
+    if handle != here:
+        # torch.cuda.stream makes the stream's device current, too
+        return handle, torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev))
+    return handle, _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _raise(lib, st):
@@ -507,7 +521,7 @@ def _scratch(need, given, dev):
 
 
 def _size(t):
-    return 0 if t is None else int(t.numel())
+    return 0 if t is None else t.numel()
 
 
 def _num_seqs(cu_seqlens, B):
@@ -529,8 +543,7 @@ def _conv_args(x, weight, bias, lead):
     _check("weight", weight, torch.float32, 2)
     W = weight.shape[1]
     _check("weight", weight, torch.float32, shape=(C, W))
-    if bias is not None:
-        _check("bias", bias, torch.float32, shape=(C,))
+    _check_param("bias", bias, (C,))
     return C, W, xs
 
 
@@ -549,20 +562,20 @@ def kda_conv_fwd(x, weight, bias=None, silu: bool = True, cu_seqlens=None, initi
     for name, t in (("initial_state", initial_state), ("final_state", final_state)):
         if t is not None:
             _check(name, t, x.dtype, shape=(N, W - 1, C))
-    if out is not None:
-        _check_rows("out", out, (x.dtype,), x.shape, 2)
-    dev = _check_devices(x=x, weight=weight, bias=bias, cu_seqlens=cu_seqlens, initial_state=initial_state,
-                         final_state=final_state, out=out)
+    os = C if out is None else _check_rows("out", out, (x.dtype,), x.shape, 2)
+    dev = _one_device(x, weight, bias, cu_seqlens, initial_state,
+                      final_state, out)
     lib = load_library()
-    with _Stream(dev, stream) as handle:
+    handle, ctx = _stream_of(dev, stream)
+    with ctx:
         if out is None:
             out = torch.empty((B, T, C), dtype=x.dtype, device=dev)
         if final_state is None and want_final_state:
             final_state = torch.empty((N, W - 1, C), dtype=x.dtype, device=dev)
-        _raise(lib, lib.kda_conv_fwd(_ptr(x), _dtype_code(x), xs, _ptr(weight), _ptr(bias),
-                                     KDA_FLAG_CONV_SILU if silu else 0, _ptr(cu_seqlens), N, B, T, C, W,
-                                     _ptr(initial_state), _ptr(final_state), _ptr(out),
-                                     _check_rows("out", out, (x.dtype,), x.shape, 2), handle))
+        _raise(lib, lib.kda_conv_fwd(_addr(x), _dtype_code(x), xs, _addr(weight), _addr(bias),
+                                     KDA_FLAG_CONV_SILU if silu else 0, _addr(cu_seqlens), N, B, T, C, W,
+                                     _addr(initial_state), _addr(final_state), _addr(out),
+                                     os, handle))
     return out, final_state
 
 
@@ -580,23 +593,23 @@ def kda_conv_bwd(x, weight, dout, bias=None, silu: bool = True, cu_seqlens=None,
     for name, t in (("initial_state", initial_state), ("dfinal_state", dfinal_state)):
         if t is not None:
             _check(name, t, x.dtype, shape=(N, W - 1, C))
-    if dx is not None:
-        _check_rows("dx", dx, (x.dtype,), x.shape, 2)
-    dev = _check_devices(x=x, weight=weight, bias=bias, cu_seqlens=cu_seqlens, initial_state=initial_state,
-                         dout=dout, dfinal_state=dfinal_state, dx=dx, workspace=workspace)
+    dxs = C if dx is None else _check_rows("dx", dx, (x.dtype,), x.shape, 2)
+    dev = _one_device(x, weight, bias, cu_seqlens, initial_state,
+                      dout, dfinal_state, dx, workspace)
     lib = load_library()
-    with _Stream(dev, stream) as handle:
+    handle, ctx = _stream_of(dev, stream)
+    with ctx:
         if dx is None:
             dx = torch.empty((B, T, C), dtype=x.dtype, device=dev)
         dweight = torch.empty((C, W), dtype=torch.float32, device=dev)
         dbias = torch.empty(C, dtype=torch.float32, device=dev) if bias is not None else None
         dinit = torch.empty((N, W - 1, C), dtype=x.dtype, device=dev) if want_dinitial_state else None
         ws = _scratch(int(lib.kda_conv_bwd_workspace(B * T, C, W)), workspace, dev)
-        _raise(lib, lib.kda_conv_bwd(_ptr(x), _dtype_code(x), xs, _ptr(weight), _ptr(bias),
-                                     KDA_FLAG_CONV_SILU if silu else 0, _ptr(cu_seqlens), N, B, T, C, W,
-                                     _ptr(initial_state), _ptr(dout), _dtype_code(dout), ds, _ptr(dfinal_state),
-                                     _ptr(dx), _check_rows("dx", dx, (x.dtype,), x.shape, 2), _ptr(dweight),
-                                     _ptr(dbias), _ptr(dinit), _ptr(ws), _size(ws), handle))
+        _raise(lib, lib.kda_conv_bwd(_addr(x), _dtype_code(x), xs, _addr(weight), _addr(bias),
+                                     KDA_FLAG_CONV_SILU if silu else 0, _addr(cu_seqlens), N, B, T, C, W,
+                                     _addr(initial_state), _addr(dout), _dtype_code(dout), ds, _addr(dfinal_state),
+                                     _addr(dx), dxs, _addr(dweight),
+                                     _addr(dbias), _addr(dinit), _addr(ws), _size(ws), handle))
     return dict(dx=dx, dweight=dweight, dbias=dbias, dinitial_state=dinit)
 
 
@@ -611,16 +624,16 @@ def kda_conv_decode(x, weight, state_in=None, state_out=None, bias=None, silu: b
     for name, t in (("state_in", state_in), ("state_out", state_out)):
         if t is not None:
             _check(name, t, x.dtype, shape=(B, W - 1, C))
-    if out is not None:
-        _check_rows("out", out, (x.dtype,), x.shape, 1)
-    dev = _check_devices(x=x, weight=weight, bias=bias, state_in=state_in, state_out=state_out, out=out)
+    os = C if out is None else _check_rows("out", out, (x.dtype,), x.shape, 1)
+    dev = _one_device(x, weight, bias, state_in, state_out, out)
     lib = load_library()
-    with _Stream(dev, stream) as handle:
+    handle, ctx = _stream_of(dev, stream)
+    with ctx:
         if out is None:
             out = torch.empty((B, C), dtype=x.dtype, device=dev)
-        _raise(lib, lib.kda_conv_decode(_ptr(x), _dtype_code(x), xs, _ptr(weight), _ptr(bias),
-                                        KDA_FLAG_CONV_SILU if silu else 0, B, C, W, _ptr(state_in), _ptr(state_out),
-                                        _ptr(out), _check_rows("out", out, (x.dtype,), x.shape, 1), handle))
+        _raise(lib, lib.kda_conv_decode(_addr(x), _dtype_code(x), xs, _addr(weight), _addr(bias),
+                                        KDA_FLAG_CONV_SILU if silu else 0, B, C, W, _addr(state_in), _addr(state_out),
+                                        _addr(out), os, handle))
     return out, state_out
 
 
@@ -635,9 +648,8 @@ def _qk_args(q, k, norm, q_weight, k_weight, positions, inv_freq):
     qs = _check_rows("q", q, (torch.bfloat16,), q.shape, 2)
     Hk = 0 if k is None else k.shape[2]
     ks = 0 if k is None else _check_rows("k", k, (torch.bfloat16,), (B, T, Hk, D), 2)
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if t is not None:
-            _check(name, t, torch.float32, shape=(D,))
+    _check_param("q_weight", q_weight, (D,))
+    _check_param("k_weight", k_weight, (D,))
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq come together")
     rot = 0
@@ -662,23 +674,21 @@ def kda_qk_fwd(q, k=None, norm: str = "l2", q_weight=None, k_weight=None, eps: f
     if k is None and k_out is not None:
         raise ValueError("k_out without k")
     bf = (torch.bfloat16,)
-    if q_out is not None:
-        _check_rows("q_out", q_out, bf, q.shape, 2)
-    if k_out is not None:
-        _check_rows("k_out", k_out, bf, k.shape, 2)
-    dev = _check_devices(q=q, k=k, q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq,
-                         q_out=q_out, k_out=k_out)
+    qos = Hq * D if q_out is None else _check_rows("q_out", q_out, bf, q.shape, 2)
+    kos = Hk * D if k_out is None else _check_rows("k_out", k_out, bf, k.shape, 2)
+    dev = _one_device(q, k, q_weight, k_weight, positions, inv_freq,
+                      q_out, k_out)
     lib = load_library()
-    with _Stream(dev, stream) as handle:
+    handle, ctx = _stream_of(dev, stream)
+    with ctx:
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
         if k_out is None and k is not None:
             k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-        _raise(lib, lib.kda_qk_fwd(_ptr(q), qs, _ptr(k), ks, B * T, Hq, Hk, D, NORM_KINDS[norm], float(eps),
-                                   _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), rot,
+        _raise(lib, lib.kda_qk_fwd(_addr(q), qs, _addr(k), ks, B * T, Hq, Hk, D, NORM_KINDS[norm], float(eps),
+                                   _addr(q_weight), _addr(k_weight), _addr(positions), _addr(inv_freq), rot,
                                    int(bool(interleaved)), float(factor),
-                                   _ptr(q_out), _check_rows("q_out", q_out, bf, q.shape, 2),
-                                   _ptr(k_out), _check_rows("k_out", k_out, bf, k.shape, 2) if Hk else 0, handle))
+                                   _addr(q_out), qos, _addr(k_out), kos, handle))
     return q_out, k_out
 
 
@@ -698,10 +708,11 @@ def kda_qk_bwd(q, k, dq_out, dk_out, norm: str = "l2", q_weight=None, k_weight=N
         raise ValueError("k_weight without k")
     dqs = _check_rows("dq_out", dq_out, (torch.bfloat16, torch.float32), q.shape, 2)
     dks = 0 if k is None else _check_rows("dk_out", dk_out, (dq_out.dtype,), k.shape, 2)
-    dev = _check_devices(q=q, k=k, q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq,
-                         dq_out=dq_out, dk_out=dk_out, workspace=workspace)
+    dev = _one_device(q, k, q_weight, k_weight, positions, inv_freq,
+                      dq_out, dk_out, workspace)
     lib = load_library()
-    with _Stream(dev, stream) as handle:
+    handle, ctx = _stream_of(dev, stream)
+    with ctx:
         dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
         dk = torch.empty(k.shape, dtype=k.dtype, device=dev) if k is not None else None
         dqw = torch.empty(D, dtype=torch.float32, device=dev) if q_weight is not None else None
@@ -710,11 +721,11 @@ def kda_qk_bwd(q, k, dq_out, dk_out, norm: str = "l2", q_weight=None, k_weight=N
         if dqw is not None or dkw is not None:
             need = int(lib.kda_qk_bwd_workspace(B * T, Hq, Hk, D))
         ws = _scratch(need, workspace, dev)
-        _raise(lib, lib.kda_qk_bwd(_ptr(q), qs, _ptr(k), ks, B * T, Hq, Hk, D, NORM_KINDS[norm], float(eps),
-                                   _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), rot,
-                                   int(bool(interleaved)), float(factor), _ptr(dq_out), dqs, _ptr(dk_out), dks,
-                                   _dtype_code(dq_out), _ptr(dq), Hq * D, _ptr(dk), Hk * D, _ptr(dqw), _ptr(dkw),
-                                   _ptr(ws), _size(ws), handle))
+        _raise(lib, lib.kda_qk_bwd(_addr(q), qs, _addr(k), ks, B * T, Hq, Hk, D, NORM_KINDS[norm], float(eps),
+                                   _addr(q_weight), _addr(k_weight), _addr(positions), _addr(inv_freq), rot,
+                                   int(bool(interleaved)), float(factor), _addr(dq_out), dqs, _addr(dk_out), dks,
+                                   _dtype_code(dq_out), _addr(dq), Hq * D, _addr(dk), Hk * D, _addr(dqw), _addr(dkw),
+                                   _addr(ws), _size(ws), handle))
     return dict(dq=dq, dk=dk, dq_weight=dqw, dk_weight=dkw)
 
 
@@ -731,9 +742,8 @@ def _scan_args(x, dt, A, B, C, D, dt_bias, lead):
                _check_rows("C", C, bf, rows + (G, N), lead))
     _check("dt", dt, torch.float32, shape=rows + (H,))
     _check("A", A, torch.float32, shape=(H,))
-    for name, t in (("D", D), ("dt_bias", dt_bias)):
-        if t is not None:
-            _check(name, t, torch.float32, shape=(H,))
+    _check_param("D", D, (H,))
+    _check_param("dt_bias", dt_bias, (H,))
     return H, P, G, N, strides
 
 
@@ -755,23 +765,23 @@ def kda_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus: bool = False
         if t is not None:
             _check(name, t, None, shape=(n, H, N, P))
     bf = (torch.bfloat16,)
-    if out is not None:
-        _check_rows("out", out, bf, x.shape, 2)
-    dev = _check_devices(x=x, dt=dt, A=A, B=B, C=C, D=D, dt_bias=dt_bias, cu_seqlens=cu_seqlens,
-                         initial_state=initial_state, final_state=final_state, out=out, workspace=workspace)
+    os = H * P if out is None else _check_rows("out", out, bf, x.shape, 2)
+    dev = _one_device(x, dt, A, B, C, D, dt_bias, cu_seqlens,
+                      initial_state, final_state, out, workspace)
     lib = load_library()
-    with _Stream(dev, stream) as handle:
+    handle, ctx = _stream_of(dev, stream)
+    with ctx:
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=dev)
         if final_state is None and final_state_dtype is not None:
             final_state = torch.empty((n, H, N, P), dtype=final_state_dtype, device=dev)
         ws = _scratch(int(lib.kda_scan_fwd_workspace(Bn * T, n, H, P, N)), workspace, dev)
         ic, fc = _dtype_code(initial_state), _dtype_code(final_state)
-        _raise(lib, lib.kda_scan_fwd(_ptr(x), xs, _ptr(dt), _ptr(A), _ptr(B), bs, _ptr(C), cs, _ptr(D), _ptr(dt_bias),
-                                     KDA_FLAG_SCAN_SOFTPLUS if dt_softplus else 0, _ptr(cu_seqlens), n, Bn, T, H, G,
-                                     P, N, _ptr(initial_state), ic if ic >= 0 else 99, _ptr(final_state),
-                                     fc if fc >= 0 else 99, _ptr(out), _check_rows("out", out, bf, x.shape, 2),
-                                     _ptr(ws), _size(ws), handle))
+        _raise(lib, lib.kda_scan_fwd(_addr(x), xs, _addr(dt), _addr(A), _addr(B), bs, _addr(C), cs, _addr(D), _addr(dt_bias),
+                                     KDA_FLAG_SCAN_SOFTPLUS if dt_softplus else 0, _addr(cu_seqlens), n, Bn, T, H, G,
+                                     P, N, _addr(initial_state), ic if ic >= 0 else 99, _addr(final_state),
+                                     fc if fc >= 0 else 99, _addr(out), os,
+                                     _addr(ws), _size(ws), handle))
     return out, final_state
 
 
@@ -792,14 +802,15 @@ def kda_scan_bwd(x, dt, A, B, C, dout, D=None, dt_bias=None, dt_softplus: bool =
         _check("initial_state", initial_state, None, shape=(n, H, N, P))
     if dfinal_state is not None:
         _check("dfinal_state", dfinal_state, torch.float32, shape=(n, H, N, P))
-    for name, t, like in (("dx", dx, x), ("dB", dB, B), ("dC", dC, C)):
-        if t is not None:
-            _check_rows(name, t, bf, like.shape, 2)
-    dev = _check_devices(x=x, dt=dt, A=A, B=B, C=C, D=D, dt_bias=dt_bias, dout=dout, cu_seqlens=cu_seqlens,
-                         initial_state=initial_state, dfinal_state=dfinal_state, dx=dx, dB=dB, dC=dC,
-                         workspace=workspace)
+    dxs = H * P if dx is None else _check_rows("dx", dx, bf, x.shape, 2)
+    dbs = G * N if dB is None else _check_rows("dB", dB, bf, B.shape, 2)
+    dcs = G * N if dC is None else _check_rows("dC", dC, bf, C.shape, 2)
+    dev = _one_device(x, dt, A, B, C, D, dt_bias, dout, cu_seqlens,
+                      initial_state, dfinal_state, dx, dB, dC,
+                      workspace)
     lib = load_library()
-    with _Stream(dev, stream) as handle:
+    handle, ctx = _stream_of(dev, stream)
+    with ctx:
         empty = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
         f32 = torch.float32
         dx = empty(x.shape, x.dtype) if dx is None else dx
@@ -811,14 +822,13 @@ def kda_scan_bwd(x, dt, A, B, C, dout, D=None, dt_bias=None, dt_softplus: bool =
                    dh0=empty((n, H, N, P), f32) if want_dinitial_state else None)
         ws = _scratch(int(lib.kda_scan_bwd_workspace(Bn * T, n, H, G, P, N)), workspace, dev)
         ic = _dtype_code(initial_state)
-        _raise(lib, lib.kda_scan_bwd(_ptr(x), xs, _ptr(dt), _ptr(A), _ptr(B), bs, _ptr(C), cs, _ptr(D), _ptr(dt_bias),
-                                     KDA_FLAG_SCAN_SOFTPLUS if dt_softplus else 0, _ptr(cu_seqlens), n, Bn, T, H, G,
-                                     P, N, _ptr(initial_state), ic if ic >= 0 else 99, _ptr(dout), ds,
-                                     _ptr(dfinal_state), _ptr(dx), _check_rows("dx", dx, bf, x.shape, 2),
-                                     _ptr(out["ddt"]), _ptr(out["dA"]), _ptr(dB),
-                                     _check_rows("dB", dB, bf, B.shape, 2), _ptr(dC),
-                                     _check_rows("dC", dC, bf, C.shape, 2), _ptr(out["dD"]), _ptr(out["ddt_bias"]),
-                                     _ptr(out["dh0"]), _ptr(ws), _size(ws), handle))
+        _raise(lib, lib.kda_scan_bwd(_addr(x), xs, _addr(dt), _addr(A), _addr(B), bs, _addr(C), cs, _addr(D), _addr(dt_bias),
+                                     KDA_FLAG_SCAN_SOFTPLUS if dt_softplus else 0, _addr(cu_seqlens), n, Bn, T, H, G,
+                                     P, N, _addr(initial_state), ic if ic >= 0 else 99, _addr(dout), ds,
+                                     _addr(dfinal_state), _addr(dx), dxs,
+                                     _addr(out["ddt"]), _addr(out["dA"]), _addr(dB),
+                                     dbs, _addr(dC), dcs, _addr(out["dD"]), _addr(out["ddt_bias"]),
+                                     _addr(out["dh0"]), _addr(ws), _size(ws), handle))
     return out
 
 
@@ -847,17 +857,18 @@ def kda_scan_decode(x, dt, A, B, C, state_in=None, state_out=None, D=None, dt_bi
         raise ValueError("state_dtype must be state_in's")
     if out is not None:
         _check("out", out, torch.bfloat16, shape=x.shape)
-    dev = _check_devices(x=x, dt=dt, A=A, B=B, C=C, D=D, dt_bias=dt_bias, state_in=state_in, state_out=state_out,
-                         out=out)
+    dev = _one_device(x, dt, A, B, C, D, dt_bias, state_in, state_out,
+                      out)
     lib = load_library()
-    with _Stream(dev, stream) as handle:
+    handle, ctx = _stream_of(dev, stream)
+    with ctx:
         if state_out is None and state_dtype is not None:
             state_out = torch.empty((n, H, N, P), dtype=state_dtype, device=dev)
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=dev)
         code = _dtype_code(state_in if state_in is not None else state_out)
-        _raise(lib, lib.kda_scan_decode(_ptr(x), xs, _ptr(dt), _ptr(A), _ptr(B), bs, _ptr(C), cs, _ptr(D),
-                                        _ptr(dt_bias), KDA_FLAG_SCAN_SOFTPLUS if dt_softplus else 0, n, H, G, P, N,
-                                        _ptr(state_in), _ptr(state_out), code if code >= 0 else 99, _ptr(out),
+        _raise(lib, lib.kda_scan_decode(_addr(x), xs, _addr(dt), _addr(A), _addr(B), bs, _addr(C), cs, _addr(D),
+                                        _addr(dt_bias), KDA_FLAG_SCAN_SOFTPLUS if dt_softplus else 0, n, H, G, P, N,
+                                        _addr(state_in), _addr(state_out), code if code >= 0 else 99, _addr(out),
                                         handle))
     return out, state_out

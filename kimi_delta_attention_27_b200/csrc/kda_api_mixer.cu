@@ -199,7 +199,8 @@ void scan_params(const ScanArgs &a, const kda::Seqs &s, int64_t rows, kda::ScanP
 }
 
 bool scan_too_large(int64_t rows, int64_t n, int32_t H, int32_t P) {
-    // the largest grid is one CTA per (64-token cell, head, 64 columns)
+    // rows are 32-bit coordinates of tensor maps; the largest grid is one CTA per (64-token cell, head, 64 columns)
+    if (rows > 0x7fffffffLL) return true;
     return kda::scan_cells(rows, n) > 0x7fffffffLL / (static_cast<int64_t>(H) * (P / 64));
 }
 

@@ -61,10 +61,18 @@ cudaError_t read_and_clear_scan_error(unsigned int *value);
 // Steps of the forward that the backward takes too (kda_scan_fwd.cu): the states entering every
 // 64-token cell of every sequence, or, with `reverse`, the gradients of the states leaving them.
 // Cells lie on the global grid of 64 tokens; sequence i's cell c has slot i + c of `states`
-// [slots, H, N, P]. `ws` as for the forward. Reverse: end_state receives what reaches the start (dh0).
+// [slots, H, N, P]. `ws`: scan_states_workspace_bytes. Reverse: what reaches the start goes to dh0.
+size_t scan_states_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N);
 cudaError_t launch_scan_states(const ScanParams &p, bool reverse, float *states, float *ws, cudaStream_t stream);
 
+// The forward's kernel for a state size of 128 (kda_scan_tc.cu): the main run over pieces (`out`), from the
+// states in `entering` or h0, or the run that finds each piece's own contribution to the state (leave, decay).
+cudaError_t launch_scan_tc(const ScanParams &p, bool out, int64_t seg, int64_t units, const float *entering, float *leave,
+                           float *decay, cudaStream_t stream);
+cudaError_t read_and_clear_scan_tc_error(unsigned int *value);
+
 constexpr int kScanTile = 64;     // tokens per tile
+constexpr int kScanTcTile = 128;  // and of launch_scan_tc
 // slots of the 64-token cells of n sequences over `rows` tokens
 inline int64_t scan_cells(int64_t rows, int64_t n) { return rows / kScanTile + n; }
 

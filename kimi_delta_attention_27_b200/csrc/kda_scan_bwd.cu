@@ -526,7 +526,7 @@ BwdLayout bwd_layout(int64_t rows, int64_t n, int32_t H, int32_t G, int32_t P, i
     l.dbc = l.grads + round256(all);
     l.part = l.dbc + (l.splits > 1 ? round256(2 * static_cast<size_t>(l.splits) * rows * G * N * sizeof(float)) : 0);
     l.pieces = l.part + round256(cells * 3 * H * sizeof(float));
-    l.total = l.pieces + round256(scan_fwd_workspace_bytes(rows, n, H, P, N));
+    l.total = l.pieces + round256(scan_states_workspace_bytes(rows, n, H, P, N));
     return l;
 }
 

@@ -433,18 +433,31 @@ __global__ void __launch_bounds__(256) scan_join_kernel(ScanParams p, int64_t se
     }
 }
 
-// Tokens per piece; 0: whole sequences. A cut costs a second reading of x and B and one state per piece,
-// so it is made only where whole sequences leave SMs without work.
-int64_t piece_tokens(int64_t rows, int64_t n, int32_t H, int32_t P) {
-    const int64_t chains = n * H * (P / PC);
-    if (chains >= 4 * 148 || n == 0) return 0;
-    int64_t seg = rows * H * (P / PC) / (4 * 148);      // about four pieces for each SM
-    seg = (seg + T - 1) / T * T;
-    if (seg < 4 * T) seg = 4 * T;
+// Tokens per piece, a multiple of `tile`; 0: whole sequences. `ctas`: CTAs of one piece. A cut costs a second
+// reading of x and B and one state per piece, so it is made only where whole sequences leave SMs without work,
+// and into no more pieces than `want` CTAs need.
+int64_t piece_tokens(int64_t rows, int64_t n, int64_t ctas, int64_t want, int tile) {
+    if (n * ctas >= want || n == 0) return 0;
+    int64_t seg = (rows * ctas + want - 1) / want;
+    seg = (seg + tile - 1) / tile * tile;
+    if (seg < 256) seg = 256;
     return seg >= rows ? 0 : seg;
+}
+// the tcgen05 kernel: one CTA per SM, each with two runs of 64 columns
+int64_t tc_piece_tokens(int64_t rows, int64_t n, int32_t H, int32_t P) {
+    return piece_tokens(rows, n, (static_cast<int64_t>(H) * (P / PC) + 1) / 2, 2 * 148, kScanTcTile);
+}
+// the warp-level kernels: several CTAs per SM
+int64_t warp_piece_tokens(int64_t rows, int64_t n, int32_t H, int32_t P) {
+    return piece_tokens(rows, n, static_cast<int64_t>(H) * (P / PC), 4 * 148, T);
 }
 
 int64_t piece_count(int64_t rows, int64_t n, int64_t seg) { return seg ? rows / seg + n : n; }
+
+size_t piece_bytes(int64_t rows, int64_t n, int64_t seg, int32_t H, int32_t P, int32_t N) {
+    if (!seg) return 0;
+    return static_cast<size_t>(piece_count(rows, n, seg)) * H * (static_cast<size_t>(N) * P + 4) * sizeof(float);
+}
 
 template <int N, int S, bool kReverse>
 cudaError_t state_launch(const ScanParams &p, int64_t seg, int64_t units, const float *entering, float *leave,
@@ -470,38 +483,44 @@ constexpr int64_t kWhole = int64_t(1) << 60;   // one cell: pieces are whole seq
 }  // namespace scan
 
 size_t scan_fwd_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N) {
-    const int64_t seg = scan::piece_tokens(rows, n, H, P);
-    if (!seg) return 0;
-    return static_cast<size_t>(scan::piece_count(rows, n, seg)) * H * (static_cast<size_t>(N) * P + 4) * sizeof(float);
+    using namespace scan;
+    return piece_bytes(rows, n, N == 128 ? tc_piece_tokens(rows, n, H, P) : warp_piece_tokens(rows, n, H, P), H, P, N);
+}
+
+size_t scan_states_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N) {
+    return scan::piece_bytes(rows, n, scan::warp_piece_tokens(rows, n, H, P), H, P, N);
 }
 
 cudaError_t launch_scan_fwd(const ScanParams &p, cudaStream_t s) {
     using namespace scan;
-    const int64_t cut = piece_tokens(p.rows, p.seqs.n, p.H, p.P), seg = cut ? cut : kWhole;
-    const int64_t units = piece_count(p.rows, p.seqs.n, cut);
+    const bool tc = p.N == 128;
+    const int64_t cut = tc ? tc_piece_tokens(p.rows, p.seqs.n, p.H, p.P) : warp_piece_tokens(p.rows, p.seqs.n, p.H, p.P);
+    const int64_t seg = cut ? cut : kWhole, units = piece_count(p.rows, p.seqs.n, cut);
     if (units * p.H * (p.P / PC) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     float *ws = p.ws, *decay = ws ? ws + units * p.H * p.N * p.P : nullptr;
-    return by_state(p.N, [&](auto nn) {
-        constexpr int N = decltype(nn)::value;
-        const bool exact = p.hT && p.hT_fp32;
-        cudaError_t err = cudaSuccess;
-        if (cut) {
-            err = exact ? state_launch<N, 3, false>(p, seg, units, nullptr, ws, decay, nullptr, s)
-                        : state_launch<N, 2, false>(p, seg, units, nullptr, ws, decay, nullptr, s);
-            if (err == cudaSuccess) err = join_launch<false>(p, seg, ws, decay, s);
-        }
-        if (err != cudaSuccess) return err;
-        auto *k = exact ? scan_fwd_kernel<N, 3> : scan_fwd_kernel<N, 2>;
-        err = allow_smem(k, FwdSmem<N>::kBytes);
-        if (err != cudaSuccess) return err;
-        k<<<static_cast<unsigned>(units * p.H * (p.P / PC)), NT, FwdSmem<N>::kBytes, s>>>(p, seg, cut ? ws : nullptr);
-        return cudaGetLastError();
-    });
+    const bool exact = p.hT && p.hT_fp32;
+    cudaError_t err = cudaSuccess;
+    if (cut) {
+        if (tc)
+            err = launch_scan_tc(p, false, seg, units, nullptr, ws, decay, s);
+        else
+            err = exact ? state_launch<64, 3, false>(p, seg, units, nullptr, ws, decay, nullptr, s)
+                        : state_launch<64, 2, false>(p, seg, units, nullptr, ws, decay, nullptr, s);
+        if (err == cudaSuccess) err = join_launch<false>(p, seg, ws, decay, s);
+    }
+    if (err != cudaSuccess) return err;
+    const float *entering = cut ? ws : nullptr;
+    if (tc) return launch_scan_tc(p, true, seg, units, entering, nullptr, nullptr, s);
+    auto *k = exact ? scan_fwd_kernel<64, 3> : scan_fwd_kernel<64, 2>;
+    err = allow_smem(k, FwdSmem<64>::kBytes);
+    if (err != cudaSuccess) return err;
+    k<<<static_cast<unsigned>(units * p.H * (p.P / PC)), NT, FwdSmem<64>::kBytes, s>>>(p, seg, entering);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_scan_states(const ScanParams &p, bool reverse, float *states, float *ws, cudaStream_t s) {
     using namespace scan;
-    const int64_t cut = piece_tokens(p.rows, p.seqs.n, p.H, p.P), seg = cut ? cut : kWhole;
+    const int64_t cut = warp_piece_tokens(p.rows, p.seqs.n, p.H, p.P), seg = cut ? cut : kWhole;
     const int64_t units = piece_count(p.rows, p.seqs.n, cut);
     if (units == 0) return cudaSuccess;
     if (units * p.H * (p.P / PC) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

@@ -1,0 +1,709 @@
+// kda_scan_tc.cu -- selective state space scan over prompts on tcgen05, state size 128, sm_100a.
+//
+// The recurrence and its tile form are those of kda_scan_fwd.cu, with tiles of 128 tokens: 128 is the M of a
+// tcgen05 product and the number of TMEM lanes, so that C B^T, y and the state (rows: its 128 entries) each have
+// one row per lane and one thread per row. Per tile and 64 columns of a head:
+//
+//   G  = C B^T                              128 x 128, K 128     once for both heads of the CTA
+//   Y  = C S_0 (bf16 copy of the state)     128 x 64,  K 128     then scaled by e^Gamma, row by row
+//   Y += (L . G d) x                        128 x 64,  K 128     the first operand from TMEM, in bf16
+//   U  = B^T (d e^(Gamma_end - Gamma) x)    128 x 64,  K 128     the second operand in 2 or 3 bf16 parts
+//   S  = e^(Gamma_end) S_0 + U                                   fp32, in the registers of 128 threads
+//
+// What bounds it: the products take some 600 cycles per tile and head at the tensor cores' rate, HBM some
+// 1500 (34 KB), the work on elements (L . G, the parts of x, scaling and rounding) some 900 instructions of
+// each of 128 threads. So the element work is what has to be kept busy: two warpgroups take a head each (of the
+// same group, so that they share C, B and G), one thread issues the products, one warp runs ahead with
+// the gates and the loads of x. Nothing the warpgroups wait for depends on the state but Y's first product.
+//
+// L . G is formed without one exponential per element: with a_b = Gamma at the end of a block of 32 columns,
+// L_ts = e^(Gamma_t - a_b) e^(a_b - Gamma_s), a factor per row and one per column, both at most 1 for the
+// rows behind the block. In the block on the diagonal the row's factor is above 1; where the block decays by
+// more than 2^60 its elements take an exponential each instead.
+//
+// Every wait is bounded; one that runs out raises kErrTimeout and winds the CTA down.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <string.h>
+
+#include "kda_scan.cuh"
+#include "sm100_ptx.cuh"
+
+namespace kda {
+namespace scan {
+namespace tc {
+
+using namespace ptx;
+
+__device__ unsigned int g_scan_tc_error = 0;
+
+constexpr int N = 128;                    // state size
+constexpr int TT = kScanTcTile;           // tokens per tile
+constexpr int NT = 320;                   // two warpgroups, an issuing warp, a gates warp
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+struct TcGates {
+    float hi[TT], lo[TT];   // log2 of the decay from the tile's start through token t, in two floats
+    float d[TT];            // the steps
+    float col[TT];          // d e^(a_b - Gamma): the column factors of L . G d
+    float from[TT];         // e^Gamma
+    float weight[TT];       // d e^(Gamma_end - Gamma)
+    float total;
+    uint32_t steep;         // bit b: block b of 32 decays by more than 2^60
+    float pad[2];
+};
+
+constexpr uint32_t kBlock = 16384;        // 128 rows of 128 bytes: 64 bf16 columns
+template <int S>
+struct Smem {
+    static constexpr uint32_t kC = 0, kB = 2 * kBlock, kX = 4 * kBlock;    // x: [head][stage]
+    static constexpr uint32_t kState = kX + 4 * kBlock;                    // [head]: the state in bf16
+    static constexpr uint32_t kPart = 64 * 128;                            // 64 tokens of one part
+    static constexpr uint32_t kParts = kState + 2 * kBlock;                // [head][S]
+    static constexpr uint32_t kGates = kParts + 2 * S * kPart;             // [head][stage]
+    static constexpr uint32_t kBars = kGates + 4 * sizeof(TcGates);
+    static constexpr uint32_t kBytes = kBars + 512;
+    static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
+};
+
+// TMEM columns: G, then per head M (L . G d in bf16 pairs), Y, U
+constexpr uint32_t kColG = 0, kColM = 128, kColY = 192, kColU = 256, kColHead = 192, kCols = 512;
+
+constexpr uint32_t kIdG = idesc_f16(128, 128, 1, 0, 0);   // C and B, both K-major
+constexpr uint32_t kIdY = idesc_f16(128, 64, 1, 0, 1);    // C or M K-major, state copy or x MN-major
+constexpr uint32_t kIdU = idesc_f16(128, 64, 1, 1, 1);    // B^T and the parts of x, both MN-major
+
+struct Maps {
+    CUtensorMap x, b, c;
+};
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float f32(uint32_t u) { return __uint_as_float(u); }
+__device__ __forceinline__ uint32_t sw128(int r, int j) { return static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4)); }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// barriers, 8 bytes each behind Smem::kBars
+enum : int {
+    kBcFull = 0,        // C and B of a tile (state run: [stage], B alone)
+    kG = 2,             // G is there
+    kXFull = 3,         // [head][stage] x
+    kGates = 7,         // [head][stage] the gates
+    kXFree = 11,        // [head][stage] the warpgroup is done with the tile's x and gates
+    kS = 15,            // [head] the state's copy is written
+    kY1 = 17,           // [head] C S_0
+    kYFree = 19,        // [head] Y has been read
+    kP0 = 21, kP1 = 23, // [head] the parts of the tile's first, second 64 tokens are written
+    kPFree = 25,        // [head] the first half's product is done
+    kU = 27,            // [head] U is there
+    kM = 29,            // [head] M is written, Y scaled
+    kY = 31,            // [head] Y is there
+    kBarCount = 33
+};
+
+struct Ctx {
+    uint32_t bars;
+    volatile uint32_t *abort;
+    __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * i; }
+    // false: this or another wait of the CTA ran out
+    __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
+        if (mbar_try_wait(bar(i), parity)) return true;
+        const uint64_t t0 = globaltimer();
+        for (;;) {
+            if (mbar_try_wait(bar(i), parity)) return true;
+            if (*abort) return false;
+            if (globaltimer() - t0 > kWaitLimitNs) {
+                *abort = 1;
+                atomicOr(&g_scan_tc_error, kErrTimeout);
+                return false;
+            }
+        }
+    }
+    __device__ __forceinline__ void arrive(int i) const { mbar_arrive(bar(i)); }
+};
+
+// The gates of a tile, by one warp: lane l has tokens 4l .. 4l + 3. Returns log2 of the tile's decay.
+__device__ __forceinline__ double make_tc_gates(TcGates &g, const ScanParams &p, int64_t start, int cnt, int h) {
+    const int lane = threadIdx.x & 31;
+    const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+    const double a = p.A[h];
+    float d[4];
+    double c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int t = 4 * lane + j;
+        float u;
+        d[j] = t < cnt ? step_of(p.dt[(start + t) * p.H + h], bias, p.softplus, &u) : 0.f;
+        c[j] = fmax(d[j] * a, kMinLog) * kLog2e + (j ? c[j - 1] : 0.0);
+    }
+    double s = c[3];
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, s, k);
+        if (lane >= k) s += o;
+    }
+    const double before = s - c[3];
+    const double total = __shfl_sync(0xffffffffu, s, 31);
+    const double anchor = __shfl_sync(0xffffffffu, s, lane | 7);                        // the block's end
+    const double opens = __shfl_sync(0xffffffffu, before, lane & 24);                   // and its start
+    const unsigned steep = __ballot_sync(0xffffffffu, opens - anchor > 60.0);
+    float hi[4], lo[4], col[4], from[4], weight[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const double v = before + c[j];
+        hi[j] = static_cast<float>(v);
+        lo[j] = static_cast<float>(v - hi[j]);
+        col[j] = d[j] * ex2(static_cast<float>(anchor - v));
+        from[j] = ex2(hi[j]) * fmaf(lo[j], kLn2, 1.f);
+        weight[j] = d[j] * ex2(static_cast<float>(total - v));
+    }
+    reinterpret_cast<float4 *>(g.hi)[lane] = make_float4(hi[0], hi[1], hi[2], hi[3]);
+    reinterpret_cast<float4 *>(g.lo)[lane] = make_float4(lo[0], lo[1], lo[2], lo[3]);
+    reinterpret_cast<float4 *>(g.d)[lane] = make_float4(d[0], d[1], d[2], d[3]);
+    reinterpret_cast<float4 *>(g.col)[lane] = make_float4(col[0], col[1], col[2], col[3]);
+    reinterpret_cast<float4 *>(g.from)[lane] = make_float4(from[0], from[1], from[2], from[3]);
+    reinterpret_cast<float4 *>(g.weight)[lane] = make_float4(weight[0], weight[1], weight[2], weight[3]);
+    if (lane == 0) {
+        g.total = ex2(static_cast<float>(total));
+        g.steep = (steep & 1u) | ((steep >> 7) & 2u) | ((steep >> 14) & 4u) | ((steep >> 21) & 8u);
+    }
+    return total;
+}
+
+// kOut: the outputs and the final state. Otherwise the state that a piece adds, from zero (leave, and its decay).
+template <bool kOut, int S>
+__global__ void __launch_bounds__(NT, 1)
+    scan_tc_kernel(ScanParams p, const __grid_constant__ Maps maps, int64_t seg, const float *entering, float *leave,
+                   float *leave_decay) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    using L = Smem<S>;
+    const uint32_t base = smem_u32(smem);
+    __shared__ uint32_t s_tmem, s_abort;
+    Ctx x;
+    x.bars = base + L::kBars;
+    x.abort = &s_abort;
+    TcGates *gates = reinterpret_cast<TcGates *>(smem + L::kGates);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (blockIdx.x == 0) check_offsets(p.seqs, &g_scan_tc_error);
+
+    // the CTA's piece and its one or two heads ("heads" here: runs of 64 columns of x, of one group)
+    const int slices = p.P / PC, per_group = p.H / p.G * slices, pairs = (per_group + 1) / 2;
+    const int64_t unit = blockIdx.x / (p.G * pairs);
+    const int gp = static_cast<int>(blockIdx.x % (p.G * pairs)), grp = gp / pairs, in_group = gp % pairs * 2;
+    const int v0 = grp * per_group + in_group, heads = in_group + 1 < per_group ? 2 : 1;
+    const Piece u = find_piece(p.seqs, unit, seg);
+    if (u.none || (!kOut && u.last)) return;
+    const int64_t c_first = u.a / TT;
+    const int tiles = static_cast<int>(u.b > u.a ? (u.b + TT - 1) / TT - c_first : 0);
+    auto start_of = [&](int i) { return (c_first + i) * TT > u.a ? (c_first + i) * TT : u.a; };
+    auto count_of = [&](int i) {
+        const int64_t e = (c_first + i + 1) * TT < u.b ? (c_first + i + 1) * TT : u.b;
+        return static_cast<int>(e - start_of(i));
+    };
+
+    if (warp == 8) {
+        if (lane == 0) {
+            for (int i = 0; i < kBarCount; ++i) {
+                const bool by_group = (i >= kXFree && i < kY1) || (i >= kYFree && i < kPFree) || (i >= kM && i < kY);
+                mbar_init(x.bar(i), by_group ? 128 : 1);
+            }
+            s_abort = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
+        tmem_alloc(smem_u32(&s_tmem), kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const uint32_t bc_bytes = kOut ? 4 * kBlock : 2 * kBlock;
+
+    if (warp < 8) {
+        // ---------------------------------------------------------------- a head's elements
+        const int hd = warp >> 2, r = tid & 127, wq = warp & 3;          // r: row (token or state entry), TMEM lane
+        if (hd < heads) {
+            const int v = v0 + hd, h = v / slices, col = v % slices * PC;
+            const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+            const uint32_t tM = tmem + kColM + hd * kColHead + lanes, tY = tmem + kColY + hd * kColHead + lanes;
+            const uint32_t tU = tmem + kColU + hd * kColHead + lanes, tG = tmem + kColG + lanes;
+            const uint32_t st = base + L::kState + hd * kBlock, parts = base + L::kParts + hd * S * L::kPart;
+            const int64_t sn = static_cast<int64_t>(N) * p.P;
+            const float Dh = p.D ? p.D[h] : 0.f;
+            float2 s[PC / 2];     // row r of the state
+            {
+                const void *src = kOut && !entering ? p.h0 : entering;
+                const bool fp32 = !(kOut && !entering) || p.h0_fp32;
+                const int64_t e = ((kOut && !entering ? static_cast<int64_t>(u.i) : unit) * p.H + h) * sn +
+                                  static_cast<int64_t>(r) * p.P + col;
+#pragma unroll
+                for (int j = 0; j < PC / 4; ++j) {
+                    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (src && fp32) {
+                        f = reinterpret_cast<const float4 *>(static_cast<const float *>(src) + e)[j];
+                    } else if (src) {
+                        const uint2 w = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(src) + e)[j];
+                        f = make_float4(bf_low(w.x), bf_high(w.x), bf_low(w.y), bf_high(w.y));
+                    }
+                    s[2 * j] = make_float2(f.x, f.y);
+                    s[2 * j + 1] = make_float2(f.z, f.w);
+                }
+            }
+            auto publish = [&]() {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    sts128(st + sw128(r, j), make_uint4(bf_pair(s[4 * j].x, s[4 * j].y), bf_pair(s[4 * j + 1].x, s[4 * j + 1].y),
+                                                        bf_pair(s[4 * j + 2].x, s[4 * j + 2].y),
+                                                        bf_pair(s[4 * j + 3].x, s[4 * j + 3].y)));
+                fence_proxy_async_smem();
+                x.arrive(kS + hd);
+            };
+            bool ok = true;
+            if (kOut && tiles > 0) {
+                // the blocks of M above the diagonal stay zero
+                const uint32_t zero[16] = {};
+                for (int b = wq + 1; b < 4; ++b) tmem_st16(tM + 16 * b, zero);
+                tmem_wait_st();
+                publish();
+            }
+            for (int i = 0; i < tiles && ok; ++i) {
+                const int stage = i & 1, cnt = count_of(i);
+                const uint32_t ph = i & 1, ph2 = (i >> 1) & 1;
+                const uint32_t xt = base + L::kX + (hd * 2 + stage) * kBlock;
+                const TcGates &g = gates[hd * 2 + stage];
+                ok = x.wait(kXFull + hd * 2 + stage, ph2) && x.wait(kGates + hd * 2 + stage, ph2);
+                if (!ok) break;
+                if (cnt < TT && hd == 0) {
+                    // rows of B behind the sequence: whatever they hold would multiply zeros below
+                    ok = x.wait(kOut ? kBcFull : kBcFull + stage, kOut ? ph : ph2);
+                    if (!ok) break;
+                    const uint32_t bt = base + (kOut || stage == 0 ? L::kB : L::kC);
+                    if (r >= cnt)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            sts128(bt + (j >> 3) * kBlock + r * 128 + (j & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
+                }
+                // d e^(Gamma_end - Gamma) x of 64 tokens in bf16 parts; two threads per token
+                auto write_parts = [&](int half) {
+                    const int row = half * 64 + (r >> 1);
+                    const float w = g.weight[row];
+                    const float2 w2 = make_float2(w, w), minus = make_float2(-1.f, -1.f);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int chunk = (r & 1) * 4 + j;
+                        uint4 part[S];
+                        if (row < cnt) {
+                            const uint4 q = lds128(xt + sw128(row, chunk));
+                            const uint32_t in[4] = {q.x, q.y, q.z, q.w};
+                            uint32_t o[S][4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float2 f = mul2(make_float2(bf_low(in[k]), bf_high(in[k])), w2);
+#pragma unroll
+                                for (int e = 0; e < S; ++e) {
+                                    o[e][k] = bf_pair(f.x, f.y);
+                                    if (e + 1 < S) f = fma2(make_float2(bf_low(o[e][k]), bf_high(o[e][k])), minus, f);
+                                }
+                            }
+#pragma unroll
+                            for (int e = 0; e < S; ++e) part[e] = make_uint4(o[e][0], o[e][1], o[e][2], o[e][3]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < S; ++e) part[e] = make_uint4(0u, 0u, 0u, 0u);
+                            sts128(xt + sw128(row, chunk), make_uint4(0u, 0u, 0u, 0u));
+                        }
+#pragma unroll
+                        for (int e = 0; e < S; ++e) sts128(parts + e * L::kPart + sw128(r >> 1, chunk), part[e]);
+                    }
+                    fence_proxy_async_smem();
+                    x.arrive((half ? kP1 : kP0) + hd);
+                };
+                write_parts(0);
+                if (kOut) {
+                    // Y = C S_0, scaled
+                    ok = x.wait(kY1 + hd, ph);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float2 f = make_float2(g.from[r], g.from[r]);
+                    uint32_t a[32], b[32];
+                    tmem_ld32(tY, a);
+                    tmem_ld32(tY + 32, b);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 q = mul2(make_float2(f32(a[j]), f32(a[j + 1])), f);
+                        a[j] = __float_as_uint(q.x);
+                        a[j + 1] = __float_as_uint(q.y);
+                        const float2 q2 = mul2(make_float2(f32(b[j]), f32(b[j + 1])), f);
+                        b[j] = __float_as_uint(q2.x);
+                        b[j + 1] = __float_as_uint(q2.y);
+                    }
+                    tmem_st32(tY, a);
+                    tmem_st32(tY + 32, b);
+                }
+                ok = x.wait(kPFree + hd, ph);
+                if (!ok) break;
+                write_parts(1);
+                if (kOut) {
+                    // M = L . G d, rows r, blocks of 32 columns up to the diagonal
+                    ok = x.wait(kG, ph);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float gh = g.hi[r], glo = g.lo[r];
+                    for (int b = 0; b <= wq; ++b) {
+                        uint32_t a[32], o[16];
+                        tmem_ld32(tG + 32 * b, a);
+                        const int e = 32 * b + 31;
+                        if (b < wq || !((g.steep >> b) & 1u)) {
+                            const float rf = ex2((gh - g.hi[e]) + (glo - g.lo[e]));
+                            const float2 rf2 = make_float2(rf, rf);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float4 cf = reinterpret_cast<const float4 *>(g.col + 32 * b)[j];
+                                const float2 m0 = mul2(mul2(make_float2(f32(a[4 * j]), f32(a[4 * j + 1])),
+                                                            make_float2(cf.x, cf.y)), rf2);
+                                const float2 m1 = mul2(mul2(make_float2(f32(a[4 * j + 2]), f32(a[4 * j + 3])),
+                                                            make_float2(cf.z, cf.w)), rf2);
+                                if (b < wq) {
+                                    o[2 * j] = bf_pair(m0.x, m0.y);
+                                    o[2 * j + 1] = bf_pair(m1.x, m1.y);
+                                } else {
+                                    // selected, not multiplied: above the diagonal is what later tokens hold
+                                    o[2 * j] = bf_pair(4 * j <= lane ? m0.x : 0.f, 4 * j + 1 <= lane ? m0.y : 0.f);
+                                    o[2 * j + 1] = bf_pair(4 * j + 2 <= lane ? m1.x : 0.f, 4 * j + 3 <= lane ? m1.y : 0.f);
+                                }
+                            }
+                        } else {
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                float m[2];
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const int sc = 32 * b + 2 * j + k;
+                                    const float q = f32(a[2 * j + k]) * g.d[sc] *
+                                                    ex2(fminf((gh - g.hi[sc]) + (glo - g.lo[sc]), 0.f));
+                                    m[k] = 2 * j + k <= lane ? q : 0.f;
+                                }
+                                o[j] = bf_pair(m[0], m[1]);
+                            }
+                        }
+                        tmem_st16(tM + 16 * b, o);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    x.arrive(kM + hd);
+                }
+                // S = e^(Gamma_end) S + U
+                ok = x.wait(kU + hd, ph);
+                if (!ok) break;
+                tc_fence_after();
+                {
+                    const float2 tot = make_float2(g.total, g.total);
+                    uint32_t a[32];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        tmem_ld32(tU + 32 * q, a);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            s[16 * q + j] = fma2(s[16 * q + j], tot, make_float2(f32(a[2 * j]), f32(a[2 * j + 1])));
+                    }
+                    tc_fence_before();
+                }
+                if (kOut) {
+                    if (i + 1 < tiles) publish();
+                    // the outputs: Y + D x, by way of x's own rows in shared memory
+                    ok = x.wait(kY + hd, ph);
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint32_t a[32], b[32];
+                    tmem_ld32(tY, a);
+                    tmem_ld32(tY + 32, b);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    x.arrive(kYFree + hd);
+                    const float2 D2 = make_float2(Dh, Dh);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint4 q = lds128(xt + sw128(r, j));
+                        const uint32_t in[4] = {q.x, q.y, q.z, q.w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int e = (8 * j + 2 * k) & 31;
+                            const float2 y = j < 4 ? make_float2(f32(a[e]), f32(a[e + 1])) : make_float2(f32(b[e]), f32(b[e + 1]));
+                            const float2 z = fma2(make_float2(bf_low(in[k]), bf_high(in[k])), D2, y);
+                            o[k] = bf_pair(z.x, z.y);
+                        }
+                        sts128(xt + sw128(r, j), make_uint4(o[0], o[1], o[2], o[3]));
+                    }
+                    named_bar_sync(1 + hd, 128);
+                    const int64_t at_out = start_of(i) * p.out_stride + static_cast<int64_t>(v) * PC;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int row = j * 16 + (r >> 3);
+                        if (row < cnt)
+                            *reinterpret_cast<uint4 *>(p.out + at_out + row * p.out_stride + (r & 7) * 8) =
+                                lds128(xt + sw128(row, r & 7));
+                    }
+                    fence_proxy_async_smem();   // x's next load comes after these reads and writes
+                }
+                x.arrive(kXFree + hd * 2 + stage);
+            }
+            // the state that leaves
+            void *dst = kOut ? (u.last ? p.hT : nullptr) : leave;
+            if (ok && dst) {
+                const bool fp32 = !kOut || p.hT_fp32;
+                const int64_t e = ((kOut ? static_cast<int64_t>(u.i) : unit) * p.H + h) * sn + static_cast<int64_t>(r) * p.P + col;
+#pragma unroll
+                for (int j = 0; j < PC / 4; ++j) {
+                    if (fp32)
+                        reinterpret_cast<float4 *>(static_cast<float *>(dst) + e)[j] =
+                            make_float4(s[2 * j].x, s[2 * j].y, s[2 * j + 1].x, s[2 * j + 1].y);
+                    else
+                        reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dst) + e)[j] =
+                            make_uint2(bf_pair(s[2 * j].x, s[2 * j].y), bf_pair(s[2 * j + 1].x, s[2 * j + 1].y));
+                }
+            }
+        }
+    } else if (warp == 8) {
+        // ---------------------------------------------------------------- loads of C and B, and the products
+        const int bcol = grp * N;
+        auto load_bc = [&](int i) {
+            if (!elect_one()) return;
+            const int bar = kOut ? kBcFull : kBcFull + (i & 1);
+            const int32_t row = static_cast<int32_t>(start_of(i));
+            mbar_arrive_expect_tx(x.bar(bar), bc_bytes);
+            const uint32_t bt = base + (kOut || (i & 1) == 0 ? L::kB : L::kC);
+            for (int k = 0; k < 2; ++k) {
+                if (kOut) tma_load_2d(base + L::kC + k * kBlock, &maps.c, x.bar(bar), bcol + 64 * k, row);
+                tma_load_2d(bt + k * kBlock, &maps.b, x.bar(bar), bcol + 64 * k, row);
+            }
+        };
+        bool ok = true;
+        if (tiles > 0) load_bc(0);
+        if (!kOut && tiles > 1) load_bc(1);
+        for (int i = 0; i < tiles && ok; ++i) {
+            const uint32_t ph = i & 1, ph2 = (i >> 1) & 1;
+            const uint32_t bt = base + (kOut || ph == 0 ? L::kB : L::kC);
+            ok = x.wait(kOut ? kBcFull : kBcFull + static_cast<int>(ph), kOut ? ph : ph2);
+            if (!ok) break;
+            __syncwarp();
+            if (kOut) {
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t o = (k >> 2) * kBlock + (k & 3) * 32;
+                        mma_f16(tmem + kColG, smem_desc(base + L::kC + o, 16, 1024, kSwizzle128),
+                                smem_desc(bt + o, 16, 1024, kSwizzle128), kIdG, k > 0);
+                    }
+                    mma_commit(x.bar(kG));
+                }
+                __syncwarp();
+                for (int hd = 0; hd < heads && ok; ++hd) {
+                    ok = x.wait(kS + hd, ph) && (i == 0 || x.wait(kYFree + hd, (i - 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_f16(tmem + kColY + hd * kColHead,
+                                    smem_desc(base + L::kC + (k >> 2) * kBlock + (k & 3) * 32, 16, 1024, kSwizzle128),
+                                    smem_desc(base + L::kState + hd * kBlock + k * 2048, kBlock, 1024, kSwizzle128), kIdY,
+                                    k > 0);
+                        mma_commit(x.bar(kY1 + hd));
+                    }
+                    __syncwarp();
+                }
+            }
+            for (int half = 0; half < 2 && ok; ++half)
+                for (int hd = 0; hd < heads && ok; ++hd) {
+                    ok = x.wait((half ? kP1 : kP0) + hd, ph);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t parts = base + L::kParts + hd * S * L::kPart;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int e = S - 1; e >= 0; --e)
+                                mma_f16(tmem + kColU + hd * kColHead,
+                                        smem_desc(bt + (half * 4 + k) * 2048, kBlock, 1024, kSwizzle128),
+                                        smem_desc(parts + e * L::kPart + k * 2048, kBlock, 1024, kSwizzle128), kIdU,
+                                        !(half == 0 && k == 0 && e == S - 1));
+                        mma_commit(x.bar((half ? kU : kPFree) + hd));
+                    }
+                    __syncwarp();
+                }
+            if (!ok) break;
+            // the last commit covers every product so far: C and B are free
+            const int next = kOut ? i + 1 : i + 2;
+            if (next < tiles) {
+                ok = x.wait(kU + heads - 1, ph);
+                if (!ok) break;
+                __syncwarp();
+                load_bc(next);
+                __syncwarp();
+            }
+            if (kOut) {
+                for (int hd = 0; hd < heads && ok; ++hd) {
+                    ok = x.wait(kM + hd, ph);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t xt = base + L::kX + (hd * 2 + (i & 1)) * kBlock;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_f16_ts(tmem + kColY + hd * kColHead, tmem + kColM + hd * kColHead + 8 * k,
+                                       smem_desc(xt + k * 2048, kBlock, 1024, kSwizzle128), kIdY, 1);
+                        mma_commit(x.bar(kY + hd));
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- x and the gates, up to two tiles ahead
+        bool ok = true;
+        double decay[2] = {0.0, 0.0};
+        for (int i = 0; i < tiles && ok; ++i) {
+            const int stage = i & 1;
+            for (int hd = 0; hd < heads && ok; ++hd) {
+                const int v = v0 + hd;
+                if (i >= 2) ok = x.wait(kXFree + hd * 2 + stage, ((i - 2) >> 1) & 1);
+                if (!ok) break;
+                __syncwarp();
+                if (elect_one()) {
+                    const int bar = kXFull + hd * 2 + stage;
+                    mbar_arrive_expect_tx(x.bar(bar), kBlock);
+                    tma_load_2d(base + L::kX + (hd * 2 + stage) * kBlock, &maps.x, x.bar(bar), v * PC,
+                                static_cast<int32_t>(start_of(i)));
+                }
+                __syncwarp();
+                decay[hd] += make_tc_gates(gates[hd * 2 + stage], p, start_of(i), count_of(i), v / slices);
+                __syncwarp();
+                if (lane == 0) x.arrive(kGates + hd * 2 + stage);
+            }
+        }
+        if (!kOut && ok && lane == 0)
+            for (int hd = 0; hd < heads; ++hd)
+                if ((v0 + hd) % slices == 0)
+                    leave_decay[unit * p.H + (v0 + hd) / slices] = ex2(static_cast<float>(decay[hd]));
+    }
+    if (s_abort) {
+        // copies may still be in flight into this CTA's shared memory
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 20000000ull) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, kCols);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }();
+    return fn;
+}
+
+// rows of `cols` bf16 elements, `stride` apart, in boxes of 128 rows x 64 columns (one swizzled block)
+bool encode(CUtensorMap *map, const void *at, int64_t cols, int64_t rows, int64_t stride) {
+    auto enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows > 1 ? stride : cols) * 2};
+    const cuuint32_t box[2] = {64, TT}, step[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(at), dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kOut, int S>
+cudaError_t launch(const ScanParams &p, int64_t seg, int64_t units, const float *entering, float *leave, float *decay,
+                   cudaStream_t s) {
+    Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    if (p.rows > 0 && (!encode(&maps.x, p.x, static_cast<int64_t>(p.H) * p.P, p.rows, p.x_stride) ||
+                       !encode(&maps.b, p.B, static_cast<int64_t>(p.G) * N, p.rows, p.b_stride) ||
+                       !encode(&maps.c, p.C, static_cast<int64_t>(p.G) * N, p.rows, p.c_stride)))
+        return cudaErrorInvalidValue;
+    auto *k = scan_tc_kernel<kOut, S>;
+    cudaError_t err = allow_smem(k, Smem<S>::kBytes);
+    if (err != cudaSuccess) return err;
+    const int64_t pairs = (p.H / p.G * (p.P / PC) + 1) / 2;
+    k<<<static_cast<unsigned>(units * p.G * pairs), NT, Smem<S>::kBytes, s>>>(p, maps, seg, entering, leave, decay);
+    return cudaGetLastError();
+}
+
+}  // namespace tc
+}  // namespace scan
+
+cudaError_t launch_scan_tc(const ScanParams &p, bool out, int64_t seg, int64_t units, const float *entering, float *leave,
+                           float *decay, cudaStream_t s) {
+    using namespace scan::tc;
+    if (p.hT && p.hT_fp32)
+        return out ? launch<true, 3>(p, seg, units, entering, leave, decay, s)
+                   : launch<false, 3>(p, seg, units, entering, leave, decay, s);
+    return out ? launch<true, 2>(p, seg, units, entering, leave, decay, s)
+               : launch<false, 2>(p, seg, units, entering, leave, decay, s);
+}
+
+cudaError_t read_and_clear_scan_tc_error(unsigned int *value) {
+    cudaError_t err = cudaMemcpyFromSymbol(value, scan::tc::g_scan_tc_error, sizeof(*value));
+    if (err != cudaSuccess || *value == 0) return err;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(scan::tc::g_scan_tc_error, &zero, sizeof(zero));
+}
+
+}  // namespace kda
