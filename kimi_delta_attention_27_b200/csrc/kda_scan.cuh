@@ -9,10 +9,9 @@ namespace scan {
 constexpr int T = kScanTile;      // tokens per tile
 constexpr int PC = 64;            // head channels per CTA (the columns of the state do not mix)
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr double kLog2e = 1.4426950408889634;
-// A step whose log decay is below this leaves nothing of the state even in 64 bits; the floor keeps
-// sums of log decays exact enough where one step of a tile decays by 10^30.
-constexpr double kMinLog = -1000.0;
+constexpr float kLog2eHi = 1.44269502f, kLog2eLo = static_cast<float>(1.4426950408889634 - 1.44269502162933349609375);
+constexpr float kMinLog2 = -1442.695f;   // log2(e^-1000)
+constexpr float kMinLog = -1000.f;
 
 __device__ __forceinline__ float ex2(float y) {
     float r;
@@ -26,9 +25,49 @@ __device__ __forceinline__ float step_of(float dt, float bias, int softplus, flo
     return softplus ? fmaxf(*u, 0.f) + log1pf(expf(-fabsf(*u))) : *u;
 }
 
-// A tile's gates, in powers of two. The sums run in 64 bits and are kept as two floats (hi + lo): the
-// difference of two of them, which is what the kernels exponentiate, then has the relative error of one
-// 32-bit rounding however large the sums are.
+// Sums of log decays are kept as two floats hi + lo (about 48 bits), added by error-free sums: the difference
+// of two of them, which is what the kernels exponentiate, then has the relative error of one 32-bit
+// rounding however large the sums are. (In fp64 the same sums took three quarters of a tile's time.)
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
+    const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t));
+    const float l = __fadd_rn(e, __fadd_rn(a.lo, b.lo));
+    const float hi = __fadd_rn(s, l);
+    return {hi, __fsub_rn(l, __fsub_rn(hi, s))};
+}
+__device__ __forceinline__ float minus(Two a, Two b) { return (a.hi - b.hi) + (a.lo - b.lo); }
+__device__ __forceinline__ Two shfl(Two v, int from) {
+    return {__shfl_sync(0xffffffffu, v.hi, from), __shfl_sync(0xffffffffu, v.lo, from)};
+}
+// the sums over lanes 0 .. l
+__device__ __forceinline__ Two scan_lanes(Two v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const Two o = {__shfl_up_sync(0xffffffffu, v.hi, k), __shfl_up_sync(0xffffffffu, v.lo, k)};
+        const Two w = o + v;
+        if (lane >= k) v = w;
+    }
+    return v;
+}
+// log2 of a step's decay, d A log2(e). A step whose decay is below e^-1000 leaves nothing of the state even in
+// 64 bits; the floor keeps the sums exact enough where one step of a tile decays by 10^30.
+__device__ __forceinline__ Two log_decay(float d, Two a2) {
+    const float hi = d * a2.hi, lo = fmaf(d, a2.hi, -hi) + d * a2.lo;
+    return hi > kMinLog2 ? Two{hi, lo} : Two{kMinLog2, 0.f};
+}
+// A log2(e) to two floats
+__device__ __forceinline__ Two log2_rate(float A) {
+    const float hi = A * kLog2eHi;
+    return {hi, fmaf(A, kLog2eHi, -hi) + A * kLog2eLo};
+}
+// 2^v
+__device__ __forceinline__ float ex2(Two v) { return ex2(v.hi) * fmaf(v.lo, kLn2, 1.f); }
+
+// A tile's gates, in powers of two.
 struct Gates {
     float hi[T], lo[T];   // log2 of the decay from the tile's start through token t
     float d[T];           // the steps
@@ -41,30 +80,26 @@ struct Gates {
 
 // By one warp: lane l has tokens 2l and 2l + 1 (steps d0, d1; 0 behind the tile's last token). Returns
 // log2 of the tile's decay.
-__device__ __forceinline__ double make_gates(Gates &g, float d0, float d1, float A) {
+__device__ __forceinline__ Two make_gates(Gates &g, float d0, float d1, float A) {
     const int lane = threadIdx.x & 31;
-    const double a = A;
-    const double l0 = fmax(d0 * a, kMinLog) * kLog2e, l1 = fmax(d1 * a, kMinLog) * kLog2e;
-    double s = l0 + l1;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, s, k);
-        if (lane >= k) s += o;
-    }
-    const double total = __shfl_sync(0xffffffffu, s, 31);
-    const double c[2] = {s - l1, s};
+    const Two a2 = log2_rate(A), l0 = log_decay(d0, a2), l1 = log_decay(d1, a2);
+    const Two s = scan_lanes(l0 + l1), total = shfl(s, 31);
+    // through the lane's first token: the sum through the lane before, and its own
+    const Two before = {__shfl_up_sync(0xffffffffu, s.hi, 1), __shfl_up_sync(0xffffffffu, s.lo, 1)};
+    const Two c[2] = {lane ? before + l0 : l0, s};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int t = 2 * lane + j;
-        const float hi = static_cast<float>(c[j]), lo = static_cast<float>(c[j] - hi);
-        g.hi[t] = hi;
-        g.lo[t] = lo;
-        g.d[t] = j ? d1 : d0;
-        g.from[t] = ex2(hi) * fmaf(lo, kLn2, 1.f);
-        g.to[t] = ex2(static_cast<float>(total - c[j]));
-        g.weight[t] = g.d[t] * g.to[t];
+        const float d = j ? d1 : d0;
+        g.hi[t] = c[j].hi;
+        g.lo[t] = c[j].lo;
+        g.d[t] = d;
+        g.from[t] = ex2(c[j]);
+        const float to = ex2(minus(total, c[j]));
+        g.to[t] = to;
+        g.weight[t] = d * to;
     }
-    if (lane == 0) g.total = ex2(static_cast<float>(total));
+    if (lane == 0) g.total = ex2(total);
     return total;
 }
 

@@ -350,14 +350,14 @@ __global__ void __launch_bounds__(NT, 3) scan_state_kernel(ScanParams p, int64_t
         load_tile<PC * 2, NT>(d + kR, cols + s * cstr, cstr, cnt);
         cp_async_commit();
     };
-    double decay = 0.0;
+    Two decay = {0.f, 0.f};
     float d0 = 0.f, d1 = 0.f;
     const bool gate_warp = warp == static_cast<int>(blockIdx.x & 3);
     if (n_tiles > 0) {
         fetch(cell(0), 0);
         if (gate_warp) {
             load_steps(p, tile_start(u, cell(0)), tile_count(u, cell(0)), h, d0, d1);
-            decay += make_gates(gates[0], d0, d1, A);
+            decay = decay + make_gates(gates[0], d0, d1, A);
             if (n_tiles > 1) load_steps(p, tile_start(u, cell(1)), tile_count(u, cell(1)), h, d0, d1);
         }
     }
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(NT, 3) scan_state_kernel(ScanParams p, int64_t
         __syncthreads();
         if (k + 1 < n_tiles) fetch(cell(k + 1), stage ^ 1);
         if (gate_warp && k + 1 < n_tiles) {
-            decay += make_gates(gates[(k + 1) & 1], d0, d1, A);
+            decay = decay + make_gates(gates[(k + 1) & 1], d0, d1, A);
             if (k + 2 < n_tiles) load_steps(p, tile_start(u, cell(k + 2)), tile_count(u, cell(k + 2)), h, d0, d1);
         }
         if (states)
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(NT, 3) scan_state_kernel(ScanParams p, int64_t
     }
     if (leave) {
         write_state<MT>(acc, leave, (unit * p.H + h) * sn + col, true, p.P, n0);
-        if (gate_warp && lane == 0 && col == 0) leave_decay[unit * p.H + h] = ex2(static_cast<float>(decay));
+        if (gate_warp && lane == 0 && col == 0) leave_decay[unit * p.H + h] = ex2(decay);
     } else if (kReverse && tail && p.dh0) {
         write_state<MT>(acc, p.dh0, at_seq, true, p.P, n0);
     }

@@ -5,16 +5,18 @@
 // one row per lane and one thread per row. Per tile and 64 columns of a head:
 //
 //   G  = C B^T                              128 x 128, K 128     once for both heads of the CTA
-//   Y  = C S_0 (bf16 copy of the state)     128 x 64,  K 128     then scaled by e^Gamma, row by row
-//   Y += (L . G d) x                        128 x 64,  K 128     the first operand from TMEM, in bf16
+//   Y1 = C S_0 (bf16 copy of the state)     128 x 64,  K 128     y = e^Gamma Y1 + Y2 + D x
+//   Y2 = (L . G d) x                        128 x 64,  K 128     the first operand from TMEM, in bf16
 //   U  = B^T (d e^(Gamma_end - Gamma) x)    128 x 64,  K 128     the second operand in 2 or 3 bf16 parts
-//   S  = e^(Gamma_end) S_0 + U                                   fp32, in the registers of 128 threads
+//   S  = e^(Gamma_end) S_0 + U                                   fp32, in the registers of 256 threads
 //
 // What bounds it: the products take some 600 cycles per tile and head at the tensor cores' rate, HBM some
-// 1500 (34 KB), the work on elements (L . G, the parts of x, scaling and rounding) some 900 instructions of
-// each of 128 threads. So the element work is what has to be kept busy: two warpgroups take a head each (of the
-// same group, so that they share C, B and G), one thread issues the products, one warp runs ahead with
-// the gates and the loads of x. Nothing the warpgroups wait for depends on the state but Y's first product.
+// 1500 (34 KB), the work on elements (L . G, the parts of x, scaling and rounding) some 6000 warp
+// instructions, 1500 cycles of the four schedulers. So the element work is what has to be kept busy: eight
+// warps take each of two heads (of the same group, so that they share C, B and G), a thread having half of a
+// row; one thread issues the products; two warps run ahead with the gates and the loads of x. A tile's outputs
+// are finished in the next tile, between the two halves of its parts, so that no product is waited for
+// while there is work, and nothing but Y's first product waits for the state.
 //
 // L . G is formed without one exponential per element: with a_b = Gamma at the end of a block of 32 columns,
 // L_ts = e^(Gamma_t - a_b) e^(a_b - Gamma_s), a factor per row and one per column, both at most 1 for the
@@ -42,7 +44,8 @@ __device__ unsigned int g_scan_tc_error = 0;
 
 constexpr int N = 128;                    // state size
 constexpr int TT = kScanTcTile;           // tokens per tile
-constexpr int NT = 320;                   // two warpgroups, an issuing warp, a gates warp
+constexpr int NT = 608;                   // eight warps for each head, an issuing warp, two for the gates
+constexpr int kIssuer = 16, kFeeder = 17; // the others' first warps
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct TcGates {
@@ -69,8 +72,8 @@ struct Smem {
     static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
 };
 
-// TMEM columns: G, then per head M (L . G d in bf16 pairs), Y, U
-constexpr uint32_t kColG = 0, kColM = 128, kColY = 192, kColU = 256, kColHead = 192, kCols = 512;
+// TMEM columns: G, then per head U, Y1 and Y2. M (L . G d in bf16 pairs) takes U's place once that has been read.
+constexpr uint32_t kColG = 0, kColU = 128, kColY1 = 192, kColY2 = 256, kColHead = 192, kCols = 512;
 
 constexpr uint32_t kIdG = idesc_f16(128, 128, 1, 0, 0);   // C and B, both K-major
 constexpr uint32_t kIdY = idesc_f16(128, 64, 1, 0, 1);    // C or M K-major, state copy or x MN-major
@@ -85,6 +88,15 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -111,33 +123,26 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return r;
 }
+__device__ __forceinline__ uint4 lds(const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
+__device__ __forceinline__ void sts(uint8_t *p, uint4 v) { *reinterpret_cast<uint4 *>(p) = v; }
 __device__ __forceinline__ float f32(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t sw128(int r, int j) { return static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4)); }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
 // barriers, 8 bytes each behind Smem::kBars
 enum : int {
     kBcFull = 0,        // C and B of a tile (state run: [stage], B alone)
     kG = 2,             // G is there
     kXFull = 3,         // [head][stage] x
     kGates = 7,         // [head][stage] the gates
-    kXFree = 11,        // [head][stage] the warpgroup is done with the tile's x and gates
-    kS = 15,            // [head] the state's copy is written
-    kY1 = 17,           // [head] C S_0
-    kYFree = 19,        // [head] Y has been read
-    kP0 = 21, kP1 = 23, // [head] the parts of the tile's first, second 64 tokens are written
-    kPFree = 25,        // [head] the first half's product is done
-    kU = 27,            // [head] U is there
-    kM = 29,            // [head] M is written, Y scaled
-    kY = 31,            // [head] Y is there
-    kBarCount = 33
+    kPFree = 11,        // [head] the first half's product is done
+    kU = 13,            // [head] U is there
+    kY = 15,            // [head] Y1 and Y2 are there
+    kByHead = 17,       // from here on: the head's eight warps arrive
+    kXFree = 17,        // [head][stage] the tile's x and gates have been used
+    kS = 21,            // [head] the state's copy is written
+    kYFree = 23,        // [head] Y1 and Y2 have been read
+    kP0 = 25, kP1 = 27, // [head] the parts of the tile's first, second 64 tokens are written
+    kM = 29,            // [head] M is written
+    kBarCount = 31
 };
 
 struct Ctx {
@@ -158,43 +163,47 @@ struct Ctx {
             }
         }
     }
-    __device__ __forceinline__ void arrive(int i) const { mbar_arrive(bar(i)); }
+    // by a converged warp, once for all its lanes: 256 threads' own arrivals at one address take their turns
+    // in shared memory, and cost more than all the work on elements
+    __device__ __forceinline__ void arrive(int i) const {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bar(i));
+    }
 };
 
-// The gates of a tile, by one warp: lane l has tokens 4l .. 4l + 3. Returns log2 of the tile's decay.
-__device__ __forceinline__ double make_tc_gates(TcGates &g, const ScanParams &p, int64_t start, int cnt, int h) {
+// the steps of a lane's tokens 4l .. 4l + 3 before bias and softplus (0 behind the tile)
+__device__ __forceinline__ void load_dt(const ScanParams &p, int64_t start, int cnt, int h, float (&dt)[4]) {
+    const int t = 4 * (threadIdx.x & 31);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dt[j] = t + j < cnt ? p.dt[(start + t + j) * p.H + h] : 0.f;
+}
+
+// The gates of a tile of cnt tokens, by one warp: lane l has tokens 4l .. 4l + 3. Returns log2 of its decay.
+__device__ __forceinline__ Two make_tc_gates(TcGates &g, const float (&dt)[4], int cnt, float bias, int softplus, Two a2) {
     const int lane = threadIdx.x & 31;
-    const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-    const double a = p.A[h];
     float d[4];
-    double c[4];
+    Two c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int t = 4 * lane + j;
         float u;
-        d[j] = t < cnt ? step_of(p.dt[(start + t) * p.H + h], bias, p.softplus, &u) : 0.f;
-        c[j] = fmax(d[j] * a, kMinLog) * kLog2e + (j ? c[j - 1] : 0.0);
+        d[j] = 4 * lane + j < cnt ? step_of(dt[j], bias, softplus, &u) : 0.f;
+        c[j] = log_decay(d[j], a2);
+        if (j) c[j] = c[j - 1] + c[j];
     }
-    double s = c[3];
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, s, k);
-        if (lane >= k) s += o;
-    }
-    const double before = s - c[3];
-    const double total = __shfl_sync(0xffffffffu, s, 31);
-    const double anchor = __shfl_sync(0xffffffffu, s, lane | 7);                        // the block's end
-    const double opens = __shfl_sync(0xffffffffu, before, lane & 24);                   // and its start
-    const unsigned steep = __ballot_sync(0xffffffffu, opens - anchor > 60.0);
+    const Two s = scan_lanes(c[3]), total = shfl(s, 31);
+    Two before = {__shfl_up_sync(0xffffffffu, s.hi, 1), __shfl_up_sync(0xffffffffu, s.lo, 1)};
+    if (lane == 0) before = {0.f, 0.f};
+    const Two anchor = shfl(s, lane | 7), opens = shfl(before, lane & 24);   // the block's end and start
+    const unsigned steep = __ballot_sync(0xffffffffu, minus(opens, anchor) > 60.f);
     float hi[4], lo[4], col[4], from[4], weight[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const double v = before + c[j];
-        hi[j] = static_cast<float>(v);
-        lo[j] = static_cast<float>(v - hi[j]);
-        col[j] = d[j] * ex2(static_cast<float>(anchor - v));
-        from[j] = ex2(hi[j]) * fmaf(lo[j], kLn2, 1.f);
-        weight[j] = d[j] * ex2(static_cast<float>(total - v));
+        const Two v = before + c[j];
+        hi[j] = v.hi;
+        lo[j] = v.lo;
+        col[j] = d[j] * ex2(minus(anchor, v));
+        from[j] = ex2(v);
+        weight[j] = d[j] * ex2(minus(total, v));
     }
     reinterpret_cast<float4 *>(g.hi)[lane] = make_float4(hi[0], hi[1], hi[2], hi[3]);
     reinterpret_cast<float4 *>(g.lo)[lane] = make_float4(lo[0], lo[1], lo[2], lo[3]);
@@ -203,7 +212,7 @@ __device__ __forceinline__ double make_tc_gates(TcGates &g, const ScanParams &p,
     reinterpret_cast<float4 *>(g.from)[lane] = make_float4(from[0], from[1], from[2], from[3]);
     reinterpret_cast<float4 *>(g.weight)[lane] = make_float4(weight[0], weight[1], weight[2], weight[3]);
     if (lane == 0) {
-        g.total = ex2(static_cast<float>(total));
+        g.total = ex2(total);
         g.steep = (steep & 1u) | ((steep >> 7) & 2u) | ((steep >> 14) & 4u) | ((steep >> 21) & 8u);
     }
     return total;
@@ -240,12 +249,9 @@ __global__ void __launch_bounds__(NT, 1)
         return static_cast<int>(e - start_of(i));
     };
 
-    if (warp == 8) {
+    if (warp == kIssuer) {
         if (lane == 0) {
-            for (int i = 0; i < kBarCount; ++i) {
-                const bool by_group = (i >= kXFree && i < kY1) || (i >= kYFree && i < kPFree) || (i >= kM && i < kY);
-                mbar_init(x.bar(i), by_group ? 128 : 1);
-            }
+            for (int i = 0; i < kBarCount; ++i) mbar_init(x.bar(i), i < kByHead ? 1 : 8);
             s_abort = 0;
             fence_mbar_init();
         }
@@ -259,25 +265,27 @@ __global__ void __launch_bounds__(NT, 1)
     const uint32_t tmem = s_tmem;
     const uint32_t bc_bytes = kOut ? 4 * kBlock : 2 * kBlock;
 
-    if (warp < 8) {
+    if (warp < kIssuer) {
         // ---------------------------------------------------------------- a head's elements
-        const int hd = warp >> 2, r = tid & 127, wq = warp & 3;          // r: row (token or state entry), TMEM lane
+        // thread: row r (token or state entry, TMEM lane) and columns 32 hf .. + 32
+        const int hd = warp >> 3, hf = (warp >> 2) & 1, wq = warp & 3, r = wq * 32 + lane, t256 = tid & 255;
         if (hd < heads) {
-            const int v = v0 + hd, h = v / slices, col = v % slices * PC;
+            const int v = v0 + hd, h = v / slices, col = v % slices * PC + 32 * hf;
             const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-            const uint32_t tM = tmem + kColM + hd * kColHead + lanes, tY = tmem + kColY + hd * kColHead + lanes;
-            const uint32_t tU = tmem + kColU + hd * kColHead + lanes, tG = tmem + kColG + lanes;
-            const uint32_t st = base + L::kState + hd * kBlock, parts = base + L::kParts + hd * S * L::kPart;
+            const uint32_t tU = tmem + kColU + hd * kColHead + 32 * hf + lanes, tG = tmem + kColG + lanes;
+            const uint32_t tY1 = tmem + kColY1 + hd * kColHead + 32 * hf + lanes;
+            const uint32_t tY2 = tmem + kColY2 + hd * kColHead + 32 * hf + lanes;
+            uint8_t *st = smem + L::kState + hd * kBlock, *parts = smem + L::kParts + hd * S * L::kPart;
             const int64_t sn = static_cast<int64_t>(N) * p.P;
             const float Dh = p.D ? p.D[h] : 0.f;
-            float2 s[PC / 2];     // row r of the state
+            float2 s[16];         // this thread's part of the state
             {
                 const void *src = kOut && !entering ? p.h0 : entering;
                 const bool fp32 = !(kOut && !entering) || p.h0_fp32;
                 const int64_t e = ((kOut && !entering ? static_cast<int64_t>(u.i) : unit) * p.H + h) * sn +
                                   static_cast<int64_t>(r) * p.P + col;
 #pragma unroll
-                for (int j = 0; j < PC / 4; ++j) {
+                for (int j = 0; j < 8; ++j) {
                     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (src && fp32) {
                         f = reinterpret_cast<const float4 *>(static_cast<const float *>(src) + e)[j];
@@ -291,107 +299,153 @@ __global__ void __launch_bounds__(NT, 1)
             }
             auto publish = [&]() {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    sts128(st + sw128(r, j), make_uint4(bf_pair(s[4 * j].x, s[4 * j].y), bf_pair(s[4 * j + 1].x, s[4 * j + 1].y),
-                                                        bf_pair(s[4 * j + 2].x, s[4 * j + 2].y),
-                                                        bf_pair(s[4 * j + 3].x, s[4 * j + 3].y)));
+                for (int j = 0; j < 4; ++j)
+                    sts(st + sw128(r, 4 * hf + j),
+                        make_uint4(bf_pair(s[4 * j].x, s[4 * j].y), bf_pair(s[4 * j + 1].x, s[4 * j + 1].y),
+                                   bf_pair(s[4 * j + 2].x, s[4 * j + 2].y), bf_pair(s[4 * j + 3].x, s[4 * j + 3].y)));
                 fence_proxy_async_smem();
                 x.arrive(kS + hd);
             };
+            // d e^(Gamma_end - Gamma) x of 64 tokens in bf16 parts; four threads per token
+            auto write_parts = [&](int half, uint8_t *xt, const TcGates &g, int cnt) {
+                const int row = half * 64 + (t256 >> 2);
+                const float w = g.weight[row];
+                const float2 w2 = make_float2(w, w), minus1 = make_float2(-1.f, -1.f);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int chunk = (t256 & 3) * 2 + j;   // two rows' chunks of a turn lie in different banks
+                    uint32_t o[S][4];
+                    if (row < cnt) {
+                        const uint4 q = lds(xt + sw128(row, chunk));
+                        const uint32_t in[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float2 f = mul2(make_float2(bf_low(in[k]), bf_high(in[k])), w2);
+#pragma unroll
+                            for (int e = 0; e < S; ++e) {
+                                o[e][k] = bf_pair(f.x, f.y);
+                                if (e + 1 < S) f = fma2(make_float2(bf_low(o[e][k]), bf_high(o[e][k])), minus1, f);
+                            }
+                        }
+                    } else {
+                        // rows behind the piece: of other tokens, or none
+#pragma unroll
+                        for (int e = 0; e < S; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0u;
+                        sts(xt + sw128(row, chunk), make_uint4(0u, 0u, 0u, 0u));
+                    }
+#pragma unroll
+                    for (int e = 0; e < S; ++e)
+                        sts(parts + e * L::kPart + sw128(t256 >> 2, chunk), make_uint4(o[e][0], o[e][1], o[e][2], o[e][3]));
+                }
+                fence_proxy_async_smem();
+                x.arrive((half ? kP1 : kP0) + hd);
+            };
+            // y = e^Gamma Y1 + Y2 + D x of tile i, by way of x's own rows in shared memory
+            auto finish = [&](int i) {
+                const int stage = i & 1, cnt = count_of(i);
+                uint8_t *xt = smem + L::kX + (hd * 2 + stage) * kBlock;
+                if (!x.wait(kY + hd, i & 1)) return false;
+                tc_fence_after();
+                const float f = gates[hd * 2 + stage].from[r];
+                const float2 f2 = make_float2(f, f), D2 = make_float2(Dh, Dh);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t a[16], b[16];
+                    tmem_ld16(tY1 + 16 * q, a);
+                    tmem_ld16(tY2 + 16 * q, b);
+                    tmem_wait_ld();
+                    if (q == 1) {
+                        tc_fence_before();
+                        x.arrive(kYFree + hd);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint8_t *at_x = xt + sw128(r, 4 * hf + 2 * q + j);
+                        const uint4 w = lds(at_x);
+                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int e = 8 * j + 2 * k;
+                            const float2 y =
+                                fma2(make_float2(f32(a[e]), f32(a[e + 1])), f2, make_float2(f32(b[e]), f32(b[e + 1])));
+                            const float2 z = fma2(make_float2(bf_low(in[k]), bf_high(in[k])), D2, y);
+                            o[k] = bf_pair(z.x, z.y);
+                        }
+                        sts(at_x, make_uint4(o[0], o[1], o[2], o[3]));
+                    }
+                }
+                named_bar_sync(1 + hd, 256);
+                uint16_t *out = p.out + start_of(i) * p.out_stride + static_cast<int64_t>(v) * PC + (t256 & 7) * 8;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = j * 32 + (t256 >> 3);
+                    if (row < cnt)
+                        *reinterpret_cast<uint4 *>(out + row * p.out_stride) = lds(xt + sw128(row, t256 & 7));
+                }
+                fence_proxy_async_smem();   // x's next load comes after these reads and writes
+                x.arrive(kXFree + hd * 2 + stage);
+                return true;
+            };
             bool ok = true;
-            if (kOut && tiles > 0) {
-                // the blocks of M above the diagonal stay zero
-                const uint32_t zero[16] = {};
-                for (int b = wq + 1; b < 4; ++b) tmem_st16(tM + 16 * b, zero);
-                tmem_wait_st();
-                publish();
-            }
+            if (kOut && tiles > 0) publish();
             for (int i = 0; i < tiles && ok; ++i) {
                 const int stage = i & 1, cnt = count_of(i);
                 const uint32_t ph = i & 1, ph2 = (i >> 1) & 1;
-                const uint32_t xt = base + L::kX + (hd * 2 + stage) * kBlock;
+                uint8_t *xt = smem + L::kX + (hd * 2 + stage) * kBlock;
                 const TcGates &g = gates[hd * 2 + stage];
                 ok = x.wait(kXFull + hd * 2 + stage, ph2) && x.wait(kGates + hd * 2 + stage, ph2);
                 if (!ok) break;
                 if (cnt < TT && hd == 0) {
-                    // rows of B behind the sequence: whatever they hold would multiply zeros below
+                    // rows of B behind the piece: whatever they hold would multiply zeros below
                     ok = x.wait(kOut ? kBcFull : kBcFull + stage, kOut ? ph : ph2);
                     if (!ok) break;
-                    const uint32_t bt = base + (kOut || stage == 0 ? L::kB : L::kC);
+                    uint8_t *bt = smem + (kOut || stage == 0 ? L::kB : L::kC) + hf * kBlock;
                     if (r >= cnt)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            sts128(bt + (j >> 3) * kBlock + r * 128 + (j & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
+                        for (int j = 0; j < 8; ++j) sts(bt + r * 128 + j * 16, make_uint4(0u, 0u, 0u, 0u));
                 }
-                // d e^(Gamma_end - Gamma) x of 64 tokens in bf16 parts; two threads per token
-                auto write_parts = [&](int half) {
-                    const int row = half * 64 + (r >> 1);
-                    const float w = g.weight[row];
-                    const float2 w2 = make_float2(w, w), minus = make_float2(-1.f, -1.f);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int chunk = (r & 1) * 4 + j;
-                        uint4 part[S];
-                        if (row < cnt) {
-                            const uint4 q = lds128(xt + sw128(row, chunk));
-                            const uint32_t in[4] = {q.x, q.y, q.z, q.w};
-                            uint32_t o[S][4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                float2 f = mul2(make_float2(bf_low(in[k]), bf_high(in[k])), w2);
-#pragma unroll
-                                for (int e = 0; e < S; ++e) {
-                                    o[e][k] = bf_pair(f.x, f.y);
-                                    if (e + 1 < S) f = fma2(make_float2(bf_low(o[e][k]), bf_high(o[e][k])), minus, f);
-                                }
-                            }
-#pragma unroll
-                            for (int e = 0; e < S; ++e) part[e] = make_uint4(o[e][0], o[e][1], o[e][2], o[e][3]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < S; ++e) part[e] = make_uint4(0u, 0u, 0u, 0u);
-                            sts128(xt + sw128(row, chunk), make_uint4(0u, 0u, 0u, 0u));
-                        }
-#pragma unroll
-                        for (int e = 0; e < S; ++e) sts128(parts + e * L::kPart + sw128(r >> 1, chunk), part[e]);
-                    }
-                    fence_proxy_async_smem();
-                    x.arrive((half ? kP1 : kP0) + hd);
-                };
-                write_parts(0);
-                if (kOut) {
-                    // Y = C S_0, scaled
-                    ok = x.wait(kY1 + hd, ph);
+                write_parts(0, xt, g, cnt);
+                if (kOut && i > 0) {
+                    ok = finish(i - 1);
                     if (!ok) break;
-                    tc_fence_after();
-                    const float2 f = make_float2(g.from[r], g.from[r]);
-                    uint32_t a[32], b[32];
-                    tmem_ld32(tY, a);
-                    tmem_ld32(tY + 32, b);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float2 q = mul2(make_float2(f32(a[j]), f32(a[j + 1])), f);
-                        a[j] = __float_as_uint(q.x);
-                        a[j + 1] = __float_as_uint(q.y);
-                        const float2 q2 = mul2(make_float2(f32(b[j]), f32(b[j + 1])), f);
-                        b[j] = __float_as_uint(q2.x);
-                        b[j + 1] = __float_as_uint(q2.y);
-                    }
-                    tmem_st32(tY, a);
-                    tmem_st32(tY + 32, b);
                 }
                 ok = x.wait(kPFree + hd, ph);
                 if (!ok) break;
-                write_parts(1);
-                if (kOut) {
-                    // M = L . G d, rows r, blocks of 32 columns up to the diagonal
-                    ok = x.wait(kG, ph);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const float gh = g.hi[r], glo = g.lo[r];
-                    for (int b = 0; b <= wq; ++b) {
-                        uint32_t a[32], o[16];
+                write_parts(1, xt, g, cnt);
+                // S = e^(Gamma_end) S + U
+                ok = x.wait(kU + hd, ph);
+                if (!ok) break;
+                tc_fence_after();
+                {
+                    const float2 tot = make_float2(g.total, g.total);
+                    uint32_t a[32];
+                    tmem_ld32(tU, a);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) s[j] = fma2(s[j], tot, make_float2(f32(a[2 * j]), f32(a[2 * j + 1])));
+                }
+                if (!kOut) {
+                    tc_fence_before();
+                    x.arrive(kXFree + hd * 2 + stage);
+                    continue;
+                }
+                // the state's copy: C S_0 of this tile has been computed, as the product behind it has
+                if (i + 1 < tiles) publish();
+                // M = L . G d in U's place: rows r, blocks of 32 columns, two for each half
+                ok = x.wait(kG, ph);
+                if (!ok) break;
+                tc_fence_after();
+                const float gh = g.hi[r], glo = g.lo[r];
+#pragma unroll
+                for (int bb = 0; bb < 2; ++bb) {
+                    const int b = 2 * hf + bb;
+                    uint32_t o[16];
+                    if (b > wq) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = 0u;
+                    } else {
+                        uint32_t a[32];
                         tmem_ld32(tG + 32 * b, a);
                         const int e = 32 * b + 31;
                         if (b < wq || !((g.steep >> b) & 1u)) {
@@ -401,10 +455,10 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 const float4 cf = reinterpret_cast<const float4 *>(g.col + 32 * b)[j];
-                                const float2 m0 = mul2(mul2(make_float2(f32(a[4 * j]), f32(a[4 * j + 1])),
-                                                            make_float2(cf.x, cf.y)), rf2);
-                                const float2 m1 = mul2(mul2(make_float2(f32(a[4 * j + 2]), f32(a[4 * j + 3])),
-                                                            make_float2(cf.z, cf.w)), rf2);
+                                const float2 m0 =
+                                    mul2(mul2(make_float2(f32(a[4 * j]), f32(a[4 * j + 1])), make_float2(cf.x, cf.y)), rf2);
+                                const float2 m1 =
+                                    mul2(mul2(make_float2(f32(a[4 * j + 2]), f32(a[4 * j + 3])), make_float2(cf.z, cf.w)), rf2);
                                 if (b < wq) {
                                     o[2 * j] = bf_pair(m0.x, m0.y);
                                     o[2 * j + 1] = bf_pair(m1.x, m1.y);
@@ -429,76 +483,21 @@ __global__ void __launch_bounds__(NT, 1)
                                 o[j] = bf_pair(m[0], m[1]);
                             }
                         }
-                        tmem_st16(tM + 16 * b, o);
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    x.arrive(kM + hd);
+                    tmem_st16(tU + 16 * bb, o);   // tU is column 32 hf: M's block 2 hf
                 }
-                // S = e^(Gamma_end) S + U
-                ok = x.wait(kU + hd, ph);
-                if (!ok) break;
-                tc_fence_after();
-                {
-                    const float2 tot = make_float2(g.total, g.total);
-                    uint32_t a[32];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        tmem_ld32(tU + 32 * q, a);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            s[16 * q + j] = fma2(s[16 * q + j], tot, make_float2(f32(a[2 * j]), f32(a[2 * j + 1])));
-                    }
-                    tc_fence_before();
-                }
-                if (kOut) {
-                    if (i + 1 < tiles) publish();
-                    // the outputs: Y + D x, by way of x's own rows in shared memory
-                    ok = x.wait(kY + hd, ph);
-                    if (!ok) break;
-                    tc_fence_after();
-                    uint32_t a[32], b[32];
-                    tmem_ld32(tY, a);
-                    tmem_ld32(tY + 32, b);
-                    tmem_wait_ld();
-                    tc_fence_before();
-                    x.arrive(kYFree + hd);
-                    const float2 D2 = make_float2(Dh, Dh);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint4 q = lds128(xt + sw128(r, j));
-                        const uint32_t in[4] = {q.x, q.y, q.z, q.w};
-                        uint32_t o[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int e = (8 * j + 2 * k) & 31;
-                            const float2 y = j < 4 ? make_float2(f32(a[e]), f32(a[e + 1])) : make_float2(f32(b[e]), f32(b[e + 1]));
-                            const float2 z = fma2(make_float2(bf_low(in[k]), bf_high(in[k])), D2, y);
-                            o[k] = bf_pair(z.x, z.y);
-                        }
-                        sts128(xt + sw128(r, j), make_uint4(o[0], o[1], o[2], o[3]));
-                    }
-                    named_bar_sync(1 + hd, 128);
-                    const int64_t at_out = start_of(i) * p.out_stride + static_cast<int64_t>(v) * PC;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int row = j * 16 + (r >> 3);
-                        if (row < cnt)
-                            *reinterpret_cast<uint4 *>(p.out + at_out + row * p.out_stride + (r & 7) * 8) =
-                                lds128(xt + sw128(row, r & 7));
-                    }
-                    fence_proxy_async_smem();   // x's next load comes after these reads and writes
-                }
-                x.arrive(kXFree + hd * 2 + stage);
+                tmem_wait_st();
+                tc_fence_before();
+                x.arrive(kM + hd);
             }
+            if (kOut && ok && tiles > 0) ok = finish(tiles - 1);
             // the state that leaves
             void *dst = kOut ? (u.last ? p.hT : nullptr) : leave;
             if (ok && dst) {
                 const bool fp32 = !kOut || p.hT_fp32;
                 const int64_t e = ((kOut ? static_cast<int64_t>(u.i) : unit) * p.H + h) * sn + static_cast<int64_t>(r) * p.P + col;
 #pragma unroll
-                for (int j = 0; j < PC / 4; ++j) {
+                for (int j = 0; j < 8; ++j) {
                     if (fp32)
                         reinterpret_cast<float4 *>(static_cast<float *>(dst) + e)[j] =
                             make_float4(s[2 * j].x, s[2 * j].y, s[2 * j + 1].x, s[2 * j + 1].y);
@@ -508,7 +507,7 @@ __global__ void __launch_bounds__(NT, 1)
                 }
             }
         }
-    } else if (warp == 8) {
+    } else if (warp == kIssuer) {
         // ---------------------------------------------------------------- loads of C and B, and the products
         const int bcol = grp * N;
         auto load_bc = [&](int i) {
@@ -532,6 +531,7 @@ __global__ void __launch_bounds__(NT, 1)
             if (!ok) break;
             __syncwarp();
             if (kOut) {
+                // G: the last tile's has been read (its M is written)
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -543,41 +543,49 @@ __global__ void __launch_bounds__(NT, 1)
                     mma_commit(x.bar(kG));
                 }
                 __syncwarp();
-                for (int hd = 0; hd < heads && ok; ++hd) {
+            }
+            auto product_u = [&](int hd, int half) {
+                if (elect_one()) {
+                    const uint32_t parts = base + L::kParts + hd * S * L::kPart;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int e = S - 1; e >= 0; --e)
+                            mma_f16(tmem + kColU + hd * kColHead,
+                                    smem_desc(bt + (half * 4 + k) * 2048, kBlock, 1024, kSwizzle128),
+                                    smem_desc(parts + e * L::kPart + k * 2048, kBlock, 1024, kSwizzle128), kIdU,
+                                    !(half == 0 && k == 0 && e == S - 1));
+                    mma_commit(x.bar((half ? kU : kPFree) + hd));
+                }
+                __syncwarp();
+            };
+            for (int hd = 0; hd < heads && ok; ++hd) {
+                // U takes the place of the last tile's M, which has been multiplied
+                ok = x.wait(kP0 + hd, ph) && (!kOut || i == 0 || x.wait(kY + hd, (i - 1) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                product_u(hd, 0);
+            }
+            for (int hd = 0; hd < heads && ok; ++hd) {
+                if (kOut) {
                     ok = x.wait(kS + hd, ph) && (i == 0 || x.wait(kYFree + hd, (i - 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            mma_f16(tmem + kColY + hd * kColHead,
+                            mma_f16(tmem + kColY1 + hd * kColHead,
                                     smem_desc(base + L::kC + (k >> 2) * kBlock + (k & 3) * 32, 16, 1024, kSwizzle128),
                                     smem_desc(base + L::kState + hd * kBlock + k * 2048, kBlock, 1024, kSwizzle128), kIdY,
                                     k > 0);
-                        mma_commit(x.bar(kY1 + hd));
                     }
                     __syncwarp();
                 }
+                ok = x.wait(kP1 + hd, ph);
+                if (!ok) break;
+                tc_fence_after();
+                product_u(hd, 1);
             }
-            for (int half = 0; half < 2 && ok; ++half)
-                for (int hd = 0; hd < heads && ok; ++hd) {
-                    ok = x.wait((half ? kP1 : kP0) + hd, ph);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t parts = base + L::kParts + hd * S * L::kPart;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-#pragma unroll
-                            for (int e = S - 1; e >= 0; --e)
-                                mma_f16(tmem + kColU + hd * kColHead,
-                                        smem_desc(bt + (half * 4 + k) * 2048, kBlock, 1024, kSwizzle128),
-                                        smem_desc(parts + e * L::kPart + k * 2048, kBlock, 1024, kSwizzle128), kIdU,
-                                        !(half == 0 && k == 0 && e == S - 1));
-                        mma_commit(x.bar((half ? kU : kPFree) + hd));
-                    }
-                    __syncwarp();
-                }
             if (!ok) break;
             // the last commit covers every product so far: C and B are free
             const int next = kOut ? i + 1 : i + 2;
@@ -597,41 +605,41 @@ __global__ void __launch_bounds__(NT, 1)
                         const uint32_t xt = base + L::kX + (hd * 2 + (i & 1)) * kBlock;
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            mma_f16_ts(tmem + kColY + hd * kColHead, tmem + kColM + hd * kColHead + 8 * k,
-                                       smem_desc(xt + k * 2048, kBlock, 1024, kSwizzle128), kIdY, 1);
+                            mma_f16_ts(tmem + kColY2 + hd * kColHead, tmem + kColU + hd * kColHead + 8 * k,
+                                       smem_desc(xt + k * 2048, kBlock, 1024, kSwizzle128), kIdY, k > 0);
                         mma_commit(x.bar(kY + hd));
                     }
                     __syncwarp();
                 }
             }
         }
-    } else {
-        // ---------------------------------------------------------------- x and the gates, up to two tiles ahead
+    } else if (warp - kFeeder < heads) {
+        // ---------------------------------------------------------------- a head's x and gates, up to two tiles ahead
+        const int hd = warp - kFeeder, v = v0 + hd, h = v / slices;
+        const Two rate = log2_rate(p.A[h]);
+        const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+        Two decay = {0.f, 0.f};
+        float dt[4];
         bool ok = true;
-        double decay[2] = {0.0, 0.0};
-        for (int i = 0; i < tiles && ok; ++i) {
+        if (tiles > 0) load_dt(p, start_of(0), count_of(0), h, dt);
+        for (int i = 0; i < tiles; ++i) {
             const int stage = i & 1;
-            for (int hd = 0; hd < heads && ok; ++hd) {
-                const int v = v0 + hd;
-                if (i >= 2) ok = x.wait(kXFree + hd * 2 + stage, ((i - 2) >> 1) & 1);
-                if (!ok) break;
-                __syncwarp();
-                if (elect_one()) {
-                    const int bar = kXFull + hd * 2 + stage;
-                    mbar_arrive_expect_tx(x.bar(bar), kBlock);
-                    tma_load_2d(base + L::kX + (hd * 2 + stage) * kBlock, &maps.x, x.bar(bar), v * PC,
-                                static_cast<int32_t>(start_of(i)));
-                }
-                __syncwarp();
-                decay[hd] += make_tc_gates(gates[hd * 2 + stage], p, start_of(i), count_of(i), v / slices);
-                __syncwarp();
-                if (lane == 0) x.arrive(kGates + hd * 2 + stage);
+            if (i >= 2) ok = x.wait(kXFree + hd * 2 + stage, ((i - 2) >> 1) & 1);
+            if (!ok) break;
+            __syncwarp();
+            if (elect_one()) {
+                const int bar = kXFull + hd * 2 + stage;
+                mbar_arrive_expect_tx(x.bar(bar), kBlock);
+                tma_load_2d(base + L::kX + (hd * 2 + stage) * kBlock, &maps.x, x.bar(bar), v * PC,
+                            static_cast<int32_t>(start_of(i)));
             }
+            __syncwarp();
+            const float now[4] = {dt[0], dt[1], dt[2], dt[3]};
+            if (i + 1 < tiles) load_dt(p, start_of(i + 1), count_of(i + 1), h, dt);
+            decay = decay + make_tc_gates(gates[hd * 2 + stage], now, count_of(i), bias, p.softplus, rate);
+            x.arrive(kGates + hd * 2 + stage);
         }
-        if (!kOut && ok && lane == 0)
-            for (int hd = 0; hd < heads; ++hd)
-                if ((v0 + hd) % slices == 0)
-                    leave_decay[unit * p.H + (v0 + hd) / slices] = ex2(static_cast<float>(decay[hd]));
+        if (!kOut && ok && lane == 0 && v % slices == 0) leave_decay[unit * p.H + h] = ex2(decay);
     }
     if (s_abort) {
         // copies may still be in flight into this CTA's shared memory
@@ -642,7 +650,7 @@ __global__ void __launch_bounds__(NT, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tmem, kCols);
+    if (warp == kIssuer) tmem_dealloc(tmem, kCols);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
