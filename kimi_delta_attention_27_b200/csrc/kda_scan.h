@@ -59,17 +59,27 @@ cudaError_t launch_scan_decode(const ScanDecodeParams &p, cudaStream_t stream);
 cudaError_t read_and_clear_scan_error(unsigned int *value);
 
 // Steps of the forward that the backward takes too (kda_scan_fwd.cu): the states entering every
-// 64-token cell of every sequence, or, with `reverse`, the gradients of the states leaving them.
-// Cells lie on the global grid of 64 tokens; sequence i's cell c has slot i + c of `states`
-// [slots, H, N, P]. `ws`: scan_states_workspace_bytes. Reverse: what reaches the start goes to dh0.
+// 64-token cell of every sequence (states), and the gradients of the states leaving them (grads; what reaches
+// a sequence's start goes to dh0). Cells lie on the global grid of 64 tokens; sequence i's cell c has
+// slot i + c of [slots, H, N, P]. `ws`: scan_states_workspace_bytes.
 size_t scan_states_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N);
-cudaError_t launch_scan_states(const ScanParams &p, bool reverse, float *states, float *ws, cudaStream_t stream);
+cudaError_t launch_scan_states(const ScanParams &p, float *states, float *grads, float *ws, cudaStream_t stream);
 
-// The forward's kernel for a state size of 128 (kda_scan_tc.cu): the main run over pieces (`out`), from the
-// states in `entering` or h0, or the run that finds each piece's own contribution to the state (leave, decay).
-cudaError_t launch_scan_tc(const ScanParams &p, bool out, int64_t seg, int64_t units, const float *entering, float *leave,
-                           float *decay, cudaStream_t stream);
+// The kernels for a state size of 128 (kda_scan_tc.cu, kda_scan_tc_state.cu). The main run over pieces, from the
+// states in `entering` or from h0:
+cudaError_t launch_scan_tc(const ScanParams &p, int64_t seg, int64_t units, const float *entering, cudaStream_t stream);
+// and the state alone, with its weighted columns in 2 or 3 bf16 parts, over the tokens (fwd) and, with two
+// directions, over dy and C backwards (rev).
+struct ScanStateRun {
+    const float *entering;   // the states that pieces enter with, or nullptr: h0 (dhT) where a sequence begins (ends)
+    float *leave;            // what each piece adds, from zero, and its decay [pieces, H]; or nullptr
+    float *leave_decay;
+    float *states;           // the state at the entry (reverse: exit) of every 64-token cell, or nullptr
+};
+cudaError_t launch_scan_tc_state(const ScanParams &p, int parts, int directions, int64_t seg, int64_t units,
+                                 const ScanStateRun &fwd, const ScanStateRun &rev, cudaStream_t stream);
 cudaError_t read_and_clear_scan_tc_error(unsigned int *value);
+cudaError_t read_and_clear_scan_state_error(unsigned int *value);
 
 constexpr int kScanTile = 64;     // tokens per tile
 constexpr int kScanTcTile = 128;  // and of launch_scan_tc

@@ -19,11 +19,11 @@
 //
 // The states S_0 and gradients R of every tile come from two sweeps (launch_scan_states), fp32 in the
 // workspace: that is its bulk, and what bounds the backward's traffic. The gradient kernel then takes all
-// tiles at once. One CTA of N / 16 warps has one tile of one group and walks (a share of) the group's heads,
+// tiles at once. One CTA of N / 8 warps has one tile of one group and walks (a share of) the group's heads,
 // so C B^T is computed once, and dB and dC add up over the heads in registers, without atomics. Warp w owns
-// the columns [16 w, +16) of dB and dC: S_0 and R go from memory straight into its operand fragments. Where
-// tiles x groups leave SMs idle the heads are shared out over several CTAs, whose dB and dC are added
-// by scan_bc_kernel in a fixed order. Sums over tokens go by partial sums per tile, too: runs repeat bit for bit.
+// the columns [8 w, +8) of dB and dC: S_0 and R go from memory straight into its operand fragments, the next
+// head's while this one's are multiplied. Where tiles x groups leave SMs idle the heads are shared out over
+// several CTAs, whose dB and dC are added by scan_bc_kernel in a fixed order. Sums over tokens go by partial sums per tile, too: runs repeat bit for bit.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -34,7 +34,7 @@ namespace scan {
 
 template <int N>
 struct BwdSmem {
-    static constexpr int NW = N / 16;
+    static constexpr int NW = N / 8;                       // warps: one per 8 columns of dB and dC
     static constexpr int kBC = T * N * 2, kX = T * PC * 2, kM = T * T * 2;
     static constexpr int kB = 0, kC = kBC;
     static constexpr int kXY = 2 * kBC;                    // two stages of x and dy
@@ -46,7 +46,8 @@ struct BwdSmem {
     static constexpr int kDiag = kCol + 4 * T * 4;         // [2][T] the diagonals of M . Q and of Q
     static constexpr int kInt = kDiag + 2 * T * 4;         // [2][NW][T] C . (S_0 dy) and B . (R x)
     static constexpr int kRS = kInt + 2 * NW * T * 4;      // [NW] <R, S_0>
-    static constexpr int kBytes = kRS + 64;
+    static constexpr int kSum = kRS + 64;                  // [11][32] the first warp's sums over a head's slices
+    static constexpr int kBytes = kSum + 11 * 32 * 4;
 };
 
 // 16 x 8 blocks of the lower triangle of a 64 x 64 matrix: row block 0 has 2, 1 has 4, 2 has 6, 3 has 8
@@ -76,7 +77,7 @@ __device__ __forceinline__ void state_frag(const float2 &v0, const float2 &v1, u
 }
 
 template <int N>
-__global__ void __launch_bounds__(2 * N, 1) scan_bwd_kernel(ScanParams p, BwdWork w) {
+__global__ void __launch_bounds__(4 * N, 1) scan_bwd_kernel(ScanParams p, BwdWork w) {
     extern __shared__ __align__(1024) uint8_t smem[];
     using L = BwdSmem<N>;
     constexpr int NW = L::NW, NT = 32 * NW, ROWB = N * 2, BLOCKS = (20 + NW - 1) / NW, XT = 32 / NW;
@@ -138,16 +139,26 @@ __global__ void __launch_bounds__(2 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
             }
         }
     }
-    float dc[4][2][4], db[4][2][4];   // rows 16 m, columns 16 warp + 8 n
+    float dc[4][4], db[4][4];   // rows 16 m, columns 8 warp
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int j = 0; j < 4; ++j) dc[m][j] = db[m][j] = 0.f;
+    // this warp's rows of S_0 and R as B fragments ([kk]: columns 16 kk + q2, + 8), one head ahead
+    float2 vs[4][2], vr[4][2];
+    auto state_at = [&](const float *of, int k) {
+        return of + (unit * p.H + hb + k / slices) * sn + (k % slices) * PC + static_cast<int64_t>(warp * 8 + gl) * p.P + q2;
+    };
+    auto load_state = [&](const float *src, float2 (&v)[4][2]) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dc[m][n][j] = db[m][n][j] = 0.f;
-    // per token (lane l of warp 0: tokens 2l and 2l + 1), summed over a head's slices
-    double t_q[2] = {0, 0}, t_int[2] = {0, 0}, t_in[2] = {0, 0}, t_rs = 0;
-    float t_dd[2] = {0.f, 0.f}, t_qd[2] = {0.f, 0.f};
+        for (int kk = 0; kk < 4; ++kk) {
+            v[kk][0] = *reinterpret_cast<const float2 *>(src + kk * 16);
+            v[kk][1] = *reinterpret_cast<const float2 *>(src + kk * 16 + 8);
+        }
+    };
+    load_state(state_at(w.states, 0), vs);
+    load_state(state_at(w.grads, 0), vr);
+    float *sum_s = reinterpret_cast<float *>(smem + L::kSum);
 
     for (int k = 0; k < work; ++k) {
         const int h = hb + k / slices, sl = k % slices, stage = k & 1;
@@ -214,57 +225,37 @@ __global__ void __launch_bounds__(2 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
                 }
             }
         }
-        // ---- dy S_0^T and x R^T: 64 x 16 for this warp; S_0 and R from memory into fragments
-        const float *S0 = w.states + (unit * p.H + h) * sn + sl * PC + static_cast<int64_t>(warp * 16 + gl) * p.P + q2;
-        const float *Re = w.grads + (unit * p.H + h) * sn + sl * PC + static_cast<int64_t>(warp * 16 + gl) * p.P + q2;
+        // ---- dy S_0^T and x R^T: 64 x 8 for this warp
         float rs = 0.f;
 #pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) rs = fmaf(vs[kk][x].x, vr[kk][x].x, fmaf(vs[kk][x].y, vr[kk][x].y, rs));
+#pragma unroll
         for (int which = 0; which < 2; ++which) {
-            const float *src = which ? Re : S0;
-            const uint32_t at_tile = which ? xt : dyt, bc = base + (which ? L::kB : L::kC);
-            float tmp[4][2][4];
+            float2(&v)[4][2] = which ? vr : vs;
+            const uint32_t at_tile = which ? xt : dyt, bc = which ? L::kB : L::kC;
+            float tmp[4][4];
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) tmp[m][n][j] = 0.f;
-            float2 v[4][2][2];
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    v[kk][n][0] = *reinterpret_cast<const float2 *>(src + static_cast<int64_t>(8 * n) * p.P + kk * 16);
-                    v[kk][n][1] = *reinterpret_cast<const float2 *>(src + static_cast<int64_t>(8 * n) * p.P + kk * 16 + 8);
-                }
+            for (int m = 0; m < 4; ++m) tmp[m][0] = tmp[m][1] = tmp[m][2] = tmp[m][3] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-                uint32_t b[2][3][2];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    state_frag<3>(v[kk][n][0], v[kk][n][1], b[n]);
-                    if (which) {
-                        const int row = warp * 16 + 8 * n + gl;
-                        *reinterpret_cast<uint32_t *>(smem + L::kR + at<PC * 2>(row, 2 * kk) + q2 * 2) = b[n][0][0];
-                        *reinterpret_cast<uint32_t *>(smem + L::kR + at<PC * 2>(row, 2 * kk + 1) + q2 * 2) = b[n][0][1];
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float2 s =
-                                *reinterpret_cast<const float2 *>(S0 + static_cast<int64_t>(8 * n) * p.P + kk * 16 + 8 * x);
-                            rs = fmaf(s.x, v[kk][n][x].x, fmaf(s.y, v[kk][n][x].y, rs));
-                        }
-                    }
+                uint32_t b[3][2];
+                state_frag<3>(v[kk][0], v[kk][1], b);
+                if (which) {
+                    const int row = warp * 8 + gl;
+                    *reinterpret_cast<uint32_t *>(smem + L::kR + at<PC * 2>(row, 2 * kk) + q2 * 2) = b[0][0];
+                    *reinterpret_cast<uint32_t *>(smem + L::kR + at<PC * 2>(row, 2 * kk + 1) + q2 * 2) = b[0][1];
                 }
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     uint32_t a[4];
                     frag_a<PC * 2>(at_tile, m * 16, 2 * kk, a);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int s = 2; s >= 0; --s) mma(tmp[m][n], a, b[n][s][0], b[n][s][1]);
+                    for (int s = 2; s >= 0; --s) mma(tmp[m], a, b[s][0], b[s][1]);
                 }
             }
+            if (k + 1 < work) load_state(state_at(which ? w.grads : w.states, k + 1), v);
             // the dot with C's or B's own columns, and into dC or dB
 #pragma unroll
             for (int m = 0; m < 4; ++m)
@@ -272,16 +263,11 @@ __global__ void __launch_bounds__(2 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
                 for (int e = 0; e < 2; ++e) {
                     const int t = m * 16 + 8 * e + gl;
                     const float f = which ? g.weight[t] : g.from[t];
-                    float dot = 0.f;
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const uint32_t cv =
-                            *reinterpret_cast<const uint32_t *>(smem + (bc - base) + at<ROWB>(t, 2 * warp + n) + q2 * 2);
-                        dot = fmaf(tmp[m][n][2 * e], bf_low(cv), fmaf(tmp[m][n][2 * e + 1], bf_high(cv), dot));
-                        float(&to)[4] = which ? db[m][n] : dc[m][n];
-                        to[2 * e] = fmaf(f, tmp[m][n][2 * e], to[2 * e]);
-                        to[2 * e + 1] = fmaf(f, tmp[m][n][2 * e + 1], to[2 * e + 1]);
-                    }
+                    const uint32_t cv = *reinterpret_cast<const uint32_t *>(smem + bc + at<ROWB>(t, warp) + q2 * 2);
+                    float dot = fmaf(tmp[m][2 * e], bf_low(cv), tmp[m][2 * e + 1] * bf_high(cv));
+                    float(&to)[4] = which ? db[m] : dc[m];
+                    to[2 * e] = fmaf(f, tmp[m][2 * e], to[2 * e]);
+                    to[2 * e + 1] = fmaf(f, tmp[m][2 * e + 1], to[2 * e + 1]);
                     dot += __shfl_xor_sync(0xffffffffu, dot, 1);
                     dot += __shfl_xor_sync(0xffffffffu, dot, 2);
                     if ((lane & 3) == 0) int_s[(which * NW + warp) * T + t] = dot;
@@ -294,21 +280,19 @@ __global__ void __launch_bounds__(2 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
         // ---- dC += K B, dB += K^T C
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-            uint32_t bb[4], bcf[4];
-            frag_bt<ROWB>(base + L::kB, kk * 16, 2 * warp, bb);
-            frag_bt<ROWB>(base + L::kC, kk * 16, 2 * warp, bcf);
+            uint32_t bb[2], bcf[2];
+            frag_bt8<ROWB>(base + L::kB, kk * 16, warp, bb);
+            frag_bt8<ROWB>(base + L::kC, kk * 16, warp, bcf);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 uint32_t a[4];
                 if (kk <= m) {
                     frag_a<T * 2>(base + L::kKt, m * 16, 2 * kk, a);
-                    mma(dc[m][0], a, bb[0], bb[1]);
-                    mma(dc[m][1], a, bb[2], bb[3]);
+                    mma(dc[m], a, bb[0], bb[1]);
                 }
                 if (kk >= m) {
                     frag_at<T * 2>(base + L::kKt, kk * 16, 2 * m, a);
-                    mma(db[m][0], a, bcf[0], bcf[1]);
-                    mma(db[m][1], a, bcf[2], bcf[3]);
+                    mma(db[m], a, bcf[0], bcf[1]);
                 }
             }
         }
@@ -368,10 +352,12 @@ __global__ void __launch_bounds__(2 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
         }
         // ---- the steps' gradients, by the first warp
         if (warp == 0) {
+            // per token (lane l: tokens 2l and 2l + 1): q, int, in, dd, Q_tt, and <R, S_0>, summed over slices
+            float v[11];
             float rs_all = 0.f;
 #pragma unroll
             for (int x = 0; x < NW; ++x) rs_all += rs_s[x];
-            t_rs += rs_all;
+            v[10] = rs_all;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int t = 2 * lane + e, rb = t >> 4;
@@ -384,44 +370,50 @@ __global__ void __launch_bounds__(2 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
                     bi += int_s[(NW + x) * T + t];
                 }
                 bi *= g.to[t];
-                t_q[e] += static_cast<double>(row) - static_cast<double>(g.d[t]) * col;
-                t_int[e] += g.from[t] * ci;
-                t_in[e] += g.d[t] * bi;
-                t_dd[e] += col + diag_s[t] + bi;
-                t_qd[e] += diag_s[T + t];
+                v[e] = fmaf(-g.d[t], col, row);
+                v[2 + e] = g.from[t] * ci;
+                v[4 + e] = g.d[t] * bi;
+                v[6 + e] = col + diag_s[t] + bi;
+                v[8 + e] = diag_s[T + t];
+            }
+            if (slices > 1) {
+#pragma unroll
+                for (int j = 0; j < 11; ++j) {
+                    if (sl > 0) v[j] += sum_s[j * 32 + lane];
+                    sum_s[j * 32 + lane] = v[j];
+                }
             }
             if (sl == slices - 1) {
                 // suffix sums of q + int, prefix sums of in
-                double suf = t_q[0] + t_int[0] + t_q[1] + t_int[1], pre = t_in[0] + t_in[1];
-                const double own = suf, own_in = pre;
+                float suf = v[0] + v[2] + v[1] + v[3], pre = v[4] + v[5];
 #pragma unroll
                 for (int x = 1; x < 32; x <<= 1) {
-                    const double a = __shfl_down_sync(0xffffffffu, suf, x), b = __shfl_up_sync(0xffffffffu, pre, x);
+                    const float a = __shfl_down_sync(0xffffffffu, suf, x), b = __shfl_up_sync(0xffffffffu, pre, x);
                     if (lane + x < 32) suf += a;
                     if (lane >= x) pre += b;
                 }
-                const double rest = static_cast<double>(g.total) * t_rs;
-                const double dl[2] = {suf + (pre - own_in) + rest,
-                                      (suf - own + t_q[1] + t_int[1]) + (pre - own_in + t_in[0]) + rest};
+                // behind the lane's tokens, and before them
+                float after = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
+                if (lane == 31) after = 0.f;
+                if (lane == 0) before = 0.f;
+                const float rest = g.total * v[10];
+                const float dl[2] = {suf + (before + rest), after + (v[1] + v[3]) + (before + v[4] + rest)};
                 const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-                double sa = 0, sb = 0, sd = 0;
+                float sa = 0.f, sb = 0.f, sd = 0.f;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int t = 2 * lane + e;
                     if (t < cnt) {
                         float uu;
                         step_of(p.dt[(start + t) * p.H + h], bias, 0, &uu);
-                        double dd = t_dd[e] + dl[e] * A;
+                        float dd = fmaf(dl[e], A, v[6 + e]);
                         if (p.softplus) dd *= 1.f / (1.f + expf(-uu));
-                        p.ddt[(start + t) * p.H + h] = static_cast<float>(dd);
-                        sa += dl[e] * g.d[t];
+                        p.ddt[(start + t) * p.H + h] = dd;
+                        sa = fmaf(dl[e], g.d[t], sa);
                         sb += dd;
-                        sd += t_qd[e];
+                        sd += v[8 + e];
                     }
-                    t_q[e] = t_int[e] = t_in[e] = 0;
-                    t_dd[e] = t_qd[e] = 0.f;
                 }
-                t_rs = 0;
 #pragma unroll
                 for (int x = 16; x > 0; x >>= 1) {
                     sa += __shfl_xor_sync(0xffffffffu, sa, x);
@@ -429,9 +421,9 @@ __global__ void __launch_bounds__(2 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
                     sd += __shfl_xor_sync(0xffffffffu, sd, x);
                 }
                 if (lane == 0) {
-                    w.part[(unit * 3 + 0) * p.H + h] = static_cast<float>(sa);
-                    w.part[(unit * 3 + 1) * p.H + h] = static_cast<float>(sb);
-                    w.part[(unit * 3 + 2) * p.H + h] = static_cast<float>(sd);
+                    w.part[(unit * 3 + 0) * p.H + h] = sa;
+                    w.part[(unit * 3 + 1) * p.H + h] = sb;
+                    w.part[(unit * 3 + 2) * p.H + h] = sd;
                 }
             }
         } else if (warp == 1 && sl == slices - 1 && h + 1 < he) {
@@ -447,20 +439,17 @@ __global__ void __launch_bounds__(2 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
         for (int e = 0; e < 2; ++e) {
             const int t = m * 16 + 8 * e + gl;
             if (t >= cnt) continue;
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int64_t at_n = static_cast<int64_t>(grp) * N + warp * 16 + 8 * n + q2;
-                if (w.dbc) {
-                    const int64_t plane = p.rows * p.G * N;
-                    float *d = w.dbc + split_i * plane + (start + t) * p.G * N + at_n;
-                    *reinterpret_cast<float2 *>(d) = make_float2(db[m][n][2 * e], db[m][n][2 * e + 1]);
-                    *reinterpret_cast<float2 *>(d + w.splits * plane) = make_float2(dc[m][n][2 * e], dc[m][n][2 * e + 1]);
-                } else {
-                    *reinterpret_cast<uint32_t *>(p.dB + (start + t) * p.db_stride + at_n) =
-                        bf_pair(db[m][n][2 * e], db[m][n][2 * e + 1]);
-                    *reinterpret_cast<uint32_t *>(p.dC + (start + t) * p.dc_stride + at_n) =
-                        bf_pair(dc[m][n][2 * e], dc[m][n][2 * e + 1]);
-                }
+            const int64_t at_n = static_cast<int64_t>(grp) * N + warp * 8 + q2;
+            if (w.dbc) {
+                const int64_t plane = p.rows * p.G * N;
+                float *d = w.dbc + split_i * plane + (start + t) * p.G * N + at_n;
+                *reinterpret_cast<float2 *>(d) = make_float2(db[m][2 * e], db[m][2 * e + 1]);
+                *reinterpret_cast<float2 *>(d + w.splits * plane) = make_float2(dc[m][2 * e], dc[m][2 * e + 1]);
+            } else {
+                *reinterpret_cast<uint32_t *>(p.dB + (start + t) * p.db_stride + at_n) =
+                    bf_pair(db[m][2 * e], db[m][2 * e + 1]);
+                *reinterpret_cast<uint32_t *>(p.dC + (start + t) * p.dc_stride + at_n) =
+                    bf_pair(dc[m][2 * e], dc[m][2 * e + 1]);
             }
         }
 }
@@ -500,14 +489,23 @@ __global__ void __launch_bounds__(256) scan_sum_kernel(ScanParams p, BwdWork w) 
     }
 }
 
-// CTAs that share a group's heads: as many as it takes for two CTAs per SM, each with a head at least
+// CTAs that share a group's heads: the number that leaves the longest-working SM the fewest (tile, head)s, with one
+// CTA per SM; the smallest such one, since each CTA's share of dB and dC is written and read again.
 int head_splits(int64_t rows, int64_t n, int32_t H, int32_t G) {
     const int64_t ctas = scan_cells(rows, n) * G;
-    int64_t s = ctas > 0 ? (2 * 148 + ctas - 1) / ctas : 1;
-    if (s > H / G) s = H / G;
-    // equal shares: no CTA without a head
-    const int64_t per = (H / G + s - 1) / s;
-    return static_cast<int>((H / G + per - 1) / per);
+    const int per_group = H / G;
+    int64_t best = 0;
+    int best_s = 1;
+    for (int s = 1; s <= per_group && s <= 32; ++s) {
+        const int per = (per_group + s - 1) / s;
+        if ((per_group + per - 1) / per != s) continue;   // a CTA without a head
+        const int64_t cost = (ctas * s + 147) / 148 * per;
+        if (s == 1 || cost < best) {
+            best = cost;
+            best_s = s;
+        }
+    }
+    return best_s;
 }
 
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
@@ -537,7 +535,7 @@ cudaError_t bwd_launch(const ScanParams &p, const BwdWork &w, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     const int64_t ctas = w.cells * p.G * w.splits;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    scan_bwd_kernel<N><<<static_cast<unsigned>(ctas), 2 * N, bytes, s>>>(p, w);
+    scan_bwd_kernel<N><<<static_cast<unsigned>(ctas), 4 * N, bytes, s>>>(p, w);
     return cudaGetLastError();
 }
 
@@ -560,8 +558,7 @@ cudaError_t launch_scan_bwd(const ScanParams &p, cudaStream_t s) {
     w.part = reinterpret_cast<float *>(ws + l.part);
     w.splits = l.splits;
     w.cells = scan_cells(p.rows, p.seqs.n);
-    cudaError_t err = launch_scan_states(p, false, states, pieces, s);
-    if (err == cudaSuccess) err = launch_scan_states(p, true, grads, pieces, s);
+    cudaError_t err = launch_scan_states(p, states, grads, pieces, s);
     if (err == cudaSuccess && w.cells > 0)
         err = by_state(p.N, [&](auto n) { return bwd_launch<decltype(n)::value>(p, w, s); });
     if (err == cudaSuccess && w.dbc && p.rows > 0) {

@@ -443,9 +443,14 @@ int64_t piece_tokens(int64_t rows, int64_t n, int64_t ctas, int64_t want, int ti
     if (seg < 256) seg = 256;
     return seg >= rows ? 0 : seg;
 }
-// the tcgen05 kernel: one CTA per SM, each with two runs of 64 columns
+// the tcgen05 kernels: one CTA per SM, each with two runs of 64 columns
 int64_t tc_piece_tokens(int64_t rows, int64_t n, int32_t H, int32_t P) {
     return piece_tokens(rows, n, (static_cast<int64_t>(H) * (P / PC) + 1) / 2, 2 * 148, kScanTcTile);
+}
+// the backward's runs of the state, both directions at once
+int64_t state_piece_tokens(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N) {
+    return N == 128 ? piece_tokens(rows, n, H * (P / PC), 96, T)
+                    : piece_tokens(rows, n, static_cast<int64_t>(H) * (P / PC), 4 * 148, T);
 }
 // the warp-level kernels: several CTAs per SM
 int64_t warp_piece_tokens(int64_t rows, int64_t n, int32_t H, int32_t P) {
@@ -460,13 +465,13 @@ size_t piece_bytes(int64_t rows, int64_t n, int64_t seg, int32_t H, int32_t P, i
 }
 
 template <int N, int S, bool kReverse>
-cudaError_t state_launch(const ScanParams &p, int64_t seg, int64_t units, const float *entering, float *leave,
-                         float *decay, float *states, cudaStream_t s) {
+cudaError_t state_launch(const ScanParams &p, int64_t seg, int64_t units, const ScanStateRun &r, cudaStream_t s) {
     constexpr int bytes = 2 * (T * N * 2 + T * PC * 2) + 2 * static_cast<int>(sizeof(Gates));
     auto *k = scan_state_kernel<N, S, kReverse>;
     cudaError_t err = allow_smem(k, bytes);
     if (err != cudaSuccess) return err;
-    k<<<static_cast<unsigned>(units * p.H * (p.P / PC)), NT, bytes, s>>>(p, seg, entering, leave, decay, states);
+    k<<<static_cast<unsigned>(units * p.H * (p.P / PC)), NT, bytes, s>>>(p, seg, r.entering, r.leave, r.leave_decay,
+                                                                          r.states);
     return cudaGetLastError();
 }
 
@@ -488,7 +493,8 @@ size_t scan_fwd_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, i
 }
 
 size_t scan_states_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N) {
-    return scan::piece_bytes(rows, n, scan::warp_piece_tokens(rows, n, H, P), H, P, N);
+    // both directions' pieces
+    return 2 * scan::piece_bytes(rows, n, scan::state_piece_tokens(rows, n, H, P, N), H, P, N);
 }
 
 cudaError_t launch_scan_fwd(const ScanParams &p, cudaStream_t s) {
@@ -502,15 +508,15 @@ cudaError_t launch_scan_fwd(const ScanParams &p, cudaStream_t s) {
     cudaError_t err = cudaSuccess;
     if (cut) {
         if (tc)
-            err = launch_scan_tc(p, false, seg, units, nullptr, ws, decay, s);
+            err = launch_scan_tc_state(p, exact ? 3 : 2, 1, seg, units, {nullptr, ws, decay, nullptr}, {}, s);
         else
-            err = exact ? state_launch<64, 3, false>(p, seg, units, nullptr, ws, decay, nullptr, s)
-                        : state_launch<64, 2, false>(p, seg, units, nullptr, ws, decay, nullptr, s);
+            err = exact ? state_launch<64, 3, false>(p, seg, units, {nullptr, ws, decay, nullptr}, s)
+                        : state_launch<64, 2, false>(p, seg, units, {nullptr, ws, decay, nullptr}, s);
         if (err == cudaSuccess) err = join_launch<false>(p, seg, ws, decay, s);
     }
     if (err != cudaSuccess) return err;
     const float *entering = cut ? ws : nullptr;
-    if (tc) return launch_scan_tc(p, true, seg, units, entering, nullptr, nullptr, s);
+    if (tc) return launch_scan_tc(p, seg, units, entering, s);
     auto *k = exact ? scan_fwd_kernel<64, 3> : scan_fwd_kernel<64, 2>;
     err = allow_smem(k, FwdSmem<64>::kBytes);
     if (err != cudaSuccess) return err;
@@ -518,28 +524,28 @@ cudaError_t launch_scan_fwd(const ScanParams &p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_scan_states(const ScanParams &p, bool reverse, float *states, float *ws, cudaStream_t s) {
+cudaError_t launch_scan_states(const ScanParams &p, float *states, float *grads, float *ws, cudaStream_t s) {
     using namespace scan;
-    const int64_t cut = warp_piece_tokens(p.rows, p.seqs.n, p.H, p.P), seg = cut ? cut : kWhole;
+    const int64_t cut = state_piece_tokens(p.rows, p.seqs.n, p.H, p.P, p.N), seg = cut ? cut : kWhole;
     const int64_t units = piece_count(p.rows, p.seqs.n, cut);
     if (units == 0) return cudaSuccess;
     if (units * p.H * (p.P / PC) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    float *decay = ws + units * p.H * p.N * p.P;
-    return by_state(p.N, [&](auto nn) {
-        constexpr int N = decltype(nn)::value;
-        cudaError_t err = cudaSuccess;
-        auto run = [&](auto rev) {
-            constexpr bool R = decltype(rev)::value;
-            if (cut) {
-                err = state_launch<N, 3, R>(p, seg, units, nullptr, ws, decay, nullptr, s);
-                if (err == cudaSuccess) err = join_launch<R>(p, seg, ws, decay, s);
-            }
-            if (err == cudaSuccess)
-                err = state_launch<N, 3, R>(p, seg, units, cut ? ws : nullptr, nullptr, nullptr, states, s);
-            return err;
-        };
-        return reverse ? run(std::true_type()) : run(std::false_type());
-    });
+    const int64_t all = units * p.H * p.N * p.P;
+    float *wf = ws, *df = wf + all, *wr = df + 4 * units * p.H, *dr = wr + all;
+    auto run = [&](bool local) {
+        const ScanStateRun f = local ? ScanStateRun{nullptr, wf, df, nullptr} : ScanStateRun{cut ? wf : nullptr, nullptr, nullptr, states};
+        const ScanStateRun r = local ? ScanStateRun{nullptr, wr, dr, nullptr} : ScanStateRun{cut ? wr : nullptr, nullptr, nullptr, grads};
+        if (p.N == 128) return launch_scan_tc_state(p, 3, 2, seg, units, f, r, s);
+        cudaError_t err = state_launch<64, 3, false>(p, seg, units, f, s);
+        return err == cudaSuccess ? state_launch<64, 3, true>(p, seg, units, r, s) : err;
+    };
+    cudaError_t err = cudaSuccess;
+    if (cut) {
+        err = run(true);
+        if (err == cudaSuccess) err = join_launch<false>(p, seg, wf, df, s);
+        if (err == cudaSuccess) err = join_launch<true>(p, seg, wr, dr, s);
+    }
+    return err == cudaSuccess ? run(false) : err;
 }
 
 cudaError_t read_and_clear_scan_error(unsigned int *value) {

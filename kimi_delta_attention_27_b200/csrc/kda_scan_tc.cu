@@ -24,29 +24,20 @@
 // more than 2^60 its elements take an exponential each instead.
 //
 // Every wait is bounded; one that runs out raises kErrTimeout and winds the CTA down.
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
-#include <string.h>
-
-#include "kda_scan.cuh"
-#include "sm100_ptx.cuh"
+#include "kda_scan_tc.cuh"
 
 namespace kda {
 namespace scan {
 namespace tc {
 
-using namespace ptx;
-
 __device__ unsigned int g_scan_tc_error = 0;
 
-constexpr int N = 128;                    // state size
 constexpr int TT = kScanTcTile;           // tokens per tile
 constexpr int NT = 608;                   // eight warps for each head, an issuing warp, two for the gates
 constexpr int kIssuer = 16, kFeeder = 17; // the others' first warps
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct TcGates {
     float hi[TT], lo[TT];   // log2 of the decay from the tile's start through token t, in two floats
@@ -59,7 +50,6 @@ struct TcGates {
     float pad[2];
 };
 
-constexpr uint32_t kBlock = 16384;        // 128 rows of 128 bytes: 64 bf16 columns
 template <int S>
 struct Smem {
     static constexpr uint32_t kC = 0, kB = 2 * kBlock, kX = 4 * kBlock;    // x: [head][stage]
@@ -83,53 +73,9 @@ struct Maps {
     CUtensorMap x, b, c;
 };
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
-        "mov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
-        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-__device__ __forceinline__ uint4 lds(const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
-__device__ __forceinline__ void sts(uint8_t *p, uint4 v) { *reinterpret_cast<uint4 *>(p) = v; }
-__device__ __forceinline__ float f32(uint32_t u) { return __uint_as_float(u); }
-__device__ __forceinline__ uint32_t sw128(int r, int j) { return static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4)); }
 // barriers, 8 bytes each behind Smem::kBars
 enum : int {
-    kBcFull = 0,        // C and B of a tile (state run: [stage], B alone)
+    kBcFull = 0,        // C and B of a tile
     kG = 2,             // G is there
     kXFull = 3,         // [head][stage] x
     kGates = 7,         // [head][stage] the gates
@@ -145,32 +91,6 @@ enum : int {
     kBarCount = 31
 };
 
-struct Ctx {
-    uint32_t bars;
-    volatile uint32_t *abort;
-    __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * i; }
-    // false: this or another wait of the CTA ran out
-    __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
-        if (mbar_try_wait(bar(i), parity)) return true;
-        const uint64_t t0 = globaltimer();
-        for (;;) {
-            if (mbar_try_wait(bar(i), parity)) return true;
-            if (*abort) return false;
-            if (globaltimer() - t0 > kWaitLimitNs) {
-                *abort = 1;
-                atomicOr(&g_scan_tc_error, kErrTimeout);
-                return false;
-            }
-        }
-    }
-    // by a converged warp, once for all its lanes: 256 threads' own arrivals at one address take their turns
-    // in shared memory, and cost more than all the work on elements
-    __device__ __forceinline__ void arrive(int i) const {
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(bar(i));
-    }
-};
-
 // the steps of a lane's tokens 4l .. 4l + 3 before bias and softplus (0 behind the tile)
 __device__ __forceinline__ void load_dt(const ScanParams &p, int64_t start, int cnt, int h, float (&dt)[4]) {
     const int t = 4 * (threadIdx.x & 31);
@@ -178,8 +98,8 @@ __device__ __forceinline__ void load_dt(const ScanParams &p, int64_t start, int 
     for (int j = 0; j < 4; ++j) dt[j] = t + j < cnt ? p.dt[(start + t + j) * p.H + h] : 0.f;
 }
 
-// The gates of a tile of cnt tokens, by one warp: lane l has tokens 4l .. 4l + 3. Returns log2 of its decay.
-__device__ __forceinline__ Two make_tc_gates(TcGates &g, const float (&dt)[4], int cnt, float bias, int softplus, Two a2) {
+// The gates of a tile of cnt tokens, by one warp: lane l has tokens 4l .. 4l + 3.
+__device__ __forceinline__ void make_tc_gates(TcGates &g, const float (&dt)[4], int cnt, float bias, int softplus, Two a2) {
     const int lane = threadIdx.x & 31;
     float d[4];
     Two c[4];
@@ -215,14 +135,11 @@ __device__ __forceinline__ Two make_tc_gates(TcGates &g, const float (&dt)[4], i
         g.total = ex2(total);
         g.steep = (steep & 1u) | ((steep >> 7) & 2u) | ((steep >> 14) & 4u) | ((steep >> 21) & 8u);
     }
-    return total;
 }
 
-// kOut: the outputs and the final state. Otherwise the state that a piece adds, from zero (leave, and its decay).
-template <bool kOut, int S>
+template <int S>
 __global__ void __launch_bounds__(NT, 1)
-    scan_tc_kernel(ScanParams p, const __grid_constant__ Maps maps, int64_t seg, const float *entering, float *leave,
-                   float *leave_decay) {
+    scan_tc_kernel(ScanParams p, const __grid_constant__ Maps maps, int64_t seg, const float *entering) {
     extern __shared__ __align__(1024) uint8_t smem[];
     using L = Smem<S>;
     const uint32_t base = smem_u32(smem);
@@ -230,6 +147,7 @@ __global__ void __launch_bounds__(NT, 1)
     Ctx x;
     x.bars = base + L::kBars;
     x.abort = &s_abort;
+    x.error = &g_scan_tc_error;
     TcGates *gates = reinterpret_cast<TcGates *>(smem + L::kGates);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (blockIdx.x == 0) check_offsets(p.seqs, &g_scan_tc_error);
@@ -240,7 +158,7 @@ __global__ void __launch_bounds__(NT, 1)
     const int gp = static_cast<int>(blockIdx.x % (p.G * pairs)), grp = gp / pairs, in_group = gp % pairs * 2;
     const int v0 = grp * per_group + in_group, heads = in_group + 1 < per_group ? 2 : 1;
     const Piece u = find_piece(p.seqs, unit, seg);
-    if (u.none || (!kOut && u.last)) return;
+    if (u.none) return;
     const int64_t c_first = u.a / TT;
     const int tiles = static_cast<int>(u.b > u.a ? (u.b + TT - 1) / TT - c_first : 0);
     auto start_of = [&](int i) { return (c_first + i) * TT > u.a ? (c_first + i) * TT : u.a; };
@@ -263,7 +181,6 @@ __global__ void __launch_bounds__(NT, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const uint32_t bc_bytes = kOut ? 4 * kBlock : 2 * kBlock;
 
     if (warp < kIssuer) {
         // ---------------------------------------------------------------- a head's elements
@@ -280,9 +197,9 @@ __global__ void __launch_bounds__(NT, 1)
             const float Dh = p.D ? p.D[h] : 0.f;
             float2 s[16];         // this thread's part of the state
             {
-                const void *src = kOut && !entering ? p.h0 : entering;
-                const bool fp32 = !(kOut && !entering) || p.h0_fp32;
-                const int64_t e = ((kOut && !entering ? static_cast<int64_t>(u.i) : unit) * p.H + h) * sn +
+                const void *src = entering ? entering : p.h0;
+                const bool fp32 = entering || p.h0_fp32;
+                const int64_t e = ((entering ? unit : static_cast<int64_t>(u.i)) * p.H + h) * sn +
                                   static_cast<int64_t>(r) * p.P + col;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -388,7 +305,7 @@ __global__ void __launch_bounds__(NT, 1)
                 return true;
             };
             bool ok = true;
-            if (kOut && tiles > 0) publish();
+            if (tiles > 0) publish();
             for (int i = 0; i < tiles && ok; ++i) {
                 const int stage = i & 1, cnt = count_of(i);
                 const uint32_t ph = i & 1, ph2 = (i >> 1) & 1;
@@ -398,15 +315,15 @@ __global__ void __launch_bounds__(NT, 1)
                 if (!ok) break;
                 if (cnt < TT && hd == 0) {
                     // rows of B behind the piece: whatever they hold would multiply zeros below
-                    ok = x.wait(kOut ? kBcFull : kBcFull + stage, kOut ? ph : ph2);
+                    ok = x.wait(kBcFull, ph);
                     if (!ok) break;
-                    uint8_t *bt = smem + (kOut || stage == 0 ? L::kB : L::kC) + hf * kBlock;
+                    uint8_t *bt = smem + L::kB + hf * kBlock;
                     if (r >= cnt)
 #pragma unroll
                         for (int j = 0; j < 8; ++j) sts(bt + r * 128 + j * 16, make_uint4(0u, 0u, 0u, 0u));
                 }
                 write_parts(0, xt, g, cnt);
-                if (kOut && i > 0) {
+                if (i > 0) {
                     ok = finish(i - 1);
                     if (!ok) break;
                 }
@@ -424,11 +341,6 @@ __global__ void __launch_bounds__(NT, 1)
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 16; ++j) s[j] = fma2(s[j], tot, make_float2(f32(a[2 * j]), f32(a[2 * j + 1])));
-                }
-                if (!kOut) {
-                    tc_fence_before();
-                    x.arrive(kXFree + hd * 2 + stage);
-                    continue;
                 }
                 // the state's copy: C S_0 of this tile has been computed, as the product behind it has
                 if (i + 1 < tiles) publish();
@@ -490,12 +402,12 @@ __global__ void __launch_bounds__(NT, 1)
                 tc_fence_before();
                 x.arrive(kM + hd);
             }
-            if (kOut && ok && tiles > 0) ok = finish(tiles - 1);
+            if (ok && tiles > 0) ok = finish(tiles - 1);
             // the state that leaves
-            void *dst = kOut ? (u.last ? p.hT : nullptr) : leave;
+            void *dst = u.last ? p.hT : nullptr;
             if (ok && dst) {
-                const bool fp32 = !kOut || p.hT_fp32;
-                const int64_t e = ((kOut ? static_cast<int64_t>(u.i) : unit) * p.H + h) * sn + static_cast<int64_t>(r) * p.P + col;
+                const bool fp32 = p.hT_fp32;
+                const int64_t e = (static_cast<int64_t>(u.i) * p.H + h) * sn + static_cast<int64_t>(r) * p.P + col;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     if (fp32)
@@ -512,25 +424,21 @@ __global__ void __launch_bounds__(NT, 1)
         const int bcol = grp * N;
         auto load_bc = [&](int i) {
             if (!elect_one()) return;
-            const int bar = kOut ? kBcFull : kBcFull + (i & 1);
             const int32_t row = static_cast<int32_t>(start_of(i));
-            mbar_arrive_expect_tx(x.bar(bar), bc_bytes);
-            const uint32_t bt = base + (kOut || (i & 1) == 0 ? L::kB : L::kC);
+            mbar_arrive_expect_tx(x.bar(kBcFull), 4 * kBlock);
             for (int k = 0; k < 2; ++k) {
-                if (kOut) tma_load_2d(base + L::kC + k * kBlock, &maps.c, x.bar(bar), bcol + 64 * k, row);
-                tma_load_2d(bt + k * kBlock, &maps.b, x.bar(bar), bcol + 64 * k, row);
+                tma_load_2d(base + L::kC + k * kBlock, &maps.c, x.bar(kBcFull), bcol + 64 * k, row);
+                tma_load_2d(base + L::kB + k * kBlock, &maps.b, x.bar(kBcFull), bcol + 64 * k, row);
             }
         };
         bool ok = true;
         if (tiles > 0) load_bc(0);
-        if (!kOut && tiles > 1) load_bc(1);
         for (int i = 0; i < tiles && ok; ++i) {
-            const uint32_t ph = i & 1, ph2 = (i >> 1) & 1;
-            const uint32_t bt = base + (kOut || ph == 0 ? L::kB : L::kC);
-            ok = x.wait(kOut ? kBcFull : kBcFull + static_cast<int>(ph), kOut ? ph : ph2);
+            const uint32_t ph = i & 1, bt = base + L::kB;
+            ok = x.wait(kBcFull, ph);
             if (!ok) break;
             __syncwarp();
-            if (kOut) {
+            {
                 // G: the last tile's has been read (its M is written)
                 tc_fence_after();
                 if (elect_one()) {
@@ -561,13 +469,13 @@ __global__ void __launch_bounds__(NT, 1)
             };
             for (int hd = 0; hd < heads && ok; ++hd) {
                 // U takes the place of the last tile's M, which has been multiplied
-                ok = x.wait(kP0 + hd, ph) && (!kOut || i == 0 || x.wait(kY + hd, (i - 1) & 1));
+                ok = x.wait(kP0 + hd, ph) && (i == 0 || x.wait(kY + hd, (i - 1) & 1));
                 if (!ok) break;
                 tc_fence_after();
                 product_u(hd, 0);
             }
             for (int hd = 0; hd < heads && ok; ++hd) {
-                if (kOut) {
+                {
                     ok = x.wait(kS + hd, ph) && (i == 0 || x.wait(kYFree + hd, (i - 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
@@ -588,15 +496,14 @@ __global__ void __launch_bounds__(NT, 1)
             }
             if (!ok) break;
             // the last commit covers every product so far: C and B are free
-            const int next = kOut ? i + 1 : i + 2;
-            if (next < tiles) {
+            if (i + 1 < tiles) {
                 ok = x.wait(kU + heads - 1, ph);
                 if (!ok) break;
                 __syncwarp();
-                load_bc(next);
+                load_bc(i + 1);
                 __syncwarp();
             }
-            if (kOut) {
+            {
                 for (int hd = 0; hd < heads && ok; ++hd) {
                     ok = x.wait(kM + hd, ph);
                     if (!ok) break;
@@ -618,7 +525,6 @@ __global__ void __launch_bounds__(NT, 1)
         const int hd = warp - kFeeder, v = v0 + hd, h = v / slices;
         const Two rate = log2_rate(p.A[h]);
         const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-        Two decay = {0.f, 0.f};
         float dt[4];
         bool ok = true;
         if (tiles > 0) load_dt(p, start_of(0), count_of(0), h, dt);
@@ -636,10 +542,9 @@ __global__ void __launch_bounds__(NT, 1)
             __syncwarp();
             const float now[4] = {dt[0], dt[1], dt[2], dt[3]};
             if (i + 1 < tiles) load_dt(p, start_of(i + 1), count_of(i + 1), h, dt);
-            decay = decay + make_tc_gates(gates[hd * 2 + stage], now, count_of(i), bias, p.softplus, rate);
+            make_tc_gates(gates[hd * 2 + stage], now, count_of(i), bias, p.softplus, rate);
             x.arrive(kGates + hd * 2 + stage);
         }
-        if (!kOut && ok && lane == 0 && v % slices == 0) leave_decay[unit * p.H + h] = ex2(decay);
     }
     if (s_abort) {
         // copies may still be in flight into this CTA's shared memory
@@ -653,58 +558,27 @@ __global__ void __launch_bounds__(NT, 1)
     if (warp == kIssuer) tmem_dealloc(tmem, kCols);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            ptr = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }();
-    return fn;
-}
-
-// rows of `cols` bf16 elements, `stride` apart, in boxes of 128 rows x 64 columns (one swizzled block)
-bool encode(CUtensorMap *map, const void *at, int64_t cols, int64_t rows, int64_t stride) {
-    auto enc = encoder();
-    if (!enc) return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows > 1 ? stride : cols) * 2};
-    const cuuint32_t box[2] = {64, TT}, step[2] = {1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(at), dims, strides, box, step,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <bool kOut, int S>
-cudaError_t launch(const ScanParams &p, int64_t seg, int64_t units, const float *entering, float *leave, float *decay,
-                   cudaStream_t s) {
+template <int S>
+cudaError_t launch(const ScanParams &p, int64_t seg, int64_t units, const float *entering, cudaStream_t s) {
     Maps maps;
     memset(&maps, 0, sizeof(maps));
-    if (p.rows > 0 && (!encode(&maps.x, p.x, static_cast<int64_t>(p.H) * p.P, p.rows, p.x_stride) ||
-                       !encode(&maps.b, p.B, static_cast<int64_t>(p.G) * N, p.rows, p.b_stride) ||
-                       !encode(&maps.c, p.C, static_cast<int64_t>(p.G) * N, p.rows, p.c_stride)))
+    if (p.rows > 0 && (!encode(&maps.x, p.x, static_cast<int64_t>(p.H) * p.P, p.rows, p.x_stride, TT) ||
+                       !encode(&maps.b, p.B, static_cast<int64_t>(p.G) * N, p.rows, p.b_stride, TT) ||
+                       !encode(&maps.c, p.C, static_cast<int64_t>(p.G) * N, p.rows, p.c_stride, TT)))
         return cudaErrorInvalidValue;
-    auto *k = scan_tc_kernel<kOut, S>;
-    cudaError_t err = allow_smem(k, Smem<S>::kBytes);
+    cudaError_t err = allow_smem(scan_tc_kernel<S>, Smem<S>::kBytes);
     if (err != cudaSuccess) return err;
     const int64_t pairs = (p.H / p.G * (p.P / PC) + 1) / 2;
-    k<<<static_cast<unsigned>(units * p.G * pairs), NT, Smem<S>::kBytes, s>>>(p, maps, seg, entering, leave, decay);
+    scan_tc_kernel<S><<<static_cast<unsigned>(units * p.G * pairs), NT, Smem<S>::kBytes, s>>>(p, maps, seg, entering);
     return cudaGetLastError();
 }
 
 }  // namespace tc
 }  // namespace scan
 
-cudaError_t launch_scan_tc(const ScanParams &p, bool out, int64_t seg, int64_t units, const float *entering, float *leave,
-                           float *decay, cudaStream_t s) {
+cudaError_t launch_scan_tc(const ScanParams &p, int64_t seg, int64_t units, const float *entering, cudaStream_t s) {
     using namespace scan::tc;
-    if (p.hT && p.hT_fp32)
-        return out ? launch<true, 3>(p, seg, units, entering, leave, decay, s)
-                   : launch<false, 3>(p, seg, units, entering, leave, decay, s);
-    return out ? launch<true, 2>(p, seg, units, entering, leave, decay, s)
-               : launch<false, 2>(p, seg, units, entering, leave, decay, s);
+    return p.hT && p.hT_fp32 ? launch<3>(p, seg, units, entering, s) : launch<2>(p, seg, units, entering, s);
 }
 
 cudaError_t read_and_clear_scan_tc_error(unsigned int *value) {

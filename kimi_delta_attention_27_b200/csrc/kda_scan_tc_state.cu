@@ -1,0 +1,364 @@
+// kda_scan_tc_state.cu -- the scan's state alone, state size 128, on tcgen05, sm_100a.
+//
+// Two uses: what each piece of a cut sequence adds to the state (kda_scan_fwd.cu), and, for the backward, the
+// state S entering every tile of 64 tokens and the gradient R of the state leaving it:
+//
+//   S_end = e^(Gamma_end) S_0 + B^T Diag(d e^(Gamma_end - Gamma)) x          tiles in order
+//   R_0   = e^(Gamma_end) R_end + C^T Diag(e^Gamma) dy                       tiles backwards (blockIdx.y 1)
+//
+// per 64 columns of a head, U = rows^T Diag(weight) cols being one tcgen05 product (128 x 64, K 64), with the
+// weighted columns in S bf16 parts (three: 24 bits). The state stays fp32 in the registers of 256 threads.
+//
+// Bound by the product: its operands come from shared memory, 128 bytes a cycle. So a CTA takes two heads of a
+// group side by side (one product with N = 128 reads the rows once for both: 64 cycles per K step and
+// part instead of 2 x 48), 768 cycles per tile with three parts. Eight warps per head form the parts of the
+// next tile while this one's product runs, then add U to the state; four warps run ahead with gates and loads.
+//
+// Every wait is bounded; one that runs out raises kErrTimeout and winds the CTA down.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "kda_scan_tc.cuh"
+
+namespace kda {
+namespace scan {
+namespace tc {
+
+__device__ unsigned int g_scan_state_error = 0;
+
+constexpr int kIssuer = 16, kFeeder = 17, NT = 32 * 21;
+constexpr int kRowStages = 3;
+
+struct StateGates {
+    float weight[T];
+    float total;
+    float pad[3];
+};
+
+constexpr uint32_t kTile = T * 128;       // 64 rows of 128 bytes
+template <int S>
+struct StateSmem {
+    static constexpr uint32_t kRows = 0;                                   // [stage] 64 x 128: two blocks of columns
+    static constexpr uint32_t kCols = kRows + kRowStages * 2 * kTile;      // [head][stage]
+    static constexpr uint32_t kParts = kCols + 4 * kTile;                  // [stage][S][head]
+    static constexpr uint32_t kOut = kParts + 2 * S * 2 * kTile;           // [warp] 32 rows x 64 bytes of the state
+    static constexpr uint32_t kGates = kOut + 16 * 2048;                   // [head][4]
+    static constexpr uint32_t kBars = kGates + 8 * sizeof(StateGates);
+    static constexpr uint32_t kBytes = kBars + 256;
+    static_assert(kBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
+};
+
+enum : int {
+    kRowsFull = 0,      // [stage]
+    kColsFull = 3,      // [head][stage]
+    kGatesFull = 7,     // [head][4]
+    kU = 15,            // [stage] the product is done
+    kColsFree = 17,     // [head][stage], the head's eight warps: the columns and gates have been used
+    kParts = 21,        // [stage], all element warps: the parts are written
+    kBarCount = 23
+};
+
+struct StateMaps {
+    CUtensorMap rows[2], cols[2];   // B and x; C and dy
+};
+
+template <int S>
+__global__ void __launch_bounds__(NT, 1)
+    scan_state_tc_kernel(ScanParams p, const __grid_constant__ StateMaps maps, int64_t seg, ScanStateRun run0,
+                         ScanStateRun run1) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    using L = StateSmem<S>;
+    const uint32_t base = smem_u32(smem);
+    __shared__ uint32_t s_tmem, s_abort;
+    __shared__ Two s_decay[4];
+    Ctx x;
+    x.bars = base + L::kBars;
+    x.abort = &s_abort;
+    x.error = &g_scan_state_error;
+    StateGates *gates = reinterpret_cast<StateGates *>(smem + L::kGates);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seqs, &g_scan_state_error);
+
+    const bool rev = blockIdx.y == 1;
+    const ScanStateRun &run = rev ? run1 : run0;
+    const int slices = p.P / PC, per_group = p.H / p.G * slices, pairs = (per_group + 1) / 2;
+    const int64_t unit = blockIdx.x / (p.G * pairs);
+    const int gp = static_cast<int>(blockIdx.x % (p.G * pairs)), grp = gp / pairs, in_group = gp % pairs * 2;
+    const int v0 = grp * per_group + in_group, heads = in_group + 1 < per_group ? 2 : 1;
+    const Piece u = find_piece(p.seqs, unit, seg);
+    const bool head = rev ? u.last : u.first, tail = rev ? u.first : u.last;
+    if (u.none || (run.leave && tail)) return;
+    const int64_t lo = u.a / T;
+    const int tiles = static_cast<int>(u.b > u.a ? (u.b + T - 1) / T - lo : 0);
+    auto cell = [&](int i) { return rev ? lo + tiles - 1 - i : lo + i; };
+
+    if (warp == kIssuer) {
+        if (lane == 0) {
+            for (int i = 0; i < kBarCount; ++i) mbar_init(x.bar(i), i < kColsFree ? 1 : i < kParts ? 8 : 8 * heads);
+            s_abort = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
+        tmem_alloc(smem_u32(&s_tmem), 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+
+    if (warp < kIssuer) {
+        // ---------------------------------------------------------------- a head's elements
+        // thread: row r of the state, columns 32 hf .. + 32
+        const int hd = warp >> 3, hf = (warp >> 2) & 1, wq = warp & 3, r = wq * 32 + lane, t256 = tid & 255;
+        if (hd < heads) {
+            const int v = v0 + hd, h = v / slices, col = v % slices * PC + 32 * hf;
+            const uint32_t tU = tmem + hd * 64 + 32 * hf + (static_cast<uint32_t>(wq * 32) << 16);
+            const int64_t sn = static_cast<int64_t>(N) * p.P, at_r = static_cast<int64_t>(r) * p.P + col;
+            float2 s[16];
+            {
+                const void *init = rev ? static_cast<const void *>(p.dhT) : p.h0;
+                const void *src = run.entering ? run.entering : head && !run.leave ? init : nullptr;
+                const bool fp32 = run.entering || rev || p.h0_fp32;
+                const int64_t e = ((run.entering ? unit : static_cast<int64_t>(u.i)) * p.H + h) * sn + at_r;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (src && fp32) {
+                        f = reinterpret_cast<const float4 *>(static_cast<const float *>(src) + e)[j];
+                    } else if (src) {
+                        const uint2 w = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(src) + e)[j];
+                        f = make_float4(bf_low(w.x), bf_high(w.x), bf_low(w.y), bf_high(w.y));
+                    }
+                    s[2 * j] = make_float2(f.x, f.y);
+                    s[2 * j + 1] = make_float2(f.z, f.w);
+                }
+            }
+            float total = 0.f, next_total = 0.f;
+            // the weighted columns of tile i in parts; four threads per token
+            auto write_parts = [&](int i) {
+                const int64_t c = cell(i);
+                const int cnt = tile_count(u, c), row = t256 >> 2;
+                if (!x.wait(kColsFull + hd * 2 + (i & 1), (i >> 1) & 1) || !x.wait(kGatesFull + hd * 4 + (i & 3), (i >> 2) & 1))
+                    return false;
+                if (cnt < T && hd == 0) {
+                    // rows behind the piece: whatever they hold would multiply zeros below
+                    if (!x.wait(kRowsFull + i % kRowStages, (i / kRowStages) & 1)) return false;
+                    uint8_t *rt = smem + L::kRows + (i % kRowStages) * 2 * kTile + row * 128;
+                    if (row >= cnt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) sts(rt + (j >> 1) * kTile + ((t256 & 3) * 2 + (j & 1)) * 16, make_uint4(0u, 0u, 0u, 0u));
+                }
+                const StateGates &g = gates[hd * 4 + (i & 3)];
+                const uint8_t *ct = smem + L::kCols + (hd * 2 + (i & 1)) * kTile;
+                uint8_t *parts = smem + L::kParts + (i & 1) * S * 2 * kTile + hd * kTile;
+                const float w = g.weight[row];
+                next_total = g.total;
+                const float2 w2 = make_float2(w, w), minus1 = make_float2(-1.f, -1.f);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int chunk = (t256 & 3) * 2 + j;   // two rows' chunks of a turn lie in different banks
+                    uint32_t o[S][4];
+                    if (row < cnt) {
+                        const uint4 q = lds(ct + sw128(row, chunk));
+                        const uint32_t in[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float2 f = mul2(make_float2(bf_low(in[k]), bf_high(in[k])), w2);
+#pragma unroll
+                            for (int e = 0; e < S; ++e) {
+                                o[e][k] = bf_pair(f.x, f.y);
+                                if (e + 1 < S) f = fma2(make_float2(bf_low(o[e][k]), bf_high(o[e][k])), minus1, f);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < S; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0u;
+                    }
+#pragma unroll
+                    for (int e = 0; e < S; ++e)
+                        sts(parts + e * 2 * kTile + sw128(row, chunk), make_uint4(o[e][0], o[e][1], o[e][2], o[e][3]));
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                x.arrive(kParts + (i & 1));
+                x.arrive(kColsFree + hd * 2 + (i & 1));
+                return true;
+            };
+            bool ok = tiles == 0 || write_parts(0);
+            for (int i = 0; i < tiles && ok; ++i) {
+                total = next_total;
+                if (i + 1 < tiles) ok = write_parts(i + 1);
+                if (!ok) break;
+                if (run.states) {
+                    // 32 rows x 16 columns at a time by way of shared memory, for runs of 64 bytes
+                    uint8_t *st = smem + L::kOut + warp * 2048;
+                    float *dst = run.states + ((u.i + cell(i)) * p.H + h) * sn + static_cast<int64_t>(wq * 32) * p.P + col;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<float4 *>(st + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                                make_float4(s[8 * q + 2 * j].x, s[8 * q + 2 * j].y, s[8 * q + 2 * j + 1].x, s[8 * q + 2 * j + 1].y);
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int row = j * 8 + (lane >> 2);
+                            *reinterpret_cast<float4 *>(dst + static_cast<int64_t>(row) * p.P + 16 * q + (lane & 3) * 4) =
+                                *reinterpret_cast<const float4 *>(st + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+                        }
+                    }
+                }
+                ok = x.wait(kU + (i & 1), (i >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t a[32];
+                tmem_ld32(tU + (i & 1) * 128, a);
+                const float2 tot = make_float2(total, total);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[j] = fma2(s[j], tot, make_float2(f32(a[2 * j]), f32(a[2 * j + 1])));
+            }
+            float *dst = run.leave ? run.leave : rev && tail ? p.dh0 : nullptr;
+            if (ok && dst) {
+                const int64_t e = ((run.leave ? unit : static_cast<int64_t>(u.i)) * p.H + h) * sn + at_r;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    reinterpret_cast<float4 *>(dst + e)[j] = make_float4(s[2 * j].x, s[2 * j].y, s[2 * j + 1].x, s[2 * j + 1].y);
+            }
+        }
+    } else if (warp == kIssuer) {
+        // ---------------------------------------------------------------- loads of the rows, and the products
+        auto load_rows = [&](int i) {
+            if (elect_one()) {
+                const int st = i % kRowStages;
+                const uint32_t bar = x.bar(kRowsFull + st), dst = base + L::kRows + st * 2 * kTile;
+                const int32_t row = static_cast<int32_t>(tile_start(u, cell(i)));
+                mbar_arrive_expect_tx(bar, 2 * kTile);
+                for (int k = 0; k < 2; ++k) tma_load_2d(dst + k * kTile, &maps.rows[rev], bar, grp * N + 64 * k, row);
+            }
+            __syncwarp();
+        };
+        const uint32_t id = idesc_f16(128, heads == 2 ? 128 : 64, 1, 1, 1);
+        bool ok = true;
+        for (int i = 0; i < 2 && i < tiles; ++i) load_rows(i);
+        for (int i = 0; i < tiles && ok; ++i) {
+            const int st = i & 1;
+            ok = x.wait(kRowsFull + i % kRowStages, (i / kRowStages) & 1) && x.wait(kParts + st, (i >> 1) & 1);
+            if (!ok) break;
+            __syncwarp();
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t rt = base + L::kRows + (i % kRowStages) * 2 * kTile;
+                const uint32_t parts = base + L::kParts + st * S * 2 * kTile;
+#pragma unroll
+                for (int k = 0; k < T / 16; ++k)
+#pragma unroll
+                    for (int e = S - 1; e >= 0; --e)
+                        mma_f16(tmem + st * 128, smem_desc(rt + k * 2048, kTile, 1024, kSwizzle128),
+                                smem_desc(parts + e * 2 * kTile + k * 2048, kTile, 1024, kSwizzle128), id,
+                                !(k == 0 && e == S - 1));
+                mma_commit(x.bar(kU + st));
+            }
+            __syncwarp();
+            if (i + 2 < tiles) {
+                // its stage held the last tile's rows
+                if (i > 0) ok = x.wait(kU + ((i - 1) & 1), ((i - 1) >> 1) & 1);
+                if (!ok) break;
+                __syncwarp();
+                load_rows(i + 2);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- a head's gates and columns, every other tile
+        const int f = warp - kFeeder, hd = f >> 1, v = v0 + hd;
+        if (hd < heads) {
+            const int h = v / slices;
+            const Two rate = log2_rate(p.A[h]);
+            Two decay = {0.f, 0.f};
+            bool ok = true;
+            float d0 = 0.f, d1 = 0.f;
+            auto steps = [&](int i) {
+                const int64_t c = cell(i);
+                load_steps(p, tile_start(u, c), tile_count(u, c), h, d0, d1);
+            };
+            if ((f & 1) < tiles) steps(f & 1);
+            for (int i = f & 1; i < tiles; i += 2) {
+                StateGates &g = gates[hd * 4 + (i & 3)];
+                const Two l0 = log_decay(d0, rate), l1 = log_decay(d1, rate);
+                const Two sum = scan_lanes(l0 + l1), all = shfl(sum, 31);
+                const Two before = {__shfl_up_sync(0xffffffffu, sum.hi, 1), __shfl_up_sync(0xffffffffu, sum.lo, 1)};
+                const Two first = lane ? before + l0 : l0;
+                const float w0 = rev ? ex2(first) : d0 * ex2(minus(all, first));
+                const float w1 = rev ? ex2(sum) : d1 * ex2(minus(all, sum));
+                reinterpret_cast<float2 *>(g.weight)[lane] = make_float2(w0, w1);
+                if (lane == 0) g.total = ex2(all);
+                decay = decay + all;
+                x.arrive(kGatesFull + hd * 4 + (i & 3));
+                if (i >= 2) ok = x.wait(kColsFree + hd * 2 + (i & 1), ((i - 2) >> 1) & 1);
+                if (!ok) break;
+                __syncwarp();
+                if (elect_one()) {
+                    const int bar = kColsFull + hd * 2 + (i & 1);
+                    mbar_arrive_expect_tx(x.bar(bar), kTile);
+                    tma_load_2d(base + L::kCols + (hd * 2 + (i & 1)) * kTile, &maps.cols[rev], x.bar(bar), v * PC,
+                                static_cast<int32_t>(tile_start(u, cell(i))));
+                }
+                __syncwarp();
+                if (i + 2 < tiles) steps(i + 2);
+            }
+            if (lane == 0) s_decay[f] = decay;
+        }
+    }
+    if (s_abort) {
+        // copies may still be in flight into this CTA's shared memory
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 20000000ull) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kIssuer) tmem_dealloc(tmem, 256);
+    if (run.leave && tid < heads && (v0 + tid) % slices == 0)
+        run.leave_decay[unit * p.H + (v0 + tid) / slices] = ex2(s_decay[2 * tid] + s_decay[2 * tid + 1]);
+}
+
+template <int S>
+cudaError_t state_launch(const ScanParams &p, int directions, int64_t seg, int64_t units, const ScanStateRun &fwd,
+                         const ScanStateRun &rev, cudaStream_t s) {
+    StateMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    const int64_t hp = static_cast<int64_t>(p.H) * p.P, gn = static_cast<int64_t>(p.G) * N;
+    if (p.rows > 0 && (!encode(&maps.rows[0], p.B, gn, p.rows, p.b_stride, T) ||
+                       !encode(&maps.cols[0], p.x, hp, p.rows, p.x_stride, T) ||
+                       (directions > 1 && (!encode(&maps.rows[1], p.C, gn, p.rows, p.c_stride, T) ||
+                                           !encode(&maps.cols[1], p.dout, hp, p.rows, p.dout_stride, T)))))
+        return cudaErrorInvalidValue;
+    cudaError_t err = allow_smem(scan_state_tc_kernel<S>, StateSmem<S>::kBytes);
+    if (err != cudaSuccess) return err;
+    const int64_t pairs = (p.H / p.G * (p.P / PC) + 1) / 2;
+    const dim3 grid(static_cast<unsigned>(units * p.G * pairs), static_cast<unsigned>(directions));
+    scan_state_tc_kernel<S><<<grid, NT, StateSmem<S>::kBytes, s>>>(p, maps, seg, fwd, rev);
+    return cudaGetLastError();
+}
+
+}  // namespace tc
+}  // namespace scan
+
+cudaError_t launch_scan_tc_state(const ScanParams &p, int parts, int directions, int64_t seg, int64_t units,
+                                 const ScanStateRun &fwd, const ScanStateRun &rev, cudaStream_t s) {
+    using namespace scan::tc;
+    return parts == 3 ? state_launch<3>(p, directions, seg, units, fwd, rev, s)
+                      : state_launch<2>(p, directions, seg, units, fwd, rev, s);
+}
+
+cudaError_t read_and_clear_scan_state_error(unsigned int *value) {
+    cudaError_t err = cudaMemcpyFromSymbol(value, scan::tc::g_scan_state_error, sizeof(*value));
+    if (err != cudaSuccess || *value == 0) return err;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(scan::tc::g_scan_state_error, &zero, sizeof(zero));
+}
+
+}  // namespace kda
