@@ -5,12 +5,14 @@
 //   pre_t = bias + sum_{k < W} w_k e_{t-W+1+k},   out_t = pre_t sigmoid(pre_t)  (or pre_t)
 //
 // All three kernels are bound by HBM: 2 W operations and one sigmoid per element against 4 bytes
-// (bf16, forward). A thread owns 8 channels (4 in the backward) and walks a run of tokens with the
+// (bf16, forward). A thread owns 4 channels (8 for single tokens) and walks a run of tokens with the
 // last W - 1 inputs in registers, so x is read once but for the W - 1 rows before each run, which
 // the neighbouring warp has just read. The loads of the next tokens are issued together, before any
 // of them is used. Sums are fp32; each output is rounded once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "kda_conv.h"
 
@@ -19,11 +21,57 @@ namespace conv {
 
 __device__ unsigned int g_conv_error = 0;
 
-constexpr int V = 8;              // channels per thread, forward and decode
+constexpr int V = 8;              // channels per thread, single tokens
+constexpr int FV = 4;             // and forward: with 8 the taps and windows take twice the registers (279 us at 71,000 x 4096)
 constexpr int FW = 4;             // warps per CTA, forward
-constexpr int U = 4;              // tokens whose loads are issued together
+constexpr int U = 4;              // tokens of a batch
+constexpr int kRing = 4;          // batches of loads in flight
 
-__device__ __forceinline__ float sigmoidf(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// A thread's own window into shared memory for the rows it will need: asynchronous copies keep kRing batches of
+// rows in flight without a register for any of them. Every thread reads back what it copied itself, so no
+// barrier is needed. (With the same rows in registers, 8 tokens ahead: 275 us instead of the figure above.)
+template <class T, int N, int kRows>
+struct Ring {
+    static constexpr int kBytes = N * sizeof(T);
+    uint32_t at;    // this thread's place in row 0; rows are 32 * kBytes apart
+    __device__ __forceinline__ uint32_t slot(int j) const {
+        return at + static_cast<uint32_t>(j & (kRows - 1)) * (32 * kBytes);
+    }
+    __device__ __forceinline__ void copy(int j, const void *src, int64_t off) const {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(slot(j)),
+                     "l"(static_cast<const T *>(src) + off), "n"(kBytes)
+                     : "memory");
+    }
+    __device__ __forceinline__ void get(int j, float (&x)[N]) const {
+        if constexpr (sizeof(T) == 4) {
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                         : "r"(slot(j)));
+        } else {
+            uint32_t a, b;
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(slot(j)));
+            x[0] = bf_low(a);
+            x[1] = bf_high(a);
+            x[2] = bf_low(b);
+            x[3] = bf_high(b);
+        }
+    }
+};
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the `kLeft` youngest batches have arrived
+template <int kLeft>
+__device__ __forceinline__ void ring_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// 1 / (1 + e^-x) by the hardware's 2^y and 1/y (relative errors about 2^-22 each). With the flushing forms: those
+// that keep denormals bring three times the instructions, which then bound the kernel.
+__device__ __forceinline__ float sigmoidf(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
 
 template <int W, int N>
 __device__ __forceinline__ void load_taps(const ConvParams &p, int ch, float (&w)[W][N], float (&b)[N]) {
@@ -61,12 +109,12 @@ __device__ __forceinline__ void load_before(const ConvParams &p, int32_t i, int6
     raw.get(e);
 }
 
-// grid (token blocks + sequence blocks, channel blocks of 256). Token blocks: warp w walks `run` tokens.
+// grid (token blocks + sequence blocks, channel blocks of 128). Token blocks: warp w walks `run` tokens.
 // Sequence blocks: warp w copies the final state of one sequence.
 template <class T, int W, bool kSilu>
 __global__ void __launch_bounds__(32 * FW) conv_fwd_kernel(ConvParams p, int run, int64_t token_blocks) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int ch = blockIdx.y * (32 * V) + lane * V;
+    const int ch = blockIdx.y * (32 * FV) + lane * FV;
     if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seqs, &g_conv_error);
     if (blockIdx.x >= token_blocks) {
         const int64_t i64 = (static_cast<int64_t>(blockIdx.x) - token_blocks) * FW + warp;
@@ -75,9 +123,9 @@ __global__ void __launch_bounds__(32 * FW) conv_fwd_kernel(ConvParams p, int run
         const int64_t b = p.seqs.begin(i), e = p.seqs.end(i);
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
-            float f[V];
-            load_before<T, W, V>(p, i, b, e, W - 1 - k, ch, f);
-            Vec<T, V>::store(p.final_state, (i64 * (W - 1) + k) * p.C + ch, f);
+            float f[FV];
+            load_before<T, W, FV>(p, i, b, e, W - 1 - k, ch, f);
+            Vec<T, FV>::store(p.final_state, (i64 * (W - 1) + k) * p.C + ch, f);
         }
         return;
     }
@@ -87,43 +135,66 @@ __global__ void __launch_bounds__(32 * FW) conv_fwd_kernel(ConvParams p, int run
     int32_t i = warp_upper(p.seqs.n, t, [&](int32_t j) { return p.seqs.begin(j); });
     int64_t b = p.seqs.begin(i), e = p.seqs.end(i);
     if (ch >= p.C) return;
-    float w[W][V], bias[V], win[W - 1][V];
-    load_taps<W, V>(p, ch, w, bias);
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) load_before<T, W, V>(p, i, b, t, W - 1 - k, ch, win[k]);
-    while (t < t1) {
-        Vec<T, V> raw[U];
+    float w[W][FV], bias[FV];
+    load_taps<W, FV>(p, ch, w, bias);
+    __shared__ __align__(16) uint8_t rows_s[FW][kRing * U * 32 * FV * sizeof(T)];
+    const Ring<T, FV, kRing * U> ring = {static_cast<uint32_t>(__cvta_generic_to_shared(rows_s[warp])) +
+                                     static_cast<uint32_t>(lane * FV * sizeof(T))};
+    const int n = static_cast<int>(t1 - t);
+    const int64_t x0 = t * p.x_stride + ch;
+    auto fetch = [&](int j) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (t + u < t1) raw[u].load(p.x, (t + u) * p.x_stride + ch);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t + u >= t1) break;
-            if (t + u >= e) {
-                // the next sequence with tokens; behind the last one nothing is written
-                do {
-                    if (++i >= p.seqs.n) return;
-                    b = p.seqs.begin(i);
-                    e = p.seqs.end(i);
-                } while (t + u >= e);
-#pragma unroll
-                for (int k = 0; k < W - 1; ++k) load_before<T, W, V>(p, i, b, t + u, W - 1 - k, ch, win[k]);
-            }
-            float x[V], y[V];
-            raw[u].get(x);
-#pragma unroll
-            for (int c = 0; c < V; ++c) {
-                float a = fmaf(w[W - 1][c], x[c], bias[c]);
-#pragma unroll
-                for (int k = 0; k < W - 1; ++k) a = fmaf(w[k][c], win[k][c], a);
-                y[c] = kSilu ? a * sigmoidf(a) : a;
-#pragma unroll
-                for (int k = 0; k < W - 2; ++k) win[k][c] = win[k + 1][c];
-                win[W - 2][c] = x[c];
-            }
-            Vec<T, V>::store(p.out, (t + u) * p.out_stride + ch, y);
+            if (j + u < n) ring.copy(j + u, p.x, x0 + (j + u) * p.x_stride);
+        ring_commit();
+    };
+    for (int k = 0; k < kRing - 1; ++k) fetch(k * U);
+    float win[W - 1][FV];
+    int64_t yi = t * p.out_stride + ch;
+    // tokens of sequence i from the run's start; the next sequence with tokens
+    int left = 0;
+    auto enter = [&](int j) {
+        while (t + j >= e) {
+            if (++i >= p.seqs.n) return false;   // behind the last sequence nothing is written
+            b = p.seqs.begin(i);
+            e = p.seqs.end(i);
         }
-        t += U;
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) load_before<T, W, FV>(p, i, b, t + j, W - 1 - k, ch, win[k]);
+        left = static_cast<int>(e - t < n ? e - t : n);
+        return true;
+    };
+    if (!enter(0)) return;
+    auto step = [&](int j) {
+        float x[FV], y[FV];
+        ring.get(j, x);
+#pragma unroll
+        for (int c = 0; c < FV; ++c) {
+            float a = fmaf(w[W - 1][c], x[c], bias[c]);
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) a = fmaf(w[k][c], win[k][c], a);
+            y[c] = kSilu ? a * sigmoidf(a) : a;
+#pragma unroll
+            for (int k = 0; k < W - 2; ++k) win[k][c] = win[k + 1][c];
+            win[W - 2][c] = x[c];
+        }
+        Vec<T, FV>::store(p.out, yi, y);
+        yi += p.out_stride;
+    };
+    for (int j = 0; j < n; j += U) {
+        fetch(j + (kRing - 1) * U);
+        ring_wait<kRing - 1>();
+        if (j + U <= left) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) step(j + u);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (j + u >= n) break;
+                if (j + u >= left && !enter(j + u)) return;
+                step(j + u);
+            }
+        }
     }
 }
 
@@ -174,51 +245,15 @@ __global__ void __launch_bounds__(128) conv_decode_kernel(ConvDecodeParams p) {
 //   de_j = sum_k w_k dpre_{j+W-1-k} (outputs of the same sequence) + dfinal_state,
 //   dw_k = sum_t dpre_t e_{t-W+1+k},  dbias = sum_t dpre_t.
 //
-// A warp walks `kRun` tokens and the W - 1 behind them (whose dpre it needs for its last dx). 4 channels
+// A warp walks one run of tokens and the W - 1 behind them (whose dpre it needs for its last dx). 4 channels
 // per thread keep the taps, their gradients and both windows within 128 registers. Each CTA adds its
 // warps' tap gradients in shared memory and writes one partial row; conv_reduce_kernel adds the rows
 // in a fixed order, so a run repeats bit for bit.
 
 constexpr int BV = 4;             // channels per thread
+constexpr int kBwdRing = 2;       // batches in flight, of four tokens (fp32: two)
 constexpr int BW = 8;             // warps per CTA
-constexpr int kRun = 32;          // tokens per warp and step
-
-template <class T>
-struct Vec4;
-template <>
-struct Vec4<float> : Vec<float, 4> {};
-template <>
-struct Vec4<__nv_bfloat16> {
-    uint2 raw;
-    __device__ __forceinline__ void load(const void *p, int64_t at) {
-        raw = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + at);
-    }
-    __device__ __forceinline__ void zero() { raw = make_uint2(0u, 0u); }
-    __device__ __forceinline__ void get(float (&x)[4]) const {
-        x[0] = bf_low(raw.x);
-        x[1] = bf_high(raw.x);
-        x[2] = bf_low(raw.y);
-        x[3] = bf_high(raw.y);
-    }
-    static __device__ __forceinline__ void store(void *p, int64_t at, const float (&x)[4]) {
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p) + at) =
-            make_uint2(bf_pair(x[0], x[1]), bf_pair(x[2], x[3]));
-    }
-};
-
-template <class T, int W>
-__device__ __forceinline__ void load_before4(const ConvParams &p, int32_t i, int64_t b, int64_t t, int back, int ch,
-                                             float (&e)[BV]) {
-    Vec4<T> raw;
-    const int64_t pos = t - back - b;
-    if (pos >= 0)
-        raw.load(p.x, (t - back) * p.x_stride + ch);
-    else if (p.init)
-        raw.load(p.init, (static_cast<int64_t>(i) * (W - 1) + (W - 1) + pos) * p.C + ch);
-    else
-        raw.zero();
-    raw.get(e);
-}
+constexpr int kMinRun = 32;       // tokens per warp, at least
 
 template <int W, bool kSilu>
 __device__ __forceinline__ void dpre_of(const float (&w)[W][BV], const float (&bias)[BV], const float (&win)[W - 1][BV],
@@ -239,8 +274,13 @@ __device__ __forceinline__ void dpre_of(const float (&w)[W][BV], const float (&b
 // grid (token blocks + sequence blocks, channel blocks of 128). Sequence blocks write dinit: warp w one
 // sequence.
 template <class T, class TD, int W, bool kSilu>
-__global__ void __launch_bounds__(32 * BW, 2) conv_bwd_kernel(ConvParams p, int token_blocks) {
-    __shared__ float part[BW][W + 1][32 * BV];
+__global__ void __launch_bounds__(32 * BW, 2) conv_bwd_kernel(ConvParams p, int token_blocks, int64_t run) {
+    // the rings, and when they are done with, the warps' sums
+    constexpr int BU = sizeof(T) == 4 ? 2 : 4;
+    constexpr int kX = kBwdRing * BU * 32 * BV * sizeof(T), kD = kBwdRing * BU * 32 * BV * sizeof(TD);
+    constexpr int kPart = (W + 1) * 32 * BV * sizeof(float), kWarp = kX + kD > kPart ? kX + kD : kPart;
+    __shared__ __align__(16) uint8_t shared[BW * kWarp];
+    float(*part)[W + 1][32 * BV] = reinterpret_cast<float(*)[W + 1][32 * BV]>(shared);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ch = blockIdx.y * (32 * BV) + lane * BV;
     if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seqs, &g_conv_error);
@@ -256,10 +296,10 @@ __global__ void __launch_bounds__(32 * BW, 2) conv_bwd_kernel(ConvParams p, int 
         float de[W - 1][BV], win[W - 1][BV];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
-            load_before4<T, W>(p, i, b, b, W - 1 - j, ch, win[j]);
+            load_before<T, W, BV>(p, i, b, b, W - 1 - j, ch, win[j]);
             const int64_t slot = j - (e - b);
             if (p.dfinal && slot >= 0) {
-                Vec4<T> r;
+                Vec<T, BV> r;
                 r.load(p.dfinal, (i64 * (W - 1) + slot) * p.C + ch);
                 r.get(de[j]);
             } else {
@@ -270,8 +310,8 @@ __global__ void __launch_bounds__(32 * BW, 2) conv_bwd_kernel(ConvParams p, int 
 #pragma unroll
         for (int u = 0; u < W - 1; ++u) {
             if (b + u < e) {
-                Vec4<T> rx;
-                Vec4<TD> rd;
+                Vec<T, BV> rx;
+                Vec<TD, BV> rd;
                 float x[BV], dy[BV], d[BV];
                 rx.load(p.x, (b + u) * p.x_stride + ch);
                 rd.load(p.dout, (b + u) * p.dout_stride + ch);
@@ -292,7 +332,7 @@ __global__ void __launch_bounds__(32 * BW, 2) conv_bwd_kernel(ConvParams p, int 
             }
         }
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) Vec4<T>::store(p.dinit, (i64 * (W - 1) + j) * p.C + ch, de[j]);
+        for (int j = 0; j < W - 1; ++j) Vec<T, BV>::store(p.dinit, (i64 * (W - 1) + j) * p.C + ch, de[j]);
         return;
     }
     float dw[W + 1][BV];
@@ -300,12 +340,14 @@ __global__ void __launch_bounds__(32 * BW, 2) conv_bwd_kernel(ConvParams p, int 
     for (int k = 0; k <= W; ++k)
 #pragma unroll
         for (int c = 0; c < BV; ++c) dw[k][c] = 0.f;
-    const int64_t step = static_cast<int64_t>(token_blocks) * BW * kRun;
-    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * BW + warp) * kRun; t0 < p.rows; t0 += step) {
-        const int64_t t1 = t0 + kRun < p.rows ? t0 + kRun : p.rows;
+    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(shared)) + warp * kWarp;
+    const Ring<T, BV, kBwdRing * BU> x_ring = {mine + static_cast<uint32_t>(lane * BV * sizeof(T))};
+    const Ring<TD, BV, kBwdRing * BU> d_ring = {mine + kX + static_cast<uint32_t>(lane * BV * sizeof(TD))};
+    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * BW + warp) * run;
+    if (t0 < p.rows) {
+        const int64_t t1 = t0 + run < p.rows ? t0 + run : p.rows;
         int32_t i = warp_upper(p.seqs.n, t0, [&](int32_t j) { return p.seqs.begin(j); });
-        if (ch >= p.C) continue;
-        int64_t a = t0;
+        int64_t a = ch < p.C ? t0 : t1;
         while (a < t1) {
             // the part [a, z) of the run that belongs to sequence i = [b, e)
             int64_t b = p.seqs.begin(i), e = p.seqs.end(i);
@@ -319,80 +361,96 @@ __global__ void __launch_bounds__(32 * BW, 2) conv_bwd_kernel(ConvParams p, int 
             float win[W - 1][BV], dp[W - 1][BV];
 #pragma unroll
             for (int k = 0; k < W - 1; ++k) {
-                load_before4<T, W>(p, i, b, a, W - 1 - k, ch, win[k]);
+                load_before<T, W, BV>(p, i, b, a, W - 1 - k, ch, win[k]);
 #pragma unroll
                 for (int c = 0; c < BV; ++c) dp[k][c] = 0.f;
             }
-            const int64_t last = z + W - 1;
-            for (int64_t t = a; t < last; t += U) {
-                Vec4<T> rx[U];
-                Vec4<TD> rd[U];
+            // counted from a: outputs n (own), tokens of the sequence left (up to the W - 1 behind the run), steps,
+            // and the first token whose place the final state holds
+            const int n = static_cast<int>(z - a), left = static_cast<int>(e - a < n + W - 1 ? e - a : n + W - 1);
+            const int steps = n + W - 1, kept = p.dfinal && e - a <= n + W - 1 ? static_cast<int>(e - a) - (W - 1) : n;
+            int64_t xi = a * p.x_stride + ch, di = a * p.dout_stride + ch;
+            int64_t oi = (a - (W - 1)) * p.dx_stride + ch;
+            auto fetch = [&](int j) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (t + u < last && t + u < e) {
-                        rx[u].load(p.x, (t + u) * p.x_stride + ch);
-                        rd[u].load(p.dout, (t + u) * p.dout_stride + ch);
-                    } else {
-                        rx[u].zero();
-                        rd[u].zero();
+                for (int u = 0; u < BU; ++u) {
+                    if (j + u < left) {
+                        x_ring.copy(j + u, p.x, xi + (j + u) * p.x_stride);
+                        d_ring.copy(j + u, p.dout, di + (j + u) * p.dout_stride);
                     }
                 }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int64_t tt = t + u;
-                    if (tt >= last) break;
-                    float x[BV], dy[BV], d[BV];
-                    rx[u].get(x);
-                    rd[u].get(dy);
-                    // behind the sequence's end dy is zero, and with it d
+                ring_commit();
+            };
+            // step j: dpre of token a + j, and with it dx of token a + j - (W - 1). kInner: all of that is there
+            auto step = [&](auto inner, int j) {
+                constexpr bool kInner = decltype(inner)::value;
+                float x[BV], dy[BV], d[BV];
+                if (kInner || j < left) {
+                    x_ring.get(j, x);
+                    d_ring.get(j, dy);
                     dpre_of<W, kSilu>(w, bias, win, x, dy, d);
-                    if (tt >= e)
+                } else {
 #pragma unroll
-                        for (int c = 0; c < BV; ++c) d[c] = 0.f;   // also where pre is not finite
-                    const int64_t o = tt - (W - 1);
-                    if (o >= a) {
-                        float g[BV];
+                    for (int c = 0; c < BV; ++c) x[c] = d[c] = 0.f;   // behind the sequence
+                }
+                if (kInner || j >= W - 1) {
+                    float g[BV];
 #pragma unroll
-                        for (int c = 0; c < BV; ++c) {
-                            g[c] = w[0][c] * d[c];
+                    for (int c = 0; c < BV; ++c) {
+                        g[c] = w[0][c] * d[c];
 #pragma unroll
-                            for (int k = 1; k < W; ++k) g[c] = fmaf(w[k][c], dp[W - 1 - k][c], g[c]);
-                        }
-                        const int64_t slot = o - (e - (W - 1));
-                        if (p.dfinal && slot >= 0) {
-                            Vec4<T> r;
-                            float f[BV];
-                            r.load(p.dfinal, (static_cast<int64_t>(i) * (W - 1) + slot) * p.C + ch);
-                            r.get(f);
-#pragma unroll
-                            for (int c = 0; c < BV; ++c) g[c] += f[c];
-                        }
-                        Vec4<T>::store(p.dx, o * p.dx_stride + ch, g);
+                        for (int k = 1; k < W; ++k) g[c] = fmaf(w[k][c], dp[W - 1 - k][c], g[c]);
                     }
-                    if (tt < z) {
+                    const int o = j - (W - 1);
+                    if (!kInner && o >= kept) {
+                        Vec<T, BV> r;
+                        float f[BV];
+                        r.load(p.dfinal, (static_cast<int64_t>(i) * (W - 1) + o + (W - 1) - (e - a)) * p.C + ch);
+                        r.get(f);
 #pragma unroll
-                        for (int c = 0; c < BV; ++c) {
-#pragma unroll
-                            for (int k = 0; k < W - 1; ++k) dw[k][c] = fmaf(d[c], win[k][c], dw[k][c]);
-                            dw[W - 1][c] = fmaf(d[c], x[c], dw[W - 1][c]);
-                            dw[W][c] += d[c];
-                        }
+                        for (int c = 0; c < BV; ++c) g[c] += f[c];
                     }
+                    Vec<T, BV>::store(p.dx, oi, g);
+                }
+                oi += p.dx_stride;
+                if (kInner || j < n) {
 #pragma unroll
                     for (int c = 0; c < BV; ++c) {
 #pragma unroll
-                        for (int k = 0; k < W - 2; ++k) {
-                            win[k][c] = win[k + 1][c];
-                            dp[k][c] = dp[k + 1][c];
-                        }
-                        win[W - 2][c] = x[c];
-                        dp[W - 2][c] = d[c];
+                        for (int k = 0; k < W - 1; ++k) dw[k][c] = fmaf(d[c], win[k][c], dw[k][c]);
+                        dw[W - 1][c] = fmaf(d[c], x[c], dw[W - 1][c]);
+                        dw[W][c] += d[c];
                     }
                 }
+#pragma unroll
+                for (int c = 0; c < BV; ++c) {
+#pragma unroll
+                    for (int k = 0; k < W - 2; ++k) {
+                        win[k][c] = win[k + 1][c];
+                        dp[k][c] = dp[k + 1][c];
+                    }
+                    win[W - 2][c] = x[c];
+                    dp[W - 2][c] = d[c];
+                }
+            };
+            for (int k = 0; k < kBwdRing - 1; ++k) fetch(k * BU);
+            for (int j = 0; j < steps; j += BU) {
+                fetch(j + (kBwdRing - 1) * BU);
+                ring_wait<kBwdRing - 1>();
+                if (j >= W - 1 && j + BU <= n && j + BU - (W - 1) <= kept) {
+#pragma unroll
+                    for (int u = 0; u < BU; ++u) step(std::true_type(), j + u);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < BU; ++u)
+                        if (j + u < steps) step(std::false_type(), j + u);
+                }
             }
+            ring_wait<0>();
             a = z;
         }
     }
+    __syncthreads();   // every warp is done with its rings
 #pragma unroll
     for (int k = 0; k <= W; ++k)
 #pragma unroll
@@ -434,9 +492,9 @@ cudaError_t by_taps(int W, F f) {
 template <class T, int W>
 cudaError_t fwd(const ConvParams &p, cudaStream_t s) {
     // Long runs re-read fewer rows (W - 1 of every `run`); short ones make enough warps of few tokens.
-    const int64_t cblocks = (p.C + 32 * V - 1) / (32 * V);
-    int run = 16;
-    while (run > U && (p.rows + run - 1) / run * cblocks < 148 * 16) run /= 2;
+    const int64_t cblocks = (p.C + 32 * FV - 1) / (32 * FV);
+    int run = 64;
+    while (run > U && (p.rows + run - 1) / run * cblocks < 148 * 32) run /= 2;
     const int64_t tb = (p.rows + FW * run - 1) / (FW * run);
     const int64_t sb = p.final_state ? (p.seqs.n + FW - 1) / FW : 0;
     if (tb + sb == 0) return cudaSuccess;
@@ -453,13 +511,13 @@ template <class T, class TD, int W>
 cudaError_t bwd(const ConvParams &p, cudaStream_t s) {
     const int32_t tb = conv_bwd_blocks(p.rows, p.C);
     const int64_t cblocks = (p.C + 32 * BV - 1) / (32 * BV);
-    const int64_t sb = p.dinit ? (p.seqs.n + BW - 1) / BW : 0;
+    const int64_t sb = p.dinit ? (p.seqs.n + BW - 1) / BW : 0, run = (p.rows + tb * BW - 1) / (tb * BW);
     if (tb + sb > 0x7fffffffLL || cblocks > 65535) return cudaErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>(tb + sb), static_cast<unsigned>(cblocks));
     if (p.silu)
-        conv_bwd_kernel<T, TD, W, true><<<grid, 32 * BW, 0, s>>>(p, tb);
+        conv_bwd_kernel<T, TD, W, true><<<grid, 32 * BW, 0, s>>>(p, tb, run);
     else
-        conv_bwd_kernel<T, TD, W, false><<<grid, 32 * BW, 0, s>>>(p, tb);
+        conv_bwd_kernel<T, TD, W, false><<<grid, 32 * BW, 0, s>>>(p, tb, run);
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess || (!p.dweight && !p.dbias)) return err;
     conv_reduce_kernel<W><<<dim3((p.C + 127) / 128, W + 1), 128, 0, s>>>(p, tb);
@@ -480,10 +538,10 @@ cudaError_t decode(const ConvDecodeParams &p, cudaStream_t s) {
 }  // namespace conv
 
 int32_t conv_bwd_blocks(int64_t rows, int32_t C) {
-    // about four CTAs for each SM over all channel blocks: each writes one row of partial sums
+    // one round of two CTAs per SM over all channel blocks: each writes one row of partial sums
     const int64_t cblocks = (static_cast<int64_t>(C) + 32 * conv::BV - 1) / (32 * conv::BV);
-    const int64_t most = (rows + conv::BW * conv::kRun - 1) / (conv::BW * conv::kRun);
-    const int64_t want = (4 * 148 + cblocks - 1) / cblocks;
+    const int64_t most = (rows + conv::BW * conv::kMinRun - 1) / (conv::BW * conv::kMinRun);
+    const int64_t want = 2 * 148 / cblocks;
     const int64_t n = most < want ? most : want;
     return static_cast<int32_t>(n < 1 ? 1 : n);
 }

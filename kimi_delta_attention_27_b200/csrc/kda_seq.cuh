@@ -70,8 +70,7 @@ __device__ __forceinline__ uint32_t bf_pair(float a, float b) {
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
-// V consecutive elements as floats; T is float or __nv_bfloat16, and p is V * sizeof(T) aligned
-// (16 bytes at a time at most).
+// V consecutive elements as floats; T is float or __nv_bfloat16; loads and stores of 16 bytes (8 for four bf16).
 template <class T, int V>
 struct Vec;
 template <int V>
@@ -103,6 +102,24 @@ struct Vec<__nv_bfloat16, V> {
         for (int i = 0; i < V / 8; ++i)
             d[i] = make_uint4(bf_pair(x[8 * i], x[8 * i + 1]), bf_pair(x[8 * i + 2], x[8 * i + 3]),
                               bf_pair(x[8 * i + 4], x[8 * i + 5]), bf_pair(x[8 * i + 6], x[8 * i + 7]));
+    }
+};
+template <>
+struct Vec<__nv_bfloat16, 4> {
+    uint2 raw;
+    __device__ __forceinline__ void load(const void *p, int64_t at) {
+        raw = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + at);
+    }
+    __device__ __forceinline__ void zero() { raw = make_uint2(0u, 0u); }
+    __device__ __forceinline__ void get(float (&x)[4]) const {
+        x[0] = bf_low(raw.x);
+        x[1] = bf_high(raw.x);
+        x[2] = bf_low(raw.y);
+        x[3] = bf_high(raw.y);
+    }
+    static __device__ __forceinline__ void store(void *p, int64_t at, const float (&x)[4]) {
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p) + at) =
+            make_uint2(bf_pair(x[0], x[1]), bf_pair(x[2], x[3]));
     }
 };
 template <int V>
