@@ -22,14 +22,15 @@ namespace conv {
 __device__ unsigned int g_conv_error = 0;
 
 constexpr int V = 8;              // channels per thread, single tokens
-constexpr int FV = 4;             // and forward: with 8 the taps and windows take twice the registers (279 us at 71,000 x 4096)
+constexpr int FV = 4;             // and forward: with 8 the taps and windows take twice the registers
 constexpr int FW = 4;             // warps per CTA, forward
 constexpr int U = 4;              // tokens of a batch
 constexpr int kRing = 4;          // batches of loads in flight
 
 // A thread's own window into shared memory for the rows it will need: asynchronous copies keep kRing batches of
 // rows in flight without a register for any of them. Every thread reads back what it copied itself, so no
-// barrier is needed. (With the same rows in registers, 8 tokens ahead: 275 us instead of the figure above.)
+// barrier is needed. (71,000 tokens x 4096 bf16 channels: 200 us, 5.9 TB/s; with the rows 8 tokens ahead in
+// registers 275 us.)
 template <class T, int N, int kRows>
 struct Ring {
     static constexpr int kBytes = N * sizeof(T);
