@@ -514,7 +514,9 @@ kda_status kda_scan_bwd(const void *x, int64_t x_stride, const float *dt, const 
     KDA_TRY(check_stride(rows, dx_stride, hp, 2));
     KDA_TRY(check_stride(rows, db_stride, gn, 2));
     KDA_TRY(check_stride(rows, dc_stride, gn, 2));
-    if (scan_too_large(rows, s.n, num_heads, head_dim)) return KDA_ERR_TOO_LARGE;
+    if (scan_too_large(rows, s.n, num_heads, head_dim) ||
+        kda::scan_cells(rows, s.n) > 0x7fffffffLL / (static_cast<int64_t>(num_heads) * state_dim))
+        return KDA_ERR_TOO_LARGE;   // the states' rows, too, are 32-bit coordinates
     const size_t need = kda::scan_bwd_workspace_bytes(rows, s.n, num_heads, num_groups, head_dim, state_dim);
     KDA_TRY(check_workspace(workspace, workspace_bytes, need));
     const int64_t st = static_cast<int64_t>(s.n) * num_heads * state_dim * head_dim;

@@ -170,18 +170,8 @@ __device__ __forceinline__ void frag_bt(uint32_t tile, int r0, int c0, uint32_t 
     ldsm4t(tile + at<ROWB>(r0 + (l & 15), c0 + (l >> 4)), f);
 }
 
-// the first n-tile of frag_bt alone
-template <int ROWB>
-__device__ __forceinline__ void frag_bt8(uint32_t tile, int r0, int c0, uint32_t (&f)[2]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
-                 : "=r"(f[0]), "=r"(f[1])
-                 : "r"(tile + at<ROWB>(r0 + static_cast<int>(threadIdx.x & 15), c0))
-                 : "memory");
-}
-
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));

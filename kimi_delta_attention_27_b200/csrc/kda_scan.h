@@ -80,6 +80,7 @@ cudaError_t launch_scan_tc_state(const ScanParams &p, int parts, int directions,
                                  const ScanStateRun &fwd, const ScanStateRun &rev, cudaStream_t stream);
 cudaError_t read_and_clear_scan_tc_error(unsigned int *value);
 cudaError_t read_and_clear_scan_state_error(unsigned int *value);
+cudaError_t read_and_clear_scan_bwd_error(unsigned int *value);
 
 constexpr int kScanTile = 64;     // tokens per tile
 constexpr int kScanTcTile = 128;  // and of launch_scan_tc

@@ -97,16 +97,20 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-// rows of `cols` bf16 elements, `stride` apart, in boxes of box_rows x 64 columns (128 bytes, swizzled)
-inline bool encode(CUtensorMap *map, const void *at, int64_t cols, int64_t rows, int64_t stride, int box_rows) {
+// rows of `cols` elements, `stride` apart, in boxes of box_rows x 128 bytes, swizzled
+inline bool encode(CUtensorMap *map, CUtensorMapDataType type, int bytes, const void *at, int64_t cols, int64_t rows,
+                   int64_t stride, int box_rows) {
     auto enc = encoder();
     if (!enc) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows > 1 ? stride : cols) * 2};
-    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(at), dims, strides, box, step,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows > 1 ? stride : cols) * bytes};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / bytes), static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
+    return enc(map, type, 2, const_cast<void *>(at), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+inline bool encode(CUtensorMap *map, const void *at, int64_t cols, int64_t rows, int64_t stride, int box_rows) {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, at, cols, rows, stride, box_rows);
 }
 
 }  // namespace tc
