@@ -41,8 +41,7 @@ struct StateSmem {
     static constexpr uint32_t kRows = 0;                                   // [stage] 64 x 128: two blocks of columns
     static constexpr uint32_t kCols = kRows + kRowStages * 2 * kTile;      // [head][stage]
     static constexpr uint32_t kParts = kCols + 4 * kTile;                  // [stage][S][head]
-    static constexpr uint32_t kOut = kParts + 2 * S * 2 * kTile;           // [warp] 32 rows x 64 bytes of the state
-    static constexpr uint32_t kGates = kOut + 16 * 2048;                   // [head][4]
+    static constexpr uint32_t kGates = kParts + 2 * S * 2 * kTile;         // [head][4]
     static constexpr uint32_t kBars = kGates + 8 * sizeof(StateGates);
     static constexpr uint32_t kBytes = kBars + 256;
     static_assert(kBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
@@ -109,31 +108,35 @@ __global__ void __launch_bounds__(NT, 1)
 
     if (warp < kIssuer) {
         // ---------------------------------------------------------------- a head's elements
-        // thread: row r of the state, columns 32 hf .. + 32
-        const int hd = warp >> 3, hf = (warp >> 2) & 1, wq = warp & 3, r = wq * 32 + lane, t256 = tid & 255;
+        // warp: rows 32 wq .. + 32 of the state, columns 32 hf .. + 32, in the layout of tmem_ld_frag: a quad of threads
+        // then has 32 bytes of a row, and the state goes to memory as it is
+        const int hd = warp >> 3, hf = (warp >> 2) & 1, wq = warp & 3, t256 = tid & 255;
         if (hd < heads) {
             const int v = v0 + hd, h = v / slices, col = v % slices * PC + 32 * hf;
             const uint32_t tU = tmem + hd * 64 + 32 * hf + (static_cast<uint32_t>(wq * 32) << 16);
-            const int64_t sn = static_cast<int64_t>(N) * p.P, at_r = static_cast<int64_t>(r) * p.P + col;
-            float2 s[16];
+            const int64_t sn = static_cast<int64_t>(N) * p.P, at_r = static_cast<int64_t>(wq * 32 + (lane >> 2)) * p.P + col + (lane & 3) * 2;
+            float2 s[16];   // [8 i + 2 j + k]: row 16 i + 8 k + lane / 4, columns 8 j + 2 (lane % 4) and the next
+            auto place = [&](int m) { return static_cast<int64_t>((m >> 3) * 16 + (m & 1) * 8) * p.P + ((m >> 1) & 3) * 8; };
             {
                 const void *init = rev ? static_cast<const void *>(p.dhT) : p.h0;
                 const void *src = run.entering ? run.entering : head && !run.leave ? init : nullptr;
                 const bool fp32 = run.entering || rev || p.h0_fp32;
                 const int64_t e = ((run.entering ? unit : static_cast<int64_t>(u.i)) * p.H + h) * sn + at_r;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int m = 0; m < 16; ++m) {
+                    s[m] = make_float2(0.f, 0.f);
                     if (src && fp32) {
-                        f = reinterpret_cast<const float4 *>(static_cast<const float *>(src) + e)[j];
+                        s[m] = *reinterpret_cast<const float2 *>(static_cast<const float *>(src) + e + place(m));
                     } else if (src) {
-                        const uint2 w = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(src) + e)[j];
-                        f = make_float4(bf_low(w.x), bf_high(w.x), bf_low(w.y), bf_high(w.y));
+                        const uint32_t w = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(src) + e + place(m));
+                        s[m] = make_float2(bf_low(w), bf_high(w));
                     }
-                    s[2 * j] = make_float2(f.x, f.y);
-                    s[2 * j + 1] = make_float2(f.z, f.w);
                 }
             }
+            auto store = [&](float *dst) {
+#pragma unroll
+                for (int m = 0; m < 16; ++m) *reinterpret_cast<float2 *>(dst + place(m)) = s[m];
+            };
             float total = 0.f, next_total = 0.f;
             // the weighted columns of tile i in parts; four threads per token
             auto write_parts = [&](int i) {
@@ -190,43 +193,21 @@ __global__ void __launch_bounds__(NT, 1)
                 total = next_total;
                 if (i + 1 < tiles) ok = write_parts(i + 1);
                 if (!ok) break;
-                if (run.states) {
-                    // 32 rows x 16 columns at a time by way of shared memory, for runs of 64 bytes
-                    uint8_t *st = smem + L::kOut + warp * 2048;
-                    float *dst = run.states + ((u.i + cell(i)) * p.H + h) * sn + static_cast<int64_t>(wq * 32) * p.P + col;
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<float4 *>(st + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-                                make_float4(s[8 * q + 2 * j].x, s[8 * q + 2 * j].y, s[8 * q + 2 * j + 1].x, s[8 * q + 2 * j + 1].y);
-                        __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int row = j * 8 + (lane >> 2);
-                            *reinterpret_cast<float4 *>(dst + static_cast<int64_t>(row) * p.P + 16 * q + (lane & 3) * 4) =
-                                *reinterpret_cast<const float4 *>(st + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
-                        }
-                    }
-                }
+                if (run.states) store(run.states + ((u.i + cell(i)) * p.H + h) * sn + at_r);
                 ok = x.wait(kU + (i & 1), (i >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t a[32];
-                tmem_ld32(tU + (i & 1) * 128, a);
+                uint32_t a[2][16];
+                tmem_ld_frag(tU + (i & 1) * 128, a[0]);
+                tmem_ld_frag(tU + (i & 1) * 128 + (16u << 16), a[1]);
                 const float2 tot = make_float2(total, total);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) s[j] = fma2(s[j], tot, make_float2(f32(a[2 * j]), f32(a[2 * j + 1])));
+                for (int m = 0; m < 16; ++m)
+                    s[m] = fma2(s[m], tot, make_float2(f32(a[m >> 3][2 * (m & 7)]), f32(a[m >> 3][2 * (m & 7) + 1])));
             }
             float *dst = run.leave ? run.leave : rev && tail ? p.dh0 : nullptr;
-            if (ok && dst) {
-                const int64_t e = ((run.leave ? unit : static_cast<int64_t>(u.i)) * p.H + h) * sn + at_r;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    reinterpret_cast<float4 *>(dst + e)[j] = make_float4(s[2 * j].x, s[2 * j].y, s[2 * j + 1].x, s[2 * j + 1].y);
-            }
+            if (ok && dst) store(dst + ((run.leave ? unit : static_cast<int64_t>(u.i)) * p.H + h) * sn + at_r);
         }
     } else if (warp == kIssuer) {
         // ---------------------------------------------------------------- loads of the rows, and the products
