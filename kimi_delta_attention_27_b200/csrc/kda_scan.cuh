@@ -188,20 +188,53 @@ __device__ __forceinline__ void split(float v0, float v1, uint32_t (&part)[S]) {
     }
 }
 
+constexpr int64_t kWhole = 0xffffffffLL;   // one cell: pieces are whole sequences
+
 struct Piece {
     int32_t i;            // sequence
     int64_t a, b;         // its tokens [a, b)
     bool first, last, none;
 };
 
+// the cell of `seg` tokens that token x lies in; both below 2^32, where a division is a third as long
+__device__ __forceinline__ int64_t cell_of(int64_t x, int64_t seg) {
+    return static_cast<uint32_t>(x) / static_cast<uint32_t>(seg);
+}
+
+// The sequence with `rank` longer ones before it (of n <= 64; equal lengths in order), by a converged warp: whole
+// sequences are worked on longest first.
+__device__ __forceinline__ int32_t by_length(const Seqs &s, int32_t rank) {
+    const int lane = threadIdx.x & 31;
+    int64_t mine[2];
+    int before[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) mine[k] = lane + 32 * k < s.n ? s.end(lane + 32 * k) - s.begin(lane + 32 * k) : -1;
+    for (int j = 0; j < s.n; ++j) {
+        const int64_t other = __shfl_sync(0xffffffffu, j < 32 ? mine[0] : mine[1], j & 31);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) before[k] += other > mine[k] || (other == mine[k] && j < lane + 32 * k);
+    }
+    const unsigned lo = __ballot_sync(0xffffffffu, before[0] == rank && lane < s.n);
+    const unsigned hi = __ballot_sync(0xffffffffu, before[1] == rank && lane + 32 < s.n);
+    return lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
+}
+
 // piece `u` on the grid of `seg` tokens; a sequence's first and last pieces may be empty
 __device__ __forceinline__ Piece find_piece(const Seqs &s, int64_t u, int64_t seg) {
     Piece p;
-    p.i = warp_upper(s.n, u, [&](int32_t j) { return j + s.begin(j) / seg; });
-    const int64_t c = u - p.i, sb = s.begin(p.i), se = s.end(p.i);
-    p.none = c < sb / seg || c > se / seg;
-    p.first = c == sb / seg;
-    p.last = c == se / seg;
+    if (seg == kWhole && s.cu && s.n <= 64) {
+        p.i = by_length(s, static_cast<int32_t>(u));
+        p.first = p.last = true;
+        p.none = false;
+        p.a = s.begin(p.i);
+        p.b = s.end(p.i);
+        return p;
+    }
+    p.i = warp_upper(s.n, u, [&](int32_t j) { return j + cell_of(s.begin(j), seg); });
+    const int64_t c = u - p.i, sb = s.begin(p.i), se = s.end(p.i), cb = cell_of(sb, seg), ce = cell_of(se, seg);
+    p.none = c < cb || c > ce;
+    p.first = c == cb;
+    p.last = c == ce;
     p.a = p.first ? sb : c * seg;
     p.b = p.last ? se : (c + 1) * seg;
     return p;

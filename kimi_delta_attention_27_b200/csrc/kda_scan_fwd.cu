@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(256) scan_join_kernel(ScanParams p, int64_t se
     const int32_t i = static_cast<int32_t>(ih / p.H), h = static_cast<int32_t>(ih % p.H);
     const int64_t sn = static_cast<int64_t>(p.N) * p.P, e = (static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x) * 4;
     if (e >= sn) return;
-    const int64_t c0 = p.seqs.begin(i) / seg, c1 = p.seqs.end(i) / seg;
+    const int64_t c0 = cell_of(p.seqs.begin(i), seg), c1 = cell_of(p.seqs.end(i), seg);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     const void *init = kReverse ? static_cast<const void *>(p.dhT) : p.h0;
     if (init) {
@@ -406,9 +406,9 @@ __global__ void __launch_bounds__(256) scan_join_kernel(ScanParams p, int64_t se
         }
     }
     const int64_t count = c1 - c0 + 1;
-    constexpr int U = 8;
+    constexpr int U = 4;
     for (int64_t k0 = 0; k0 < count; k0 += U) {
-        // the contributions do not depend on one another: eight loads at once, then the chain
+        // the contributions do not depend on one another: four loads at once, then the chain
         float4 v[U];
         float f[U];
 #pragma unroll
@@ -433,28 +433,33 @@ __global__ void __launch_bounds__(256) scan_join_kernel(ScanParams p, int64_t se
     }
 }
 
-// Tokens per piece, a multiple of `tile`; 0: whole sequences. `ctas`: CTAs of one piece. A cut costs a second
-// reading of x and B and one state per piece, so it is made only where whole sequences leave SMs without work,
-// and into no more pieces than `want` CTAs need.
-int64_t piece_tokens(int64_t rows, int64_t n, int64_t ctas, int64_t want, int tile) {
-    if (n * ctas >= want || n == 0) return 0;
+// Tokens per piece, a multiple of `tile`; 0: whole sequences. `ctas`: CTAs of one piece, `slots` as many as run at
+// once. A cut costs a second reading of x and B, one state per piece and, in all, about 1.55 times the time; whole
+// sequences take as long as the longest. So they are cut where that is longer: with equal ones where they fill fewer
+// than slots / 1.55, with packed ones, of which the longest is taken to be twice the mean, twice that. (8 packed
+// sequences of 64 heads: whole 0.43 ms, cut 0.82 ms; one of 65536 tokens x 32 heads x 128: cut 0.89 ms, whole 2.7 ms.)
+int64_t piece_tokens(int64_t rows, int64_t n, bool packed, int64_t ctas, int slots, int tile) {
+    if (n == 0 || 2 * n * ctas >= (packed ? 5 : 3) * slots / 2) return 0;
+    const int64_t want = 2 * slots;
     int64_t seg = (rows * ctas + want - 1) / want;
     seg = (seg + tile - 1) / tile * tile;
     if (seg < 256) seg = 256;
     return seg >= rows ? 0 : seg;
 }
-// the tcgen05 kernels: one CTA per SM, each with two runs of 64 columns
-int64_t tc_piece_tokens(int64_t rows, int64_t n, int32_t H, int32_t P) {
-    return piece_tokens(rows, n, (static_cast<int64_t>(H) * (P / PC) + 1) / 2, 2 * 148, kScanTcTile);
+// State size 128: sequences of more than 256 tokens on average take the tcgen05 kernels, one CTA per SM with two runs
+// of 64 columns. Their first tile takes some 18 us, where the warp-level kernel's takes 8 (one sequence of 200 tokens x
+// 32 heads: 24 against 20 us; 16 of 200 x 64: 110 against 105; 16 of 512 x 64: 141 against 192).
+bool takes_tc(int64_t rows, int64_t n, int32_t N) { return N == 128 && rows > 256 * n; }
+int64_t fwd_piece_tokens(int64_t rows, int64_t n, bool packed, int32_t H, int32_t P, int32_t N) {
+    const int64_t columns = static_cast<int64_t>(H) * (P / PC);
+    return takes_tc(rows, n, N) ? piece_tokens(rows, n, packed, (columns + 1) / 2, 148, kScanTcTile)
+                                : piece_tokens(rows, n, packed, columns, 2 * 148, T);
 }
 // the backward's runs of the state, both directions at once
-int64_t state_piece_tokens(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N) {
-    return N == 128 ? piece_tokens(rows, n, H * (P / PC), 96, T)
-                    : piece_tokens(rows, n, static_cast<int64_t>(H) * (P / PC), 4 * 148, T);
-}
-// the warp-level kernels: several CTAs per SM
-int64_t warp_piece_tokens(int64_t rows, int64_t n, int32_t H, int32_t P) {
-    return piece_tokens(rows, n, static_cast<int64_t>(H) * (P / PC), 4 * 148, T);
+int64_t state_piece_tokens(int64_t rows, int64_t n, bool packed, int32_t H, int32_t P, int32_t N) {
+    const int64_t columns = static_cast<int64_t>(H) * (P / PC);
+    return N == 128 ? piece_tokens(rows, n, packed, (columns + 1) / 2 * 2, 148, T)
+                    : piece_tokens(rows, n, packed, columns, 2 * 148, T);
 }
 
 int64_t piece_count(int64_t rows, int64_t n, int64_t seg) { return seg ? rows / seg + n : n; }
@@ -483,50 +488,56 @@ cudaError_t join_launch(const ScanParams &p, int64_t seg, float *ws, const float
     return cudaGetLastError();
 }
 
-constexpr int64_t kWhole = int64_t(1) << 60;   // one cell: pieces are whole sequences
-
 }  // namespace scan
 
+// the larger need, that of packed sequences: where equal ones are cut, those are too
 size_t scan_fwd_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N) {
-    using namespace scan;
-    return piece_bytes(rows, n, N == 128 ? tc_piece_tokens(rows, n, H, P) : warp_piece_tokens(rows, n, H, P), H, P, N);
+    return scan::piece_bytes(rows, n, scan::fwd_piece_tokens(rows, n, true, H, P, N), H, P, N);
 }
 
 size_t scan_states_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N) {
     // both directions' pieces
-    return 2 * scan::piece_bytes(rows, n, scan::state_piece_tokens(rows, n, H, P, N), H, P, N);
+    return 2 * scan::piece_bytes(rows, n, scan::state_piece_tokens(rows, n, true, H, P, N), H, P, N);
+}
+
+// the warp-level kernels, each piece's own contribution and the main run
+template <int N>
+cudaError_t scan_fwd_warps(const ScanParams &p, int64_t seg, int64_t units, float *ws, float *decay, bool local, cudaStream_t s) {
+    using namespace scan;
+    const bool exact = p.hT && p.hT_fp32;
+    if (local)
+        return exact ? state_launch<N, 3, false>(p, seg, units, {nullptr, ws, decay, nullptr}, s)
+                     : state_launch<N, 2, false>(p, seg, units, {nullptr, ws, decay, nullptr}, s);
+    auto *k = exact ? scan_fwd_kernel<N, 3> : scan_fwd_kernel<N, 2>;
+    const cudaError_t err = allow_smem(k, FwdSmem<N>::kBytes);
+    if (err != cudaSuccess) return err;
+    k<<<static_cast<unsigned>(units * p.H * (p.P / PC)), NT, FwdSmem<N>::kBytes, s>>>(p, seg, ws);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_scan_fwd(const ScanParams &p, cudaStream_t s) {
     using namespace scan;
-    const bool tc = p.N == 128;
-    const int64_t cut = tc ? tc_piece_tokens(p.rows, p.seqs.n, p.H, p.P) : warp_piece_tokens(p.rows, p.seqs.n, p.H, p.P);
+    const bool tc = takes_tc(p.rows, p.seqs.n, p.N);
+    const int64_t cut = fwd_piece_tokens(p.rows, p.seqs.n, p.seqs.cu != nullptr, p.H, p.P, p.N);
     const int64_t seg = cut ? cut : kWhole, units = piece_count(p.rows, p.seqs.n, cut);
     if (units * p.H * (p.P / PC) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     float *ws = p.ws, *decay = ws ? ws + units * p.H * p.N * p.P : nullptr;
-    const bool exact = p.hT && p.hT_fp32;
-    cudaError_t err = cudaSuccess;
+    auto warps = [&](bool local, float *states) {
+        return by_state(p.N, [&](auto n) { return scan_fwd_warps<decltype(n)::value>(p, seg, units, states, decay, local, s); });
+    };
     if (cut) {
-        if (tc)
-            err = launch_scan_tc_state(p, exact ? 3 : 2, 1, seg, units, {nullptr, ws, decay, nullptr}, {}, s);
-        else
-            err = exact ? state_launch<64, 3, false>(p, seg, units, {nullptr, ws, decay, nullptr}, s)
-                        : state_launch<64, 2, false>(p, seg, units, {nullptr, ws, decay, nullptr}, s);
+        cudaError_t err = tc ? launch_scan_tc_state(p, p.hT && p.hT_fp32 ? 3 : 2, 1, seg, units, {nullptr, ws, decay, nullptr}, {}, s)
+                             : warps(true, ws);
         if (err == cudaSuccess) err = join_launch<false>(p, seg, ws, decay, s);
+        if (err != cudaSuccess) return err;
     }
-    if (err != cudaSuccess) return err;
-    const float *entering = cut ? ws : nullptr;
-    if (tc) return launch_scan_tc(p, seg, units, entering, s);
-    auto *k = exact ? scan_fwd_kernel<64, 3> : scan_fwd_kernel<64, 2>;
-    err = allow_smem(k, FwdSmem<64>::kBytes);
-    if (err != cudaSuccess) return err;
-    k<<<static_cast<unsigned>(units * p.H * (p.P / PC)), NT, FwdSmem<64>::kBytes, s>>>(p, seg, entering);
-    return cudaGetLastError();
+    float *entering = cut ? ws : nullptr;
+    return tc ? launch_scan_tc(p, seg, units, entering, s) : warps(false, entering);
 }
 
 cudaError_t launch_scan_states(const ScanParams &p, float *states, float *grads, float *ws, cudaStream_t s) {
     using namespace scan;
-    const int64_t cut = state_piece_tokens(p.rows, p.seqs.n, p.H, p.P, p.N), seg = cut ? cut : kWhole;
+    const int64_t cut = state_piece_tokens(p.rows, p.seqs.n, p.seqs.cu != nullptr, p.H, p.P, p.N), seg = cut ? cut : kWhole;
     const int64_t units = piece_count(p.rows, p.seqs.n, cut);
     if (units == 0) return cudaSuccess;
     if (units * p.H * (p.P / PC) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
