@@ -328,3 +328,61 @@ def test_conv_bwd_repeats(lib):
     a, b = (kda.kda_conv_bwd(dev(d["x"])[None], dev(d["w"]), dev(d["dout"])[None], dev(d["b"]), cu_seqlens=cu_of([3000, 1, 2500]))
             for _ in range(2))
     assert all(torch.equal(a[k], b[k]) for k in ("dx", "dweight", "dbias"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("batch,C", [(1, 8), (3, 8), (2, 304128), (1187, 1024), (1186, 1032)])
+def test_conv_decode_batches(lib, batch, C, dtype):
+    """Small batches, and ones large enough for four requests per thread, whole and with a rest; rows of x and out
+    strided."""
+    g = torch.Generator().manual_seed(batch)
+    W = 4
+    x = torch.randn(batch, C + 8, generator=g).to(dtype).cuda()[:, :C]
+    w, b = torch.randn(C, W, generator=g).cuda(), torch.randn(C, generator=g).cuda()
+    state = torch.randn(batch, W - 1, C, generator=g).to(dtype).cuda()
+    out = torch.full((batch + 1, C + 16), 7.0, dtype=dtype, device="cuda")
+    new = torch.empty_like(state)
+    kda.kda_conv_decode(x, w, state, new, bias=b, out=out[:batch, 8:8 + C])
+    e = torch.cat([state, x[:, None]], 1).double()
+    pre = (e * w.t().double()).sum(1) + b.double()
+    mag = (e.abs() * w.t().double().abs()).sum(1) + b.double().abs()
+    r = dict(out=(pre * pre.sigmoid()).cpu(), pre=pre.cpu(), pre_abs=mag.cpu())
+    assert ref.worst(out[:batch, 8:8 + C], r["out"], out_tol(r, dtype, True)) <= 1
+    assert torch.equal(new, e[:, 1:].to(dtype))
+    assert bool((out[batch] == 7).all()) and bool((out[:, :8] == 7).all()) and bool((out[:, 8 + C:] == 7).all())
+    inplace = state.clone()
+    kda.kda_conv_decode(x, w, inplace, inplace, bias=b)
+    assert torch.equal(inplace, new) and kda.device_error() == 0
+
+
+@pytest.mark.gpu
+def test_conv_calls_at_once_and_captured(lib):
+    """Gradients (which need scratch memory) in flight on two streams, and replayed from a graph."""
+    lengths = [900, 3, 410]
+    sets = [{k: dev(v) for k, v in make(lengths, 512, 4, torch.bfloat16, seed=s).items()} for s in (1, 2)]
+    cu = cu_of(lengths)
+
+    def run(d):
+        return kda.kda_conv_bwd(d["x"][None], d["w"], d["dout"][None], d["b"], True, cu, d["init"], d["dfinal"], True)
+
+    want = [run(d) for d in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for d, s in zip(sets, streams):
+            with torch.cuda.stream(s):
+                got.append(run(d))
+        torch.cuda.synchronize()
+        assert all(torch.equal(w[k], g[k]) for w, g in zip(want, got) for k in w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = run(sets[0])
+    for d, w in ((sets[1], want[1]), (sets[1], want[1])):
+        for k in ("x", "w", "b", "init", "dout", "dfinal"):
+            sets[0][k].copy_(d[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(w[k], res[k]) for k in w)
+    assert kda.device_error() == 0

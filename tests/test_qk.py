@@ -232,3 +232,38 @@ def test_qk_bwd_takes_kda_bwds_gradients_and_repeats(lib):
     # out is linear in q, so the difference is exact but for roundings: kda_fwd's operands are bf16 (2^-8 each, of
     # terms that add up to `mag` at most; they average out over more than 10^4 of them)
     assert abs((hi - lo) / 2 - float((a["dq_weight"] * way).sum())) <= 2.0 ** -8 * mag
+
+
+@pytest.mark.gpu
+def test_qk_calls_at_once_and_captured(lib):
+    """Both directions in flight on two streams, and replayed from a graph."""
+    sets = []
+    for s in (1, 2):
+        d = make(400, 6, 2, 128, 64, 5 * s, True, seed=s)
+        g = torch.Generator().manual_seed(s)
+        d.update(dyq=torch.randn(d["q"].shape, generator=g), dyk=torch.randn(d["k"].shape, generator=g))
+        sets.append({k: dev(v) for k, v in d.items()})
+
+    def run(d):
+        opt = ("rms", d["qw"], d["kw"], 1e-6, d["pos"], d["freq"])
+        q, k = kda.kda_qk_fwd(d["q"], d["k"], *opt)
+        return dict(kda.kda_qk_bwd(d["q"], d["k"], d["dyq"], d["dyk"], *opt), q=q, k=k)
+
+    want = [run(d) for d in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for d, s in zip(sets, streams):
+            with torch.cuda.stream(s):
+                got.append(run(d))
+        torch.cuda.synchronize()
+        assert all(torch.equal(w[k], g[k]) for w, g in zip(want, got) for k in w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = run(sets[0])
+    for k, v in sets[1].items():
+        sets[0][k].copy_(v)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(want[1][k], res[k]) for k in res) and kda.device_error() == 0
