@@ -27,7 +27,7 @@ __device__ __forceinline__ float step_of(float dt, float bias, int softplus, flo
 
 // Sums of log decays are kept as two floats hi + lo (about 48 bits), added by error-free sums: the difference
 // of two of them, which is what the kernels exponentiate, then has the relative error of one 32-bit
-// rounding however large the sums are. (In fp64 the same sums took three quarters of a tile's time.)
+// rounding however large the sums are. (In fp64, which this GPU has little of, the same sums took most of a tile's time.)
 struct Two {
     float hi, lo;
 };
@@ -115,6 +115,10 @@ __device__ __forceinline__ uint32_t at(int row, int chunk) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
     const int bytes = valid ? 16 : 0;   // 0: the 16 bytes are filled with zeros and nothing is read
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid) {
+    const int bytes = valid ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }

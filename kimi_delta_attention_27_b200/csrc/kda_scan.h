@@ -59,8 +59,8 @@ cudaError_t launch_scan_decode(const ScanDecodeParams &p, cudaStream_t stream);
 cudaError_t read_and_clear_scan_error(unsigned int *value);
 
 // Steps of the forward that the backward takes too (kda_scan_fwd.cu): the states entering every
-// 64-token cell of every sequence (states), and the gradients of the states leaving them (grads; what reaches
-// a sequence's start goes to dh0). Cells lie on the global grid of 64 tokens; sequence i's cell c has
+// cell of every sequence (states), and the gradients of the states leaving them (grads; what reaches a
+// sequence's start goes to dh0). Cells (see scan_cells) lie on one grid over all tokens; sequence i's cell c has
 // slot i + c of [slots, H, N, P]. `ws`: scan_states_workspace_bytes.
 size_t scan_states_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N);
 cudaError_t launch_scan_states(const ScanParams &p, float *states, float *grads, float *ws, cudaStream_t stream);
@@ -74,7 +74,7 @@ struct ScanStateRun {
     const float *entering;   // the states that pieces enter with, or nullptr: h0 (dhT) where a sequence begins (ends)
     float *leave;            // what each piece adds, from zero, and its decay [pieces, H]; or nullptr
     float *leave_decay;
-    float *states;           // the state at the entry (reverse: exit) of every 64-token cell, or nullptr
+    float *states;           // the state at the entry (reverse: exit) of every cell of 128 tokens, or nullptr
 };
 cudaError_t launch_scan_tc_state(const ScanParams &p, int parts, int directions, int64_t seg, int64_t units,
                                  const ScanStateRun &fwd, const ScanStateRun &rev, cudaStream_t stream);
@@ -84,7 +84,19 @@ cudaError_t read_and_clear_scan_bwd_error(unsigned int *value);
 
 constexpr int kScanTile = 64;     // tokens per tile
 constexpr int kScanTcTile = 128;  // and of launch_scan_tc
-// slots of the 64-token cells of n sequences over `rows` tokens
-inline int64_t scan_cells(int64_t rows, int64_t n) { return rows / kScanTile + n; }
+// The backward's tiles, and the cells that its states are kept for: 64 tokens at a state size of 64, else 128. Slots
+// of the cells of n sequences over `rows` tokens:
+inline int64_t scan_cells(int64_t rows, int64_t n, int32_t N) { return rows / (N == 64 ? kScanTile : kScanTcTile) + n; }
+
+// The gradients of all tiles (kda_scan_bwd.cu, and kda_scan_tc_bwd.cu for a state size of 128)
+struct BwdWork {
+    const float *states, *grads;   // [cells, H, N, P]: entering states, gradients of leaving states
+    float *dbc;                    // [2][splits][rows][G][N] or nullptr (one split: written to dB, dC)
+    float *part;                   // [cells][3][H]: sums of d dlog a, ddt, Q_tt
+    int32_t splits;
+    int64_t cells;
+};
+cudaError_t launch_scan_tc_bwd(const ScanParams &p, const BwdWork &w, cudaStream_t stream);
+cudaError_t read_and_clear_scan_tc_bwd_error(unsigned int *value);
 
 }  // namespace kda

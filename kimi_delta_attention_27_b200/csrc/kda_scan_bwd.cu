@@ -18,13 +18,17 @@
 // bf16 parts (24 bits). M, K and the copy of R that makes dx are rounded to bf16 once, for results in bf16.
 //
 // The states S_0 and gradients R of every tile come from two sweeps (launch_scan_states), fp32 in the
-// workspace: that is its bulk, and what bounds the backward's traffic. The gradient kernel then takes all
-// tiles at once. One CTA has one tile of one group and walks (a share of) the group's heads, so C B^T is
-// computed once, and dB and dC add up over the heads in registers, without atomics: N / 16 warps own 16
-// columns of dC each and multiply with S_0, N / 16 others own dB and multiply with R; Q, M, K and dx are shared
-// out over all of them. (Half as many warps with both: 666 us instead of the time below.) The next head's x and dy, and once this one's have been used its S_0 and
-// R, arrive by TMA: issuing those loads from all threads took a quarter of a head's time. Where tiles x groups leave SMs idle the heads are shared out over several CTAs, whose dB
-// and dC are added by scan_bc_kernel in a fixed order. Sums over tokens go by partial sums per tile, too: runs repeat bit for bit.
+// workspace. The gradient kernel then takes all tiles at once: the one of this file at a state size of 64, that of
+// kda_scan_tc_bwd.cu, with tiles of 128 tokens, at 128. Here one CTA has one tile of one group and walks (a share of)
+// the group's heads, so C B^T is computed once, and dB and dC add up over the heads in registers, without atomics:
+// N / 16 warps own 16 columns of dC each and multiply with S_0, N / 16 others own dB and multiply with R; Q, M, K and
+// dx are shared out over all of them. The next head's x and dy, and once this one's have been used its S_0 and R, arrive
+// by TMA. Where tiles x groups leave SMs idle the heads are shared out over several CTAs, whose dB and dC are added by
+// scan_bc_kernel in a fixed order. Sums over tokens go by partial sums per tile, too: runs repeat bit for bit.
+//
+// Bound by shared memory, which the fragments of every product come from, and by the chain of a head's phases: 5 packed
+// sequences, 5001 tokens x 32 heads x 128, 2 groups, 64 entries: 192 us (198 with a head's steps waited for at the head;
+// the workspace's 0.33 GB alone is 50 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -33,7 +37,13 @@
 namespace kda {
 namespace scan {
 
-template <int N>
+struct BwdGates : Gates {
+    float slope[T];   // of the step in dt
+    float A, D, pad2[2];
+};
+
+constexpr int N = 64;
+
 struct BwdSmem {
     static constexpr int NW = N / 16;                      // warps for dC, and as many for dB: 16 columns each
     static constexpr int kBC = T * N * 2, kX = T * PC * 2, kM = T * T * 2;
@@ -42,13 +52,14 @@ struct BwdSmem {
     static constexpr int kMt = kXY + 4 * kX, kKt = kMt + kM;
     static constexpr int kR = kKt + kM;                    // R in bf16, N x 64
     static constexpr int kGates = kR + N * PC * 2;
-    static constexpr int kRow = kGates + 3 * static_cast<int>(sizeof(Gates));   // [8][T] row sums of M . Q d
+    static constexpr int kRow = kGates + 3 * static_cast<int>(sizeof(BwdGates));   // [8][T] row sums of M . Q d
     static constexpr int kCol = kRow + 8 * T * 4;          // [4][T] column sums of M . Q, without the diagonal
     static constexpr int kDiag = kCol + 4 * T * 4;         // [2][T] the diagonals of M . Q and of Q
     static constexpr int kInt = kDiag + 2 * T * 4;         // [2][NW][T] C . (S_0 dy) and B . (R x)
     static constexpr int kRS = kInt + 2 * NW * T * 4;      // [2 NW] <R, S_0>
     static constexpr int kTok = kRS + 64;                  // [5][T] per token, summed over a head's slices; <R, S_0>
-    static constexpr int kBars = kTok + 5 * T * 4 + 16;
+    static constexpr int kNext = kTok + 5 * T * 4 + 16;    // the next head's dt, A, bias and D
+    static constexpr int kBars = kNext + (T + 4) * 4;
     static constexpr int kState = (kBars + 64 + 1023) / 1024 * 1024;   // S_0, R: each two blocks of 32 columns
     static constexpr int kBytes = kState + 2 * N * PC * 4;
     static_assert(kBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
@@ -66,14 +77,6 @@ struct BwdMaps {
     CUtensorMap x, dy, states, grads;
 };
 
-struct BwdWork {
-    const float *states, *grads;   // [cells, H, N, P]: entering states, gradients of leaving states
-    float *dbc;                    // [2][splits][rows][G][N] or nullptr (one split: written to dB, dC)
-    float *part;                   // [cells][3][H]: sums of d dlog a, ddt, Q_tt
-    int32_t splits;
-    int64_t cells;
-};
-
 // two consecutive columns of two rows of a state as a B fragment in S parts: element [n][p], k = p
 template <int S>
 __device__ __forceinline__ void state_frag(const float2 &v0, const float2 &v1, uint32_t (&b)[S][2]) {
@@ -86,13 +89,12 @@ __device__ __forceinline__ void state_frag(const float2 &v0, const float2 &v1, u
     for (int s = 0; s < S; ++s) b[s][1] = part[s];
 }
 
-template <int N>
 __global__ void __launch_bounds__(4 * N, 1) scan_bwd_kernel(ScanParams p, BwdWork w, const __grid_constant__ BwdMaps maps) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    using L = BwdSmem<N>;
+    using L = BwdSmem;
     constexpr int NW = L::NW, ALL = 2 * NW, NT = 32 * ALL, ROWB = N * 2, BLOCKS = (20 + ALL - 1) / ALL, XT = 32 / ALL;
     const uint32_t base = smem_addr(smem);
-    Gates *gates = reinterpret_cast<Gates *>(smem + L::kGates);
+    BwdGates *gates = reinterpret_cast<BwdGates *>(smem + L::kGates);
     float *rows_s = reinterpret_cast<float *>(smem + L::kRow), *cols_s = reinterpret_cast<float *>(smem + L::kCol);
     float *diag_s = reinterpret_cast<float *>(smem + L::kDiag), *int_s = reinterpret_cast<float *>(smem + L::kInt);
     float *rs_s = reinterpret_cast<float *>(smem + L::kRS);
@@ -126,6 +128,43 @@ __global__ void __launch_bounds__(4 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
         ptx::fence_mbar_init();
     }
     __syncthreads();
+    // Gates, by one warp: what they take from memory is on its way a head ahead.
+    // Lane l copies and reads tokens 2l and 2l + 1; the last three words go through a lane each.
+    const float *next_s = reinterpret_cast<const float *>(smem + L::kNext);
+    auto fetch_gates = [&](int h) {
+        const uint32_t d = base + L::kNext;
+        const float *src = p.dt + start * p.H + h;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * lane + e;
+            cp_async4(d + t * 4, src + (t < cnt ? static_cast<int64_t>(t) * p.H : 0), t < cnt);
+        }
+        if (lane < 3) {
+            const float *f = lane == 0 ? p.A : lane == 1 ? p.dt_bias : p.D;
+            cp_async4(d + (T + lane) * 4, (f ? f : p.A) + h, f != nullptr);
+        }
+        cp_async_commit();
+    };
+    auto make_head = [&](BwdGates &g) {
+        cp_async_wait_all();
+        __syncwarp();
+        const float A = next_s[T], bias = next_s[T + 1];
+        float d[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * lane + e;
+            float u;
+            d[e] = step_of(next_s[t], bias, p.softplus, &u);
+            if (t >= cnt) d[e] = 0.f;
+            g.slope[t] = p.softplus ? 1.f / (1.f + expf(-u)) : 1.f;
+        }
+        make_gates(g, d[0], d[1], A);
+        if (lane == 0) {
+            g.A = A;
+            g.D = next_s[T + 2];
+        }
+        __syncwarp();
+    };
     // by one thread
     auto fetch = [&](int k, int stage) {
         const int32_t col = (hb + k / slices) * p.P + (k % slices) * PC, row = static_cast<int32_t>(start);
@@ -149,10 +188,10 @@ __global__ void __launch_bounds__(4 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
         fetch(0, 0);
         fetch_state(0);
     }
-    if (warp == 0) {
-        float d0, d1;
-        load_steps(p, start, cnt, hb, d0, d1);
-        make_gates(gates[0], d0, d1, p.A[hb]);
+    if (warp == NW - 2) {
+        fetch_gates(hb);
+        make_head(gates[0]);
+        if (hb + 1 < he) fetch_gates(hb + 1);
     }
     cp_async_wait_all();
     __syncthreads();
@@ -188,7 +227,7 @@ __global__ void __launch_bounds__(4 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
     float *tok_s = reinterpret_cast<float *>(smem + L::kTok);   // q, int, in, dd, Q_tt (see below)
 
     // The steps' gradients of head h from its tokens' sums, by one warp (lane l: tokens 2l and 2l + 1).
-    auto finish_head = [&](int h, const Gates &g) {
+    auto finish_head = [&](int h, const BwdGates &g) {
         float v[10];
 #pragma unroll
         for (int j = 0; j < 5; ++j) {
@@ -210,16 +249,12 @@ __global__ void __launch_bounds__(4 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
         if (lane == 0) before = 0.f;
         const float rest = g.total * tok_s[5 * T];
         const float dl[2] = {suf + (before + rest), after + (v[1] + v[3]) + (before + v[4] + rest)};
-        const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
         float sa = 0.f, sb = 0.f, sd = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int t = 2 * lane + e;
             if (t < cnt) {
-                float uu;
-                step_of(p.dt[(start + t) * p.H + h], bias, 0, &uu);
-                float dd = fmaf(dl[e], A, v[6 + e]);
-                if (p.softplus) dd *= 1.f / (1.f + expf(-uu));
+                const float dd = fmaf(dl[e], g.A, v[6 + e]) * g.slope[t];
                 p.ddt[(start + t) * p.H + h] = dd;
                 sa = fmaf(dl[e], g.d[t], sa);
                 sb += dd;
@@ -242,7 +277,7 @@ __global__ void __launch_bounds__(4 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
     bool ok = true;
     for (int k = 0; k < work; ++k) {
         const int h = hb + k / slices, sl = k % slices, stage = k & 1;
-        const Gates &g = gates[(k / slices) % 3];
+        const BwdGates &g = gates[(k / slices) % 3];
         const uint32_t xt = base + L::kXY + stage * 2 * L::kX, dyt = xt + L::kX;
         // all of the last head's sums, M, K and the other stage are free
         if (k > 0 && __syncthreads_or(!ok)) break;
@@ -258,7 +293,7 @@ __global__ void __launch_bounds__(4 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
             ptx::fence_proxy_async_smem();
             __syncthreads();
         }
-                // ---- Q, M, K and the sums of M . Q; the blocks' products side by side
+        // ---- Q, M, K and the sums of M . Q; the blocks' products side by side
         float qs[BLOCKS][4];
 #pragma unroll
         for (int j = 0; j < BLOCKS; ++j) qs[j][0] = qs[j][1] = qs[j][2] = qs[j][3] = 0.f;
@@ -395,9 +430,8 @@ __global__ void __launch_bounds__(4 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
         // head's gates (its own buffer: the last one's are in use)
         if (warp == NW - 1 && sl == 0 && k > 0) finish_head(h - 1, gates[(k / slices + 2) % 3]);
         if (warp == NW - 2 && sl == slices - 1 && h + 1 < he) {
-            float d0, d1;
-            load_steps(p, start, cnt, h + 1, d0, d1);
-            make_gates(gates[(k / slices + 1) % 3], d0, d1, p.A[h + 1]);
+            make_head(gates[(k / slices + 1) % 3]);
+            if (h + 2 < he) fetch_gates(h + 2);
         }
         __syncthreads();   // M, K, R and the sums are complete, S_0 and R used
         if (tid == 0 && k + 1 < work) {
@@ -469,20 +503,28 @@ __global__ void __launch_bounds__(4 * N, 1) scan_bwd_kernel(ScanParams p, BwdWor
                     mma(out[2 * j + 1], a, b[2], b[3]);
                 }
             }
-            const float Dh = p.D ? p.D[h] : 0.f;
+            const float Dh = g.D;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int t = row + 8 * e;
-                if (t < cnt) {
-                    const float d = g.d[t];
-                    uint16_t *dst = p.dx + (start + t) * p.dx_stride + static_cast<int64_t>(h) * p.P + sl * PC;
+                const float d = g.d[t];
+                uint16_t *dst = p.dx + (start + t) * p.dx_stride + static_cast<int64_t>(h) * p.P + sl * PC;
 #pragma unroll
-                    for (int j = 0; j < XT; ++j) {
+                for (int j = 0; j < XT; j += 2) {
+                    // two lanes exchange a pair each: four columns in a row for either
+                    uint32_t v[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
                         const uint32_t y =
-                            *reinterpret_cast<const uint32_t *>(smem + (dyt - base) + at<PC * 2>(t, c0 + j) + q2 * 2);
-                        *reinterpret_cast<uint32_t *>(dst + (c0 + j) * 8 + q2) =
-                            bf_pair(fmaf(Dh, bf_low(y), d * out[j][2 * e]), fmaf(Dh, bf_high(y), d * out[j][2 * e + 1]));
+                            *reinterpret_cast<const uint32_t *>(smem + (dyt - base) + at<PC * 2>(t, c0 + j + i) + q2 * 2);
+                        v[i] = bf_pair(fmaf(Dh, bf_low(y), d * out[j + i][2 * e]),
+                                       fmaf(Dh, bf_high(y), d * out[j + i][2 * e + 1]));
                     }
+                    const bool odd = lane & 1;
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
+                    if (t < cnt)
+                        *reinterpret_cast<uint2 *>(dst + (c0 + j + odd) * 8 + (q2 & 4)) =
+                            odd ? make_uint2(got, v[1]) : make_uint2(v[0], got);
                 }
             }
         }
@@ -587,8 +629,8 @@ __global__ void __launch_bounds__(256) scan_sum_kernel(ScanParams p, BwdWork w) 
 
 // CTAs that share a group's heads: the number that leaves the longest-working SM the fewest (tile, head)s, with one
 // CTA per SM; the smallest such one, since each CTA's share of dB and dC is written and read again.
-int head_splits(int64_t rows, int64_t n, int32_t H, int32_t G) {
-    const int64_t ctas = scan_cells(rows, n) * G;
+int head_splits(int64_t rows, int64_t n, int32_t H, int32_t G, int32_t N) {
+    const int64_t ctas = scan_cells(rows, n, N) * G;
     const int per_group = H / G;
     int64_t best = 0;
     int best_s = 1;
@@ -612,9 +654,9 @@ struct BwdLayout {
 };
 BwdLayout bwd_layout(int64_t rows, int64_t n, int32_t H, int32_t G, int32_t P, int32_t N) {
     BwdLayout l;
-    const size_t cells = static_cast<size_t>(scan_cells(rows, n));
+    const size_t cells = static_cast<size_t>(scan_cells(rows, n, N));
     const size_t all = cells * H * N * P * sizeof(float);
-    l.splits = head_splits(rows, n, H, G);
+    l.splits = head_splits(rows, n, H, G, N);
     l.states = 0;
     l.grads = round256(all);
     l.dbc = l.grads + round256(all);
@@ -624,10 +666,9 @@ BwdLayout bwd_layout(int64_t rows, int64_t n, int32_t H, int32_t G, int32_t P, i
     return l;
 }
 
-template <int N>
 cudaError_t bwd_launch(const ScanParams &p, const BwdWork &w, cudaStream_t s) {
-    constexpr int bytes = BwdSmem<N>::kBytes;
-    cudaError_t err = allow_smem(scan_bwd_kernel<N>, bytes);
+    constexpr int bytes = BwdSmem::kBytes;
+    cudaError_t err = allow_smem(scan_bwd_kernel, bytes);
     if (err != cudaSuccess) return err;
     const int64_t ctas = w.cells * p.G * w.splits;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -640,7 +681,7 @@ cudaError_t bwd_launch(const ScanParams &p, const BwdWork &w, cudaStream_t s) {
                        !tc::encode(&maps.states, f32, 4, w.states, p.P, all, p.P, N) ||
                        !tc::encode(&maps.grads, f32, 4, w.grads, p.P, all, p.P, N)))
         return cudaErrorInvalidValue;
-    scan_bwd_kernel<N><<<static_cast<unsigned>(ctas), 4 * N, bytes, s>>>(p, w, maps);
+    scan_bwd_kernel<<<static_cast<unsigned>(ctas), 4 * N, bytes, s>>>(p, w, maps);
     return cudaGetLastError();
 }
 
@@ -662,10 +703,10 @@ cudaError_t launch_scan_bwd(const ScanParams &p, cudaStream_t s) {
     w.dbc = l.splits > 1 ? reinterpret_cast<float *>(ws + l.dbc) : nullptr;
     w.part = reinterpret_cast<float *>(ws + l.part);
     w.splits = l.splits;
-    w.cells = scan_cells(p.rows, p.seqs.n);
+    w.cells = scan_cells(p.rows, p.seqs.n, p.N);
     cudaError_t err = launch_scan_states(p, states, grads, pieces, s);
     if (err == cudaSuccess && w.cells > 0)
-        err = by_state(p.N, [&](auto n) { return bwd_launch<decltype(n)::value>(p, w, s); });
+        err = p.N == 128 ? launch_scan_tc_bwd(p, w, s) : bwd_launch(p, w, s);
     if (err == cudaSuccess && w.dbc && p.rows > 0) {
         const int64_t blocks = (p.rows * p.G * p.N / 4 + 255) / 256;
         if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

@@ -434,12 +434,14 @@ __global__ void __launch_bounds__(256) scan_join_kernel(ScanParams p, int64_t se
 }
 
 // Tokens per piece, a multiple of `tile`; 0: whole sequences. `ctas`: CTAs of one piece, `slots` as many as run at
-// once. A cut costs a second reading of x and B, one state per piece and, in all, about 1.55 times the time; whole
-// sequences take as long as the longest. So they are cut where that is longer: with equal ones where they fill fewer
-// than slots / 1.55, with packed ones, of which the longest is taken to be twice the mean, twice that. (8 packed
-// sequences of 64 heads: whole 0.43 ms, cut 0.82 ms; one of 65536 tokens x 32 heads x 128: cut 0.89 ms, whole 2.7 ms.)
+// once. Whole sequences take as long as the longest; a cut costs a second reading of x and B, one state per piece and
+// two more launches, 1.5 times the work where the pieces are long and over twice that where they are not. So sequences
+// are cut where equal ones fill less than half of the slots, and packed ones, of which the longest is taken to be twice
+// the mean, fewer than all. (4096 tokens x 64 heads x 64: 2 sequences, 64 CTAs, 176 us whole, 181 cut; 3 sequences 181
+// and 231. One of 65536 tokens x 32 heads x 128, 32 CTAs: 2.62 ms whole, 0.86 cut. The states of 5 packed ones for the
+// gradients, 320 CTAs of 296: 123 us whole, 163 cut.)
 int64_t piece_tokens(int64_t rows, int64_t n, bool packed, int64_t ctas, int slots, int tile) {
-    if (n == 0 || 2 * n * ctas >= (packed ? 5 : 3) * slots / 2) return 0;
+    if (n == 0 || (packed ? 1 : 2) * n * ctas >= slots) return 0;
     const int64_t want = 2 * slots;
     int64_t seg = (rows * ctas + want - 1) / want;
     seg = (seg + tile - 1) / tile * tile;
@@ -455,10 +457,12 @@ int64_t fwd_piece_tokens(int64_t rows, int64_t n, bool packed, int32_t H, int32_
     return takes_tc(rows, n, N) ? piece_tokens(rows, n, packed, (columns + 1) / 2, 148, kScanTcTile)
                                 : piece_tokens(rows, n, packed, columns, 2 * 148, T);
 }
-// the backward's runs of the state, both directions at once
+// The backward's runs of the state, both directions at once; at a state size of 128 their tiles take so little that
+// packed sequences, too, are cut only below half of the slots (the gradients of 2 packed ones, 13493 tokens x 64 heads:
+// 656 us whole, 827 cut).
 int64_t state_piece_tokens(int64_t rows, int64_t n, bool packed, int32_t H, int32_t P, int32_t N) {
     const int64_t columns = static_cast<int64_t>(H) * (P / PC);
-    return N == 128 ? piece_tokens(rows, n, packed, (columns + 1) / 2 * 2, 148, T)
+    return N == 128 ? piece_tokens(rows, n, false, (columns + 1) / 2 * 2, 148, T)
                     : piece_tokens(rows, n, packed, columns, 2 * 148, T);
 }
 

@@ -292,13 +292,14 @@ __global__ void __launch_bounds__(NT, 1)
                         sts(at_x, make_uint4(o[0], o[1], o[2], o[3]));
                     }
                 }
-                named_bar_sync(1 + hd, 256);
-                uint16_t *out = p.out + start_of(i) * p.out_stride + static_cast<int64_t>(v) * PC + (t256 & 7) * 8;
+                // the warp's rows, 64 bytes of each
+                __syncwarp();
+                const int chunk = 4 * hf + (lane & 3);
+                uint16_t *out = p.out + start_of(i) * p.out_stride + static_cast<int64_t>(v) * PC + chunk * 8;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int row = j * 32 + (t256 >> 3);
-                    if (row < cnt)
-                        *reinterpret_cast<uint4 *>(out + row * p.out_stride) = lds(xt + sw128(row, t256 & 7));
+                    const int row = wq * 32 + j * 8 + (lane >> 2);
+                    if (row < cnt) *reinterpret_cast<uint4 *>(out + row * p.out_stride) = lds(xt + sw128(row, chunk));
                 }
                 fence_proxy_async_smem();   // x's next load comes after these reads and writes
                 x.arrive(kXFree + hd * 2 + stage);

@@ -58,8 +58,7 @@ __device__ __forceinline__ uint4 lds(const uint8_t *p) { return *reinterpret_cas
 __device__ __forceinline__ void sts(uint8_t *p, uint4 v) { *reinterpret_cast<uint4 *>(p) = v; }
 __device__ __forceinline__ float f32(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t sw128(int r, int j) { return static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4)); }
-// Whether the phase of the given parity has completed. Acquire at CTA scope: nothing here comes from another CTA,
-// and at cluster scope each such look costs some 300 cycles, more than most of the work between two of them.
+// Whether the phase of the given parity has completed. Acquire at CTA scope: nothing here comes from another CTA.
 __device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(

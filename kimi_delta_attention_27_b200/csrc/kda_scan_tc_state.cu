@@ -1,7 +1,7 @@
 // kda_scan_tc_state.cu -- the scan's state alone, state size 128, on tcgen05, sm_100a.
 //
 // Two uses: what each piece of a cut sequence adds to the state (kda_scan_fwd.cu), and, for the backward, the
-// state S entering every tile of 64 tokens and the gradient R of the state leaving it:
+// state S entering every cell of 128 tokens, two tiles, and the gradient R of the state leaving it:
 //
 //   S_end = e^(Gamma_end) S_0 + B^T Diag(d e^(Gamma_end - Gamma)) x          tiles in order
 //   R_0   = e^(Gamma_end) R_end + C^T Diag(e^Gamma) dy                       tiles backwards (blockIdx.y 1)
@@ -193,7 +193,11 @@ __global__ void __launch_bounds__(NT, 1)
                 total = next_total;
                 if (i + 1 < tiles) ok = write_parts(i + 1);
                 if (!ok) break;
-                if (run.states) store(run.states + ((u.i + cell(i)) * p.H + h) * sn + at_r);
+                if (run.states) {
+                    // of the two tiles of a cell the one that the direction enters first
+                    const int64_t c = cell(i);
+                    if ((c & 1) == (rev ? 1 : 0) || (head && i == 0)) store(run.states + ((u.i + c / 2) * p.H + h) * sn + at_r);
+                }
                 ok = x.wait(kU + (i & 1), (i >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
