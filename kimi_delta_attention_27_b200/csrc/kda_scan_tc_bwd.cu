@@ -53,6 +53,7 @@ struct Partials {
     float col[4][TT];       // and of Mt . Qt, without the diagonal
     float leave[4][TT];     // dy . Y over 16 columns
     float enter[4][TT];     // x . Z
+    float near[TT];         // of Mt . Qt d over the token's own quarter
     float diag[TT], q[TT];  // the diagonals of Mt . Qt and of Qt
     float rs[16];           // <R, S_0>
 };
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
                 const float gh = g.hi[r], gl = g.lo[r], ds = g.d[r];
                 const float rf = ex2((g.open_hi[cq] - gh) + (g.open_lo[cq] - gl));
                 const float2 rf2 = make_float2(rf, rf), ds2 = make_float2(ds, ds);
-                float2 col = make_float2(0.f, 0.f);
+                float2 col = make_float2(0.f, 0.f), near = make_float2(0.f, 0.f);
                 float on_diag = 0.f, q_diag = 0.f;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -376,6 +377,8 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
                                 col.x += c > lane ? hq.x : 0.f;
                                 col.y += c + 1 > lane ? hq.y : 0.f;
                                 hw = make_float2(c > lane ? hw.x : 0.f, c + 1 > lane ? hw.y : 0.f);
+                                near.x += hw.x;
+                                near.y += hw.y;
                                 m = make_float2(c >= lane ? m.x : 0.f, c + 1 >= lane ? m.y : 0.f);
                                 kk = make_float2(c >= lane ? kk.x : 0.f, c + 1 >= lane ? kk.y : 0.f);
                             }
@@ -391,6 +394,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
                 }
                 add_to(sums.col[cq][r], col.x + col.y, sl > 0);
                 if constexpr (kKind > 0) {
+                    add_to(sums.near[r], near.x + near.y, sl > 0);
                     add_to(sums.diag[r], on_diag, sl > 0);
                     add_to(sums.q[r], q_diag, sl > 0);
                 }
@@ -674,22 +678,33 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             const HeadGates &g = gates[(hh - 1) & 1];
             ok = x.wait(kSums, (hh - 1) & 1);
             if (!ok) break;
-            float qi[4], in[4], dd[4], qq[4];   // per token: sums over later pairs, what enters, through the input, Qt
+            // Pairs s < t <= u of dlog a_t: within t's quarter they are what its later rows have more than its later
+            // columns, and only there is anything subtracted; with one of the two or both in other quarters they are sums.
+            float own[4], to_u[4], from_s[4], lv[4], in[4], dd[4], qq[4], z1 = 0.f, z2 = 0.f;
+            const int quarter = lane >> 3;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int t = t4 + j, quarter = lane >> 3;
-                float row = 0.f, col = 0.f, lv = 0.f, en = 0.f;
+                const int t = t4 + j;
+                float l = 0.f, en = 0.f, row = 0.f, col = 0.f, c0 = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    if (e <= quarter) row += sums.row[e][t];
-                    if (e >= quarter) col += sums.col[e][t];
-                    lv += sums.leave[e][t];
+                    l += sums.leave[e][t];
                     en += sums.enter[e][t];
+                    if (e < quarter) row += sums.row[e][t];
+                    if (e > quarter) col += sums.col[e][t];
+                    if (e == quarter) {
+                        own[j] = sums.row[e][t] - sums.near[t];
+                        c0 = sums.col[e][t];
+                    }
                 }
+                if (quarter >= 2) z1 += sums.row[0][t];
+                if (quarter == 3) z2 += sums.row[0][t] + sums.row[1][t];
                 en *= g.to[t];
-                qi[j] = fmaf(-g.d[t], col, row) + g.from[t] * lv;
+                to_u[j] = row;
+                from_s[j] = g.d[t] * col;
+                lv[j] = g.from[t] * l;
                 in[j] = g.d[t] * en;
-                dd[j] = col + sums.diag[t] + en;
+                dd[j] = c0 + col + sums.diag[t] + en;
                 qq[j] = sums.q[t];
             }
             float rs = lane < 16 ? sums.rs[lane] : 0.f;
@@ -697,29 +712,58 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
 #pragma unroll
             for (int m = 8; m > 0; m >>= 1) rs += __shfl_xor_sync(0xffffffffu, rs, m);
             rs = g.total * __shfl_sync(0xffffffffu, rs, 0);
-            // suffix sums of qi, prefix sums of in
-            const float qi_all = (qi[0] + qi[1]) + (qi[2] + qi[3]), in_all = (in[0] + in[1]) + (in[2] + in[3]);
-            float suf = qi_all, pre = in_all;
+            // sums over later (earlier) tokens: over the tile, and over the quarter
+            float later = (lv[0] + lv[1]) + (lv[2] + lv[3]), earlier = (in[0] + in[1]) + (in[2] + in[3]);
+            float later8 = (own[0] + own[1]) + (own[2] + own[3]), cross8 = (to_u[0] + to_u[1]) + (to_u[2] + to_u[3]);
+            float earlier8 = (from_s[0] + from_s[1]) + (from_s[2] + from_s[3]);
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
-                const float a = __shfl_down_sync(0xffffffffu, suf, m), b = __shfl_up_sync(0xffffffffu, pre, m);
-                if (lane + m < 32) suf += a;
-                if (lane >= m) pre += b;
+                const float a = __shfl_down_sync(0xffffffffu, later, m), b = __shfl_up_sync(0xffffffffu, earlier, m);
+                if (lane + m < 32) later += a;
+                if (lane >= m) earlier += b;
+                z1 += __shfl_xor_sync(0xffffffffu, z1, m);
+                z2 += __shfl_xor_sync(0xffffffffu, z2, m);
+                if (m < 8) {
+                    const float c = __shfl_down_sync(0xffffffffu, later8, m), d = __shfl_down_sync(0xffffffffu, cross8, m);
+                    const float e = __shfl_up_sync(0xffffffffu, earlier8, m);
+                    if ((lane & 7) + m < 8) {
+                        later8 += c;
+                        cross8 += d;
+                    }
+                    if ((lane & 7) >= m) earlier8 += e;
+                }
             }
-            float after = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
-            if (lane == 31) after = 0.f;
-            if (lane == 0) before = 0.f;
+            auto before_lane = [&](float v, int width) {
+                const float o = __shfl_up_sync(0xffffffffu, v, 1);
+                return lane & (width - 1) ? o : 0.f;
+            };
+            auto behind_lane = [&](float v, int width) {
+                const float o = __shfl_down_sync(0xffffffffu, v, 1);
+                return (lane & (width - 1)) < width - 1 ? o : 0.f;
+            };
+            later = behind_lane(later, 32);
+            later8 = behind_lane(later8, 8);
+            cross8 = behind_lane(cross8, 8);
+            earlier = before_lane(earlier, 32);
+            earlier8 = before_lane(earlier8, 8);
+            const float far = rs + (quarter == 1 ? z1 : quarter == 2 ? z2 : 0.f);
             float dl[4];
 #pragma unroll
             for (int j = 3; j >= 0; --j) {
-                after += qi[j];
-                dl[j] = after;
+                later += lv[j];
+                later8 += own[j];
+                cross8 += to_u[j];
+                dl[j] = (later8 + cross8) + (later + far);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                dl[j] += earlier + earlier8;
+                earlier += in[j];
+                earlier8 += from_s[j];
             }
             float sa = 0.f, sb = 0.f, sd = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                dl[j] += before + rs;
-                before += in[j];
                 const int t = t4 + j;
                 if (t < cnt) {
                     const float v = fmaf(dl[j], g.A, dd[j]) * g.slope[t];
