@@ -345,14 +345,13 @@ kda_status kda_decode(const void *q, const void *k, const void *v, const float *
 
 kda_status kda_device_error(void) {
     if (cudaDeviceSynchronize() != cudaSuccess) return KDA_ERR_CUDA;
-    unsigned int v = 0, conv = 0, scan = 0, scan_tc = 0, scan_state = 0, scan_bwd = 0, scan_tc_bwd = 0;
+    unsigned int v = 0, conv = 0, scan = 0, scan_tc = 0, scan_state = 0, scan_tc_bwd = 0;
     if (kda::read_and_clear_device_error(&v) != cudaSuccess || kda::read_and_clear_conv_error(&conv) != cudaSuccess ||
         kda::read_and_clear_scan_error(&scan) != cudaSuccess || kda::read_and_clear_scan_tc_error(&scan_tc) != cudaSuccess ||
         kda::read_and_clear_scan_state_error(&scan_state) != cudaSuccess ||
-        kda::read_and_clear_scan_bwd_error(&scan_bwd) != cudaSuccess ||
         kda::read_and_clear_scan_tc_bwd_error(&scan_tc_bwd) != cudaSuccess)
         return KDA_ERR_CUDA;
-    v |= conv | scan | scan_tc | scan_state | scan_bwd | scan_tc_bwd;
+    v |= conv | scan | scan_tc | scan_state | scan_tc_bwd;
     if (v & kda::kErrCuSeqlens) return KDA_ERR_BAD_CU_SEQLENS;
     if (v & kda::kErrTimeout) return KDA_ERR_TIMEOUT;
     if (v & kda::kErrRingIndex) return KDA_ERR_INTERNAL;

@@ -201,7 +201,7 @@ void scan_params(const ScanArgs &a, const kda::Seqs &s, int64_t rows, kda::ScanP
 bool scan_too_large(int64_t rows, int64_t n, int32_t H, int32_t P) {
     // rows are 32-bit coordinates of tensor maps; the largest grid is one CTA per (64-token cell, head, 64 columns)
     if (rows > 0x7fffffffLL) return true;
-    return kda::scan_cells(rows, n, 64) > 0x7fffffffLL / (static_cast<int64_t>(H) * (P / 64));
+    return 2 * kda::scan_cells(rows, n) > 0x7fffffffLL / (static_cast<int64_t>(H) * (P / 64));
 }
 
 kda_status check_workspace(const void *ws, size_t have, size_t need) {
@@ -515,7 +515,7 @@ kda_status kda_scan_bwd(const void *x, int64_t x_stride, const float *dt, const 
     KDA_TRY(check_stride(rows, db_stride, gn, 2));
     KDA_TRY(check_stride(rows, dc_stride, gn, 2));
     if (scan_too_large(rows, s.n, num_heads, head_dim) ||
-        kda::scan_cells(rows, s.n, state_dim) > 0x7fffffffLL / (static_cast<int64_t>(num_heads) * state_dim))
+        kda::scan_cells(rows, s.n) > 0x7fffffffLL / (static_cast<int64_t>(num_heads) * state_dim))
         return KDA_ERR_TOO_LARGE;   // the states' rows, too, are 32-bit coordinates
     const size_t need = kda::scan_bwd_workspace_bytes(rows, s.n, num_heads, num_groups, head_dim, state_dim);
     KDA_TRY(check_workspace(workspace, workspace_bytes, need));

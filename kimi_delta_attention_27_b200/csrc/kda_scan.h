@@ -80,15 +80,14 @@ cudaError_t launch_scan_tc_state(const ScanParams &p, int parts, int directions,
                                  const ScanStateRun &fwd, const ScanStateRun &rev, cudaStream_t stream);
 cudaError_t read_and_clear_scan_tc_error(unsigned int *value);
 cudaError_t read_and_clear_scan_state_error(unsigned int *value);
-cudaError_t read_and_clear_scan_bwd_error(unsigned int *value);
 
 constexpr int kScanTile = 64;     // tokens per tile
-constexpr int kScanTcTile = 128;  // and of launch_scan_tc
-// The backward's tiles, and the cells that its states are kept for: 64 tokens at a state size of 64, else 128. Slots
-// of the cells of n sequences over `rows` tokens:
-inline int64_t scan_cells(int64_t rows, int64_t n, int32_t N) { return rows / (N == 64 ? kScanTile : kScanTcTile) + n; }
+constexpr int kScanTcTile = 128;  // and of launch_scan_tc and the gradients
+// The backward's tiles, and the cells that its states are kept for, are those of kScanTcTile. Slots of the cells of n
+// sequences over `rows` tokens:
+inline int64_t scan_cells(int64_t rows, int64_t n) { return rows / kScanTcTile + n; }
 
-// The gradients of all tiles (kda_scan_bwd.cu, and kda_scan_tc_bwd.cu for a state size of 128)
+// The gradients of all tiles (kda_scan_tc_bwd.cu)
 struct BwdWork {
     const float *states, *grads;   // [cells, H, N, P]: entering states, gradients of leaving states
     float *dbc;                    // [2][splits][rows][G][N] or nullptr (one split: written to dB, dC)

@@ -370,12 +370,25 @@ __global__ void __launch_bounds__(NT, 3) scan_state_kernel(ScanParams p, int64_t
             decay = decay + make_gates(gates[(k + 1) & 1], d0, d1, A);
             if (k + 2 < n_tiles) load_steps(p, tile_start(u, cell(k + 2)), tile_count(u, cell(k + 2)), h, d0, d1);
         }
-        if (states)
-            write_state<MT>(acc, states, ((u.i + cell(k)) * p.H + h) * sn + col, true, p.P, n0);
+        // of the two tiles of a cell the one that the direction enters first
+        const int64_t c = cell(k);
+        if (states && ((c & 1) == (kReverse ? 1 : 0) || (head && k == 0)))
+            write_state<MT>(acc, states, ((u.i + c / 2) * p.H + h) * sn + col, true, p.P, n0);
         const Gates &g = gates[k & 1];
         const uint32_t rt = base + stage * kStage;
-        scale_state<MT>(acc, g.total);
-        add_outer<ROWB, MT, S>(acc, rt, rt + kR, kReverse ? g.from : g.weight, n0);
+        // the tile's share by itself: the tensor cores cut a sum off at its last bit, twelve times a tile
+        float share[MT][8][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) share[m][c][0] = share[m][c][1] = share[m][c][2] = share[m][c][3] = 0.f;
+        add_outer<ROWB, MT, S>(share, rt, rt + kR, kReverse ? g.from : g.weight, n0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][c][e] = fmaf(acc[m][c][e], g.total, share[m][c][e]);
     }
     if (leave) {
         write_state<MT>(acc, leave, (unit * p.H + h) * sn + col, true, p.P, n0);

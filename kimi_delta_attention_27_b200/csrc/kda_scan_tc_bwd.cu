@@ -58,11 +58,15 @@ struct Partials {
     float rs[16];           // <R, S_0>
 };
 
+// NS: state size
+template <int NS>
 struct BwdSmem {
-    static constexpr uint32_t kC = 0, kB = 2 * kBlock;
-    static constexpr uint32_t kXY = 4 * kBlock;                            // [stage] x and dy; before them, the last head's R
-    static constexpr uint32_t kParts = kXY + 4 * kBlock;                   // three parts of S_0, then of R
-    static constexpr uint32_t kK = kParts + 3 * kBlock;                    // S_0, then Kt: two blocks of columns
+    static constexpr uint32_t kTile = NS / 64 * kBlock;                    // B or C: blocks of 64 columns
+    static constexpr uint32_t kPart = NS * 128;                            // a part of a state: rows of 64 columns
+    static constexpr uint32_t kC = 0, kB = kTile;
+    static constexpr uint32_t kXY = 2 * kTile;               // [stage] x and dy; before them, the last head's R
+    static constexpr uint32_t kParts = kXY + 4 * kBlock;     // three parts of S_0, then of R
+    static constexpr uint32_t kK = kParts + 3 * kPart;       // S_0, then Kt: two blocks of columns
     static constexpr uint32_t kGates = kK + 2 * kBlock;                    // [2]
     static constexpr uint32_t kSums = kGates + 2 * sizeof(HeadGates);
     static constexpr uint32_t kBars = kSums + sizeof(Partials);
@@ -75,8 +79,6 @@ constexpr uint32_t kColDc = 0, kColDb = 128, kColQ = 256, kColM = 256, kColX = 3
 
 constexpr uint32_t kIdQ = idesc_f16(128, 128, 1, 0, 0);    // both K-major
 constexpr uint32_t kIdY = idesc_f16(128, 64, 1, 0, 1);     // K-major, MN-major
-constexpr uint32_t kIdDb = idesc_f16(128, 128, 1, 0, 1);
-constexpr uint32_t kIdDc = idesc_f16(128, 128, 1, 1, 1);
 
 struct BwdMaps {
     CUtensorMap x, dy, b, c, states, grads;
@@ -173,9 +175,12 @@ __device__ __forceinline__ float sum_lanes16(float (&v)[16]) {
     return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
+template <int NS>
 __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWork w, const __grid_constant__ BwdMaps maps) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    using L = BwdSmem;
+    using L = BwdSmem<NS>;
+    constexpr uint32_t kIdS = idesc_f16(128, NS, 1, 0, 0);    // with a state's transpose: K-major
+    constexpr uint32_t kIdDb = idesc_f16(128, NS, 1, 0, 1), kIdDc = idesc_f16(128, NS, 1, 1, 1);
     const uint32_t base = smem_u32(smem);
     __shared__ uint32_t s_tmem, s_abort;
     Ctx x;
@@ -226,10 +231,10 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
         bool ok = x.wait(kBcFull, 0);
         if (ok) {
             // rows behind the piece: of other tokens, or none
-            uint8_t *t = smem + (cq >> 1 ? L::kB : L::kC) + (cq & 1) * kBlock + r * 128;
+            uint8_t *t = smem + (cq >> 1 ? L::kB : L::kC) + r * 128 + (NS == 128 ? (cq & 1) * kBlock : (cq & 1) * 64);
             if (r >= cnt)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sts(t + j * 16, make_uint4(0u, 0u, 0u, 0u));
+                for (int j = 0; j < NS / 16; ++j) sts(t + j * 16, make_uint4(0u, 0u, 0u, 0u));
             fence_proxy_async_smem();
             x.arrive(kSParts);
         }
@@ -247,11 +252,18 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             x.arrive(kQReady);
             return true;
         };
-        // this thread's part of a state matrix: row r, columns 16 cq .. + 16, four at a time
-        auto state_at = [&](uint32_t tile, int j) {
-            return *reinterpret_cast<const float4 *>(smem + tile + (cq >> 1) * kBlock + sw128(r, (cq & 1) * 4 + j));
+        // this thread's part of a state matrix: of row sr JS times 8 columns, from 8 (s8 + j) on
+        constexpr int JS = NS / 64;
+        const int sr = NS == 128 ? r : r & 63, s8 = NS == 128 ? 2 * cq : 2 * cq + (wq >> 1);
+        auto state_at = [&](uint32_t tile, int j, int i) {
+            if constexpr (NS == 128)
+                return *reinterpret_cast<const float4 *>(smem + tile + (cq >> 1) * L::kPart + sw128(r, (cq & 1) * 4 + 2 * j + i));
+            else
+                return *reinterpret_cast<const float4 *>(smem + tile + (s8 >> 2) * L::kPart + sw128(sr, (s8 & 3) * 2 + i));
         };
-        auto part_at = [&](int e, int j) { return smem + L::kParts + e * kBlock + sw128(r, 2 * cq + j); };
+        auto part_at = [&](int e, int j) {
+            return smem + L::kParts + e * L::kPart + (NS == 128 ? sw128(r, 2 * cq + j) : sw128(sr, s8));
+        };
         auto split8 = [&](const float4 &f0, const float4 &f1, uint4 (&o)[3]) {
             uint32_t v[4][3];
             split<3>(f0.x, f0.y, v[0]);
@@ -318,9 +330,9 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             ok = x.wait(kSFull, ph);
             if (!ok) break;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < JS; ++j) {
                 uint4 o[3];
-                split8(state_at(L::kK, 2 * j), state_at(L::kK, 2 * j + 1), o);
+                split8(state_at(L::kK, j, 0), state_at(L::kK, j, 1), o);
 #pragma unroll
                 for (int e = 0; e < 3; ++e) sts(part_at(e, j), o[e]);
             }
@@ -436,10 +448,10 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             if (!ok) break;
             float2 rs2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < JS; ++j) {
                 uint4 o[3];
-                const float4 f0 = state_at(L::kXY + (stage ^ 1) * 2 * kBlock, 2 * j);
-                const float4 f1 = state_at(L::kXY + (stage ^ 1) * 2 * kBlock, 2 * j + 1);
+                const float4 f0 = state_at(L::kXY + (stage ^ 1) * 2 * kBlock, j, 0);
+                const float4 f1 = state_at(L::kXY + (stage ^ 1) * 2 * kBlock, j, 1);
                 const float2 f[4] = {make_float2(f0.x, f0.y), make_float2(f0.z, f0.w), make_float2(f1.x, f1.y), make_float2(f1.z, f1.w)};
 #pragma unroll
                 for (int e = 2; e >= 0; --e) {
@@ -503,18 +515,21 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
         // ---- dB and dC: this CTA's share, or the result where it has the whole group
         if (ok) {
 #pragma unroll
-            for (int which = 0; which < 2; ++which) {   // dB, dC
+            for (int i = 0; i < NS / 64; ++i) {
+                // 0: dB, 1: dC; 32 columns for this thread
+                const int which = NS == 128 ? i : cq >> 1, c32 = NS == 128 ? cq : cq & 1;
                 uint32_t a[32];
-                tmem_ld32(tmem + (which ? kColDc : kColDb) + 32 * cq + lanes, a);
+                tmem_ld32(tmem + (which ? kColDc : kColDb) + 32 * c32 + lanes, a);
                 tmem_wait_ld();
-                const int64_t at_n = static_cast<int64_t>(grp) * N + 32 * cq;
+                const int64_t at_n = static_cast<int64_t>(grp) * NS + 32 * c32;
                 if (r >= cnt) continue;
                 if (w.dbc) {
                     // planes: the splits' dB, then their dC
-                    float *d = w.dbc + (split_i + (which ? w.splits : 0)) * (p.rows * p.G * N) + (start + r) * p.G * N + at_n;
+                    float *d = w.dbc + (split_i + (which ? w.splits : 0)) * (p.rows * p.G * NS) + (start + r) * p.G * NS + at_n;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        reinterpret_cast<float4 *>(d)[j] = make_float4(f32(a[4 * j]), f32(a[4 * j + 1]), f32(a[4 * j + 2]), f32(a[4 * j + 3]));
+                        reinterpret_cast<float4 *>(d)[j] =
+                            make_float4(f32(a[4 * j]), f32(a[4 * j + 1]), f32(a[4 * j + 2]), f32(a[4 * j + 3]));
                 } else {
                     uint16_t *d = (which ? p.dC + (start + r) * p.dc_stride : p.dB + (start + r) * p.db_stride) + at_n;
 #pragma unroll
@@ -548,17 +563,17 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
         // fp32 states, two blocks of 32 columns
         auto load_state = [&](int k, const CUtensorMap *map, int bar, uint32_t dst) {
             if (elect_one()) {
-                const int32_t row = static_cast<int32_t>((unit * p.H + hb + k / slices) * N), col = (k % slices) * PC;
-                mbar_arrive_expect_tx(x.bar(bar), 2 * kBlock);
-                for (int j = 0; j < 2; ++j) tma_load_2d(base + dst + j * kBlock, map, x.bar(bar), col + 32 * j, row);
+                const int32_t row = static_cast<int32_t>((unit * p.H + hb + k / slices) * NS), col = (k % slices) * PC;
+                mbar_arrive_expect_tx(x.bar(bar), 2 * L::kPart);
+                for (int j = 0; j < 2; ++j) tma_load_2d(base + dst + j * L::kPart, map, x.bar(bar), col + 32 * j, row);
             }
             __syncwarp();
         };
         if (elect_one()) {
-            mbar_arrive_expect_tx(x.bar(kBcFull), 4 * kBlock);
-            for (int k = 0; k < 2; ++k) {
-                tma_load_2d(ct + k * kBlock, &maps.c, x.bar(kBcFull), grp * N + 64 * k, static_cast<int32_t>(start));
-                tma_load_2d(bt + k * kBlock, &maps.b, x.bar(kBcFull), grp * N + 64 * k, static_cast<int32_t>(start));
+            mbar_arrive_expect_tx(x.bar(kBcFull), 2 * L::kTile);
+            for (int k = 0; k < NS / 64; ++k) {
+                tma_load_2d(ct + k * kBlock, &maps.c, x.bar(kBcFull), grp * NS + 64 * k, static_cast<int32_t>(start));
+                tma_load_2d(bt + k * kBlock, &maps.b, x.bar(kBcFull), grp * NS + 64 * k, static_cast<int32_t>(start));
             }
         }
         __syncwarp();
@@ -570,7 +585,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma_f16(tmem + kColQ, k_major(bt, k), k_major(ct, k), kIdQ, k > 0);
+                for (int k = 0; k < NS / 16; ++k) mma_f16(tmem + kColQ, k_major(bt, k), k_major(ct, k), kIdQ, k > 0);
                 mma_commit(x.bar(kQ));
             }
             __syncwarp();
@@ -594,15 +609,15 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < NS / 16; ++j)
 #pragma unroll
                     for (int e = 2; e >= 0; --e)
-                        mma_f16(tmem + kColY, k_major(ct, j), mn_major(parts + e * kBlock, j), kIdY, !(j == 0 && e == 2));
+                        mma_f16(tmem + kColY, k_major(ct, j), mn_major(parts + e * L::kPart, j), kIdY, !(j == 0 && e == 2));
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int e = 1; e >= 0; --e)
-                        mma_f16_ts(tmem + kColDc, tmem + kColDy + 8 * j, k_major(parts + e * kBlock, j), kIdQ,
+                        mma_f16_ts(tmem + kColDc, tmem + kColDy + 8 * j, k_major(parts + e * L::kPart, j), kIdS,
                                    !(k == 0 && j == 0 && e == 1));
                 mma_commit(x.bar(kSDone));
             }
@@ -629,16 +644,16 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < NS / 16; ++j)
 #pragma unroll
                     for (int e = 2; e >= 0; --e)
-                        mma_f16(tmem + kColY, k_major(bt, j), mn_major(parts + e * kBlock, j), kIdY, !(j == 0 && e == 2));
+                        mma_f16(tmem + kColY, k_major(bt, j), mn_major(parts + e * L::kPart, j), kIdY, !(j == 0 && e == 2));
                 mma_commit(x.bar(kZ));
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int e = 1; e >= 0; --e)
-                        mma_f16_ts(tmem + kColDb, tmem + kColSx + 8 * j, k_major(parts + e * kBlock, j), kIdQ, 1);
+                        mma_f16_ts(tmem + kColDb, tmem + kColSx + 8 * j, k_major(parts + e * L::kPart, j), kIdS, 1);
                 mma_commit(x.bar(kEnd));
             }
             __syncwarp();
@@ -802,24 +817,34 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
 }  // namespace tc
 }  // namespace scan
 
-cudaError_t launch_scan_tc_bwd(const ScanParams &p, const BwdWork &w, cudaStream_t s) {
-    using namespace scan::tc;
+namespace scan {
+namespace tc {
+
+template <int NS>
+cudaError_t bwd_launch(const ScanParams &p, const BwdWork &w, cudaStream_t s) {
     const int64_t ctas = w.cells * p.G * w.splits;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     BwdMaps maps;
     memset(&maps, 0, sizeof(maps));
-    const int64_t hp = static_cast<int64_t>(p.H) * p.P, gn = static_cast<int64_t>(p.G) * N, all = w.cells * p.H * N;
-    constexpr auto f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-    if (p.rows > 0 && (!encode(&maps.states, f32, 4, w.states, p.P, all, p.P, N) ||
-                       !encode(&maps.grads, f32, 4, w.grads, p.P, all, p.P, N) ||
+    const int64_t hp = static_cast<int64_t>(p.H) * p.P, gn = static_cast<int64_t>(p.G) * NS, all = w.cells * p.H * NS;
+    constexpr auto type = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    if (p.rows > 0 && (!encode(&maps.states, type, 4, w.states, p.P, all, p.P, NS) ||
+                       !encode(&maps.grads, type, 4, w.grads, p.P, all, p.P, NS) ||
                        !encode(&maps.x, p.x, hp, p.rows, p.x_stride, TT) ||
                        !encode(&maps.dy, p.dout, hp, p.rows, p.dout_stride, TT) ||
                        !encode(&maps.b, p.B, gn, p.rows, p.b_stride, TT) || !encode(&maps.c, p.C, gn, p.rows, p.c_stride, TT)))
         return cudaErrorInvalidValue;
-    cudaError_t err = scan::allow_smem(scan_tc_bwd_kernel, BwdSmem::kBytes);
+    cudaError_t err = allow_smem(scan_tc_bwd_kernel<NS>, BwdSmem<NS>::kBytes);
     if (err != cudaSuccess) return err;
-    scan_tc_bwd_kernel<<<static_cast<unsigned>(ctas), NT, BwdSmem::kBytes, s>>>(p, w, maps);
+    scan_tc_bwd_kernel<NS><<<static_cast<unsigned>(ctas), NT, BwdSmem<NS>::kBytes, s>>>(p, w, maps);
     return cudaGetLastError();
+}
+
+}  // namespace tc
+}  // namespace scan
+
+cudaError_t launch_scan_tc_bwd(const ScanParams &p, const BwdWork &w, cudaStream_t s) {
+    return p.N == 128 ? scan::tc::bwd_launch<128>(p, w, s) : scan::tc::bwd_launch<64>(p, w, s);
 }
 
 cudaError_t read_and_clear_scan_tc_bwd_error(unsigned int *value) {
