@@ -310,25 +310,28 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p, int64_t s
 // C, columns dy and weights e^Gamma:  R_start = e^(Gamma_end) R_end + C^T Diag(e^Gamma) dy.
 // `local`: what each piece adds (leave[unit], and its decay leave_decay[unit, h]); pieces behind which
 // nothing follows need none. `states`: the state at every tile's entry (reverse: exit).
-template <int N, int S, bool kReverse>
-__global__ void __launch_bounds__(NT, 3) scan_state_kernel(ScanParams p, int64_t seg, const float *entering, float *leave,
-                                                           float *leave_decay, float *states) {
+template <int S>
+__global__ void __launch_bounds__(NT, 3) scan_state_kernel(ScanParams p, int64_t seg, ScanStateRun run0, ScanStateRun run1) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr int MT = N / 64, ROWB = N * 2, kR = T * N * 2, kX = T * PC * 2, kStage = kR + kX;
+    constexpr int N = 64, MT = N / 64, ROWB = N * 2, kR = T * N * 2, kX = T * PC * 2, kStage = kR + kX;
     Gates *gates = reinterpret_cast<Gates *>(smem + 2 * kStage);
     const uint32_t base = smem_addr(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slices = p.P / PC, hs = static_cast<int>(blockIdx.x % (p.H * slices));
     const int h = hs / slices, col = (hs % slices) * PC;
     const int64_t unit = blockIdx.x / (p.H * slices);
-    if (blockIdx.x == 0) check_offsets(p.seqs, &g_scan_error);
+    const bool rev = blockIdx.y == 1;
+    const float *entering = rev ? run1.entering : run0.entering;
+    float *leave = rev ? run1.leave : run0.leave, *leave_decay = rev ? run1.leave_decay : run0.leave_decay;
+    float *states = rev ? run1.states : run0.states;
+    if (blockIdx.x == 0 && !rev) check_offsets(p.seqs, &g_scan_error);
     const Piece u = find_piece(p.seqs, unit, seg);
-    const bool head = kReverse ? u.last : u.first, tail = kReverse ? u.first : u.last;
+    const bool head = rev ? u.last : u.first, tail = rev ? u.first : u.last;
     if (u.none || (leave && tail)) return;
     const int n0 = warp * (N / 4);
     const int64_t grp = h / (p.H / p.G);
-    const uint16_t *cols = kReverse ? p.dout : p.x, *rows = kReverse ? p.C : p.B;
-    const int64_t cstr = kReverse ? p.dout_stride : p.x_stride, rstr = kReverse ? p.c_stride : p.b_stride;
+    const uint16_t *cols = rev ? p.dout : p.x, *rows = rev ? p.C : p.B;
+    const int64_t cstr = rev ? p.dout_stride : p.x_stride, rstr = rev ? p.c_stride : p.b_stride;
     cols += static_cast<int64_t>(h) * p.P + col;
     rows += grp * N;
     const float A = p.A[h];
@@ -337,11 +340,11 @@ __global__ void __launch_bounds__(NT, 3) scan_state_kernel(ScanParams p, int64_t
     if (entering)
         read_state<MT>(acc, entering, (unit * p.H + h) * sn + col, true, p.P, n0);
     else if (head && !leave)
-        read_state<MT>(acc, kReverse ? static_cast<const void *>(p.dhT) : p.h0, at_seq, kReverse || p.h0_fp32, p.P, n0);
+        read_state<MT>(acc, rev ? static_cast<const void *>(p.dhT) : p.h0, at_seq, rev || p.h0_fp32, p.P, n0);
     else
         read_state<MT>(acc, nullptr, 0, true, p.P, n0);
     const int64_t lo = u.a / T, n_tiles = u.b > u.a ? (u.b + T - 1) / T - lo : 0;
-    auto cell = [&](int64_t k) { return kReverse ? lo + n_tiles - 1 - k : lo + k; };
+    auto cell = [&](int64_t k) { return rev ? lo + n_tiles - 1 - k : lo + k; };
     auto fetch = [&](int64_t c, int stage) {
         const int64_t s = tile_start(u, c);
         const int cnt = tile_count(u, c);
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(NT, 3) scan_state_kernel(ScanParams p, int64_t
         }
         // of the two tiles of a cell the one that the direction enters first
         const int64_t c = cell(k);
-        if (states && ((c & 1) == (kReverse ? 1 : 0) || (head && k == 0)))
+        if (states && ((c & 1) == (rev ? 1 : 0) || (head && k == 0)))
             write_state<MT>(acc, states, ((u.i + c / 2) * p.H + h) * sn + col, true, p.P, n0);
         const Gates &g = gates[k & 1];
         const uint32_t rt = base + stage * kStage;
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(NT, 3) scan_state_kernel(ScanParams p, int64_t
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int c = 0; c < 8; ++c) share[m][c][0] = share[m][c][1] = share[m][c][2] = share[m][c][3] = 0.f;
-        add_outer<ROWB, MT, S>(share, rt, rt + kR, kReverse ? g.from : g.weight, n0);
+        add_outer<ROWB, MT, S>(share, rt, rt + kR, rev ? g.from : g.weight, n0);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -393,7 +396,7 @@ __global__ void __launch_bounds__(NT, 3) scan_state_kernel(ScanParams p, int64_t
     if (leave) {
         write_state<MT>(acc, leave, (unit * p.H + h) * sn + col, true, p.P, n0);
         if (gate_warp && lane == 0 && col == 0) leave_decay[unit * p.H + h] = ex2(decay);
-    } else if (kReverse && tail && p.dh0) {
+    } else if (rev && tail && p.dh0) {
         write_state<MT>(acc, p.dh0, at_seq, true, p.P, n0);
     }
 }
@@ -476,7 +479,7 @@ int64_t fwd_piece_tokens(int64_t rows, int64_t n, bool packed, int32_t H, int32_
 int64_t state_piece_tokens(int64_t rows, int64_t n, bool packed, int32_t H, int32_t P, int32_t N) {
     const int64_t columns = static_cast<int64_t>(H) * (P / PC);
     return N == 128 ? piece_tokens(rows, n, false, (columns + 1) / 2 * 2, 148, T)
-                    : piece_tokens(rows, n, packed, columns, 2 * 148, T);
+                    : piece_tokens(rows, n, packed, 2 * columns, 3 * 148, T);
 }
 
 int64_t piece_count(int64_t rows, int64_t n, int64_t seg) { return seg ? rows / seg + n : n; }
@@ -486,15 +489,23 @@ size_t piece_bytes(int64_t rows, int64_t n, int64_t seg, int32_t H, int32_t P, i
     return static_cast<size_t>(piece_count(rows, n, seg)) * H * (static_cast<size_t>(N) * P + 4) * sizeof(float);
 }
 
-template <int N, int S, bool kReverse>
-cudaError_t state_launch(const ScanParams &p, int64_t seg, int64_t units, const ScanStateRun &r, cudaStream_t s) {
-    constexpr int bytes = 2 * (T * N * 2 + T * PC * 2) + 2 * static_cast<int>(sizeof(Gates));
-    auto *k = scan_state_kernel<N, S, kReverse>;
-    cudaError_t err = allow_smem(k, bytes);
+template <int S>
+cudaError_t state_launch(const ScanParams &p, int directions, int64_t seg, int64_t units, const ScanStateRun &fwd,
+                         const ScanStateRun &rev, cudaStream_t s) {
+    constexpr int bytes = 2 * (T * 64 * 2 + T * PC * 2) + 2 * static_cast<int>(sizeof(Gates));
+    cudaError_t err = allow_smem(scan_state_kernel<S>, bytes);
     if (err != cudaSuccess) return err;
-    k<<<static_cast<unsigned>(units * p.H * (p.P / PC)), NT, bytes, s>>>(p, seg, r.entering, r.leave, r.leave_decay,
-                                                                          r.states);
+    const dim3 grid(static_cast<unsigned>(units * p.H * (p.P / PC)), static_cast<unsigned>(directions));
+    scan_state_kernel<S><<<grid, NT, bytes, s>>>(p, seg, fwd, rev);
     return cudaGetLastError();
+}
+
+// The state alone (see launch_scan_tc_state)
+cudaError_t launch_state(const ScanParams &p, int parts, int directions, int64_t seg, int64_t units, const ScanStateRun &fwd,
+                         const ScanStateRun &rev, cudaStream_t s) {
+    if (p.N == 128) return launch_scan_tc_state(p, parts, directions, seg, units, fwd, rev, s);
+    return parts == 3 ? state_launch<3>(p, directions, seg, units, fwd, rev, s)
+                      : state_launch<2>(p, directions, seg, units, fwd, rev, s);
 }
 
 template <bool kReverse>
@@ -517,39 +528,30 @@ size_t scan_states_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P
     return 2 * scan::piece_bytes(rows, n, scan::state_piece_tokens(rows, n, true, H, P, N), H, P, N);
 }
 
-// the warp-level kernels, each piece's own contribution and the main run
 template <int N>
-cudaError_t scan_fwd_warps(const ScanParams &p, int64_t seg, int64_t units, float *ws, float *decay, bool local, cudaStream_t s) {
+cudaError_t scan_fwd_launch(const ScanParams &p, int64_t seg, int64_t units, const float *entering, cudaStream_t s) {
     using namespace scan;
-    const bool exact = p.hT && p.hT_fp32;
-    if (local)
-        return exact ? state_launch<N, 3, false>(p, seg, units, {nullptr, ws, decay, nullptr}, s)
-                     : state_launch<N, 2, false>(p, seg, units, {nullptr, ws, decay, nullptr}, s);
-    auto *k = exact ? scan_fwd_kernel<N, 3> : scan_fwd_kernel<N, 2>;
+    auto *k = p.hT && p.hT_fp32 ? scan_fwd_kernel<N, 3> : scan_fwd_kernel<N, 2>;
     const cudaError_t err = allow_smem(k, FwdSmem<N>::kBytes);
     if (err != cudaSuccess) return err;
-    k<<<static_cast<unsigned>(units * p.H * (p.P / PC)), NT, FwdSmem<N>::kBytes, s>>>(p, seg, ws);
+    k<<<static_cast<unsigned>(units * p.H * (p.P / PC)), NT, FwdSmem<N>::kBytes, s>>>(p, seg, entering);
     return cudaGetLastError();
 }
 
 cudaError_t launch_scan_fwd(const ScanParams &p, cudaStream_t s) {
     using namespace scan;
-    const bool tc = takes_tc(p.rows, p.seqs.n, p.N);
     const int64_t cut = fwd_piece_tokens(p.rows, p.seqs.n, p.seqs.cu != nullptr, p.H, p.P, p.N);
     const int64_t seg = cut ? cut : kWhole, units = piece_count(p.rows, p.seqs.n, cut);
     if (units * p.H * (p.P / PC) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    float *ws = p.ws, *decay = ws ? ws + units * p.H * p.N * p.P : nullptr;
-    auto warps = [&](bool local, float *states) {
-        return by_state(p.N, [&](auto n) { return scan_fwd_warps<decltype(n)::value>(p, seg, units, states, decay, local, s); });
-    };
     if (cut) {
-        cudaError_t err = tc ? launch_scan_tc_state(p, p.hT && p.hT_fp32 ? 3 : 2, 1, seg, units, {nullptr, ws, decay, nullptr}, {}, s)
-                             : warps(true, ws);
-        if (err == cudaSuccess) err = join_launch<false>(p, seg, ws, decay, s);
+        float *decay = p.ws + units * p.H * p.N * p.P;
+        cudaError_t err = launch_state(p, p.hT && p.hT_fp32 ? 3 : 2, 1, seg, units, {nullptr, p.ws, decay, nullptr}, {}, s);
+        if (err == cudaSuccess) err = join_launch<false>(p, seg, p.ws, decay, s);
         if (err != cudaSuccess) return err;
     }
-    float *entering = cut ? ws : nullptr;
-    return tc ? launch_scan_tc(p, seg, units, entering, s) : warps(false, entering);
+    const float *entering = cut ? p.ws : nullptr;
+    if (takes_tc(p.rows, p.seqs.n, p.N)) return launch_scan_tc(p, seg, units, entering, s);
+    return by_state(p.N, [&](auto n) { return scan_fwd_launch<decltype(n)::value>(p, seg, units, entering, s); });
 }
 
 cudaError_t launch_scan_states(const ScanParams &p, float *states, float *grads, float *ws, cudaStream_t s) {
@@ -563,9 +565,7 @@ cudaError_t launch_scan_states(const ScanParams &p, float *states, float *grads,
     auto run = [&](bool local) {
         const ScanStateRun f = local ? ScanStateRun{nullptr, wf, df, nullptr} : ScanStateRun{cut ? wf : nullptr, nullptr, nullptr, states};
         const ScanStateRun r = local ? ScanStateRun{nullptr, wr, dr, nullptr} : ScanStateRun{cut ? wr : nullptr, nullptr, nullptr, grads};
-        if (p.N == 128) return launch_scan_tc_state(p, 3, 2, seg, units, f, r, s);
-        cudaError_t err = state_launch<64, 3, false>(p, seg, units, f, s);
-        return err == cudaSuccess ? state_launch<64, 3, true>(p, seg, units, r, s) : err;
+        return launch_state(p, 3, 2, seg, units, f, r, s);
     };
     cudaError_t err = cudaSuccess;
     if (cut) {
