@@ -431,8 +431,8 @@ kda_status kda_qk_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_
  *            fp32 (the same when both are given) or NULL, as in kda_fwd. final_state may be
  *            initial_state (in place).
  * head_dim and state_dim are 64 or 128; num_heads a multiple of num_groups. States are carried in fp32. The
- * tokens are taken 64 at a time: a NaN or infinity in x, B or C can reach outputs up to 63 tokens before
- * its own, of the same sequence and head.
+ * tokens are taken up to 128 at a time: a NaN or infinity in x, B or C can reach outputs up to 127 tokens before
+ * its own, of the same sequence and group.
  *
  * Long sequences of few heads are cut into pieces that run at once (as in kda_fwd_segmented, but a
  * scalar decay needs no second run for a transition matrix); their states go to `workspace`,
@@ -455,7 +455,8 @@ kda_status kda_scan_fwd(const void *x, int64_t x_stride, const float *dt, const 
  * dfinal_state fp32 [num_seqs_eff, num_heads, state_dim, head_dim] or NULL. Written: dx bf16, dB, dC bf16
  * (summed over a group's heads; all three rows strided), ddt fp32 [batch, seq_len, num_heads], dA fp32
  * [num_heads], and, each or NULL, dD, ddt_bias fp32 [num_heads], dinitial_state fp32 (shape of the states).
- * workspace: kda_scan_bwd_workspace(...) bytes (two fp32 states per 64 tokens and head are its bulk).
+ * workspace: kda_scan_bwd_workspace(...) bytes (two fp32 states per 128 tokens and head are its bulk). A NaN or
+ * infinity in an input can reach the gradients of the 127 tokens to either side of those that depend on it.
  */
 size_t kda_scan_bwd_workspace(int64_t total_tokens, int32_t num_seqs, int32_t num_heads, int32_t num_groups,
                               int32_t head_dim, int32_t state_dim);
