@@ -4,7 +4,7 @@
 //
 //   pre_t = bias + sum_{k < W} w_k e_{t-W+1+k},   out_t = pre_t sigmoid(pre_t)  (or pre_t)
 //
-// All three kernels are bound by HBM: 2 W operations and one sigmoid per element against 4 bytes
+// All kernels are bound by HBM: 2 W operations and one sigmoid per element against 4 bytes
 // (bf16, forward). A thread owns 4 channels (8 for single tokens) and walks a run of tokens with the
 // last W - 1 inputs in registers, so x is read once but for the W - 1 rows before each run, which
 // the neighbouring warp has just read. The loads of the next tokens are issued together, before any
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(32 * FW) conv_fwd_kernel(ConvParams p, int run
 // ---------------------------------------------------------------- single tokens
 
 // A thread takes kRows requests of its 8 channels, with the taps read once: at 256 x 12288 bf16 the taps alone, read
-// for every request, were as many bytes again as everything else (20 us instead of the time in the table).
+// for every request, were as many bytes again as everything else (20 us; with four requests 9.0, 5.6 TB/s).
 template <class T, int W, bool kSilu, int kRows>
 __global__ void __launch_bounds__(128) conv_decode_kernel(ConvDecodeParams p) {
     const int ch = (blockIdx.x * 128 + threadIdx.x) * V;

@@ -15,7 +15,8 @@
 // Each pair (s, u) is counted in dlog a as it stands, never as a difference of sums over the whole
 // sequence, so a long sequence loses no digits. C B^T and Q have operands that are exact in bf16, and M . Q
 // is taken elementwise in fp32; the products with S_0 and R from which fp32 results follow take them as three
-// bf16 parts (24 bits). M and K are rounded to bf16 once, for results in bf16.
+// bf16 parts (24 bits). M, K and the rows e^Gamma dy, d e^(Gamma_end - Gamma) x that multiply S_0^T, R^T (in two parts, 16
+// bits) are rounded to bf16 once, for results in bf16.
 //
 // The states S_0 and gradients R of every tile come from two sweeps (launch_scan_states), fp32 in the
 // workspace: that is its bulk. The gradient kernel (kda_scan_tc_bwd.cu) then takes all tiles at once. One CTA has one

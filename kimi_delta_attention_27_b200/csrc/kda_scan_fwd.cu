@@ -19,6 +19,8 @@
 // columns (columns do not mix). Warp w has 16 rows of y and N / 4 rows of the state, whose accumulators stay
 // in its registers from tile to tile; L . (C B^T) never leaves registers either: the accumulator layout of
 // C B^T is the operand layout of the product with x. The next tile's x, B, C arrive by cp.async meanwhile.
+// It is this kernel for a state size of 64, and for short sequences at 128; others take kda_scan_tc.cu. Bound by the
+// latency of a tile's chain: one sequence of 200 tokens x 32 heads, four tiles, 19 us.
 //
 // Few long sequences make few CTAs. Then sequences are cut into pieces of whole tiles: a first launch
 // finds each piece's own contribution to the state it leaves (from zero), scan_join_kernel adds those up
@@ -308,8 +310,9 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p, int64_t s
 // The state alone. Forwards: from zero (or `entering`) over the piece's tiles with rows B, columns x and
 // weights d e^(Gamma_end - Gamma). Reverse: the gradient of the state, over the tiles backwards, with rows
 // C, columns dy and weights e^Gamma:  R_start = e^(Gamma_end) R_end + C^T Diag(e^Gamma) dy.
-// `local`: what each piece adds (leave[unit], and its decay leave_decay[unit, h]); pieces behind which
-// nothing follows need none. `states`: the state at every tile's entry (reverse: exit).
+// `leave`: what each piece adds (leave[unit], and its decay leave_decay[unit, h]); pieces behind which
+// nothing follows need none. `states`: the state at every cell's entry (reverse: exit). State size 64; at 128 it is
+// kda_scan_tc_state.cu. (Both directions of 5 packed sequences, 5001 tokens x 32 heads x 128: 77 us, 117 in two launches.)
 template <int S>
 __global__ void __launch_bounds__(NT, 3) scan_state_kernel(ScanParams p, int64_t seg, ScanStateRun run0, ScanStateRun run1) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(256) scan_join_kernel(ScanParams p, int64_t se
 // are cut where equal ones fill less than half of the slots, and packed ones, of which the longest is taken to be twice
 // the mean, fewer than all. (4096 tokens x 64 heads x 64: 2 sequences, 64 CTAs, 176 us whole, 181 cut; 3 sequences 181
 // and 231. One of 65536 tokens x 32 heads x 128, 32 CTAs: 2.62 ms whole, 0.86 cut. The states of 5 packed ones for the
-// gradients, 320 CTAs of 296: 123 us whole, 163 cut.)
+// gradients, one direction's 320 CTAs of 296: 61 us whole, 81 cut.)
 int64_t piece_tokens(int64_t rows, int64_t n, bool packed, int64_t ctas, int slots, int tile) {
     if (n == 0 || (packed ? 1 : 2) * n * ctas >= slots) return 0;
     const int64_t want = 2 * slots;
@@ -464,14 +467,16 @@ int64_t piece_tokens(int64_t rows, int64_t n, bool packed, int64_t ctas, int slo
     if (seg < 256) seg = 256;
     return seg >= rows ? 0 : seg;
 }
-// State size 128: sequences of more than 256 tokens on average take the tcgen05 kernels, one CTA per SM with two runs
-// of 64 columns. Their first tile takes some 18 us, where the warp-level kernel's takes 8 (one sequence of 200 tokens x
-// 32 heads: 24 against 20 us; 16 of 200 x 64: 110 against 105; 16 of 512 x 64: 141 against 192).
-bool takes_tc(int64_t rows, int64_t n, int32_t N) { return N == 128 && rows > 256 * n; }
+// State size 128: the tcgen05 kernel takes sequences of more than 160 tokens on average, or, where the CTAs of the
+// warp-level one fit the SMs at once, of more than 256: a first tile takes it some 3 us longer. (16 sequences x 64 heads:
+// of 140 tokens 63 us against 61, of 180 68 and 71, of 256 60 and 85, of 512 100 and 166; one of 200 x 32: 22 and 19.)
+bool takes_tc(int64_t rows, int64_t n, int64_t columns, int32_t N) {
+    return N == 128 && rows > (n * columns > 2 * 148 ? 160 : 256) * n;
+}
 int64_t fwd_piece_tokens(int64_t rows, int64_t n, bool packed, int32_t H, int32_t P, int32_t N) {
     const int64_t columns = static_cast<int64_t>(H) * (P / PC);
-    return takes_tc(rows, n, N) ? piece_tokens(rows, n, packed, (columns + 1) / 2, 148, kScanTcTile)
-                                : piece_tokens(rows, n, packed, columns, 2 * 148, T);
+    return takes_tc(rows, n, columns, N) ? piece_tokens(rows, n, packed, (columns + 1) / 2, 148, kScanTcTile)
+                                         : piece_tokens(rows, n, packed, columns, 2 * 148, T);
 }
 // The backward's runs of the state, both directions at once; at a state size of 128 their tiles take so little that
 // packed sequences, too, are cut only below half of the slots (the gradients of 2 packed ones, 13493 tokens x 64 heads:
@@ -550,7 +555,7 @@ cudaError_t launch_scan_fwd(const ScanParams &p, cudaStream_t s) {
         if (err != cudaSuccess) return err;
     }
     const float *entering = cut ? p.ws : nullptr;
-    if (takes_tc(p.rows, p.seqs.n, p.N)) return launch_scan_tc(p, seg, units, entering, s);
+    if (takes_tc(p.rows, p.seqs.n, static_cast<int64_t>(p.H) * (p.P / PC), p.N)) return launch_scan_tc(p, seg, units, entering, s);
     return by_state(p.N, [&](auto n) { return scan_fwd_launch<decltype(n)::value>(p, seg, units, entering, s); });
 }
 

@@ -10,11 +10,13 @@
 //   U  = B^T (d e^(Gamma_end - Gamma) x)    128 x 64,  K 128     the second operand in 2 or 3 bf16 parts
 //   S  = e^(Gamma_end) S_0 + U                                   fp32, in the registers of 256 threads
 //
-// What bounds it: the products take some 600 cycles per tile and head at the tensor cores' rate, HBM some
-// 1500 (34 KB), the work on elements (L . G, the parts of x, scaling and rounding) some 6000 warp
-// instructions, 1500 cycles of the four schedulers. So the element work is what has to be kept busy: eight
-// warps take each of two heads (of the same group, so that they share C, B and G), a thread having half of a
-// row; one thread issues the products; two warps run ahead with the gates and the loads of x. A tile's outputs
+// What bounds it: with two heads side by side a tile's products read 0.7 MB of operands from shared memory, 5500 cycles
+// at 128 bytes a cycle; the elements' own traffic with shared memory and TMEM is 4100 more; HBM takes some 3000
+// cycles (68 KB), the work on elements (L . G, the parts of x, scaling and rounding) some 3900 of the four schedulers.
+// So eight warps take each of the two heads (of the same group, so that they share C, B and G), a thread having half of
+// a row; one thread issues the products; two warps run ahead with the gates and the loads of x. (65536 tokens x 32 heads
+// x 128, pieces of 1024: 573 us, 9800 cycles for two heads' tile, tensor cores 36 % and the L1 pipes 53 % busy; with
+// tiles of 64 tokens on warp-level products 1.2 ms.) A tile's outputs
 // are finished in the next tile, between the two halves of its parts, so that no product is waited for
 // while there is work, and nothing but Y's first product waits for the state.
 //
@@ -298,7 +300,8 @@ __global__ void __launch_bounds__(NT, 1)
                 uint16_t *out = p.out + start_of(i) * p.out_stride + static_cast<int64_t>(v) * PC + chunk * 8;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int row = wq * 32 + j * 8 + (lane >> 2);
+                    // rows four apart side by side: their chunks lie in different banks
+                    const int row = wq * 32 + j * 8 + (lane & 4) + (lane >> 3);
                     if (row < cnt) *reinterpret_cast<uint4 *>(out + row * p.out_stride) = lds(xt + sw128(row, chunk));
                 }
                 fence_proxy_async_smem();   // x's next load comes after these reads and writes

@@ -13,6 +13,8 @@
 // group side by side (one product with N = 128 reads the rows once for both: 64 cycles per K step and
 // part instead of 2 x 48), 768 cycles per tile with three parts. Eight warps per head form the parts of the
 // next tile while this one's product runs, then add U to the state; four warps run ahead with gates and loads.
+// (2 x 4096 tokens x 64 heads x 64, both directions, states stored every 128 tokens: 123 us, 3400 cycles for two heads'
+// tile, the L1 pipes 62 % busy.)
 //
 // Every wait is bounded; one that runs out raises kErrTimeout and winds the CTA down.
 #include <cuda_bf16.h>
