@@ -511,6 +511,12 @@ def _stream_of(dev, stream):
     return handle, _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
+def _like(t):
+    """A contiguous tensor of t's shape, type and device (half the time of torch.empty with all three)."""
+    import torch
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -578,7 +584,7 @@ def kda_conv_fwd(x, weight, bias=None, silu: bool = True, cu_seqlens=None, initi
     handle, ctx = _stream_of(dev, stream)
     with ctx:
         if out is None:
-            out = torch.empty((B, T, C), dtype=x.dtype, device=dev)
+            out = _like(x)
         if final_state is None and want_final_state:
             final_state = torch.empty((N, W - 1, C), dtype=x.dtype, device=dev)
         _raise(lib, lib.kda_conv_fwd(_addr(x), _dtype_code(x), xs, _addr(weight), _addr(bias),
@@ -609,7 +615,7 @@ def kda_conv_bwd(x, weight, dout, bias=None, silu: bool = True, cu_seqlens=None,
     handle, ctx = _stream_of(dev, stream)
     with ctx:
         if dx is None:
-            dx = torch.empty((B, T, C), dtype=x.dtype, device=dev)
+            dx = _like(x)
         dweight = torch.empty((C, W), dtype=torch.float32, device=dev)
         dbias = torch.empty(C, dtype=torch.float32, device=dev) if bias is not None else None
         dinit = torch.empty((N, W - 1, C), dtype=x.dtype, device=dev) if want_dinitial_state else None
@@ -639,7 +645,7 @@ def kda_conv_decode(x, weight, state_in=None, state_out=None, bias=None, silu: b
     handle, ctx = _stream_of(dev, stream)
     with ctx:
         if out is None:
-            out = torch.empty((B, C), dtype=x.dtype, device=dev)
+            out = _like(x)
         _raise(lib, lib.kda_conv_decode(_addr(x), _dtype_code(x), xs, _addr(weight), _addr(bias),
                                         KDA_FLAG_CONV_SILU if silu else 0, B, C, W, _addr(state_in), _addr(state_out),
                                         _addr(out), os, handle))
@@ -691,9 +697,9 @@ def kda_qk_fwd(q, k=None, norm: str = "l2", q_weight=None, k_weight=None, eps: f
     handle, ctx = _stream_of(dev, stream)
     with ctx:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = _like(q)
         if k_out is None and k is not None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+            k_out = _like(k)
         _raise(lib, lib.kda_qk_fwd(_addr(q), qs, _addr(k), ks, B * T, Hq, Hk, D, NORM_KINDS[norm], float(eps),
                                    _addr(q_weight), _addr(k_weight), _addr(positions), _addr(inv_freq), rot,
                                    int(bool(interleaved)), float(factor),
@@ -722,8 +728,8 @@ def kda_qk_bwd(q, k, dq_out, dk_out, norm: str = "l2", q_weight=None, k_weight=N
     lib = load_library()
     handle, ctx = _stream_of(dev, stream)
     with ctx:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        dk = torch.empty(k.shape, dtype=k.dtype, device=dev) if k is not None else None
+        dq = _like(q)
+        dk = _like(k) if k is not None else None
         dqw = torch.empty(D, dtype=torch.float32, device=dev) if q_weight is not None else None
         dkw = torch.empty(D, dtype=torch.float32, device=dev) if k_weight is not None else None
         need = 0
@@ -781,7 +787,7 @@ def kda_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus: bool = False
     handle, ctx = _stream_of(dev, stream)
     with ctx:
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            out = _like(x)
         if final_state is None and final_state_dtype is not None:
             final_state = torch.empty((n, H, N, P), dtype=final_state_dtype, device=dev)
         ws = _scratch(int(lib.kda_scan_fwd_workspace(Bn * T, n, H, P, N)), workspace, dev)
@@ -822,10 +828,10 @@ def kda_scan_bwd(x, dt, A, B, C, dout, D=None, dt_bias=None, dt_softplus: bool =
     with ctx:
         empty = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
         f32 = torch.float32
-        dx = empty(x.shape, x.dtype) if dx is None else dx
-        dB = empty(B.shape, B.dtype) if dB is None else dB
-        dC = empty(C.shape, C.dtype) if dC is None else dC
-        out = dict(dx=dx, dB=dB, dC=dC, ddt=empty(dt.shape, f32), dA=empty((H,), f32),
+        dx = _like(x) if dx is None else dx
+        dB = _like(B) if dB is None else dB
+        dC = _like(C) if dC is None else dC
+        out = dict(dx=dx, dB=dB, dC=dC, ddt=_like(dt), dA=_like(A),
                    dD=empty((H,), f32) if D is not None else None,
                    ddt_bias=empty((H,), f32) if dt_bias is not None else None,
                    dh0=empty((n, H, N, P), f32) if want_dinitial_state else None)
@@ -874,7 +880,7 @@ def kda_scan_decode(x, dt, A, B, C, state_in=None, state_out=None, D=None, dt_bi
         if state_out is None and state_dtype is not None:
             state_out = torch.empty((n, H, N, P), dtype=state_dtype, device=dev)
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            out = _like(x)
         code = _dtype_code(state_in if state_in is not None else state_out)
         _raise(lib, lib.kda_scan_decode(_addr(x), xs, _addr(dt), _addr(A), _addr(B), bs, _addr(C), cs, _addr(D),
                                         _addr(dt_bias), KDA_FLAG_SCAN_SOFTPLUS if dt_softplus else 0, n, H, G, P, N,
