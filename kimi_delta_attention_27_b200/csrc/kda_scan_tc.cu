@@ -10,15 +10,14 @@
 //   U  = B^T (d e^(Gamma_end - Gamma) x)    128 x 64,  K 128     the second operand in 2 or 3 bf16 parts
 //   S  = e^(Gamma_end) S_0 + U                                   fp32, in the registers of 256 threads
 //
-// What bounds it: with two heads side by side a tile's products read 0.7 MB of operands from shared memory, 5500 cycles
-// at 128 bytes a cycle; the elements' own traffic with shared memory and TMEM is 4100 more; HBM takes some 3000
-// cycles (68 KB), the work on elements (L . G, the parts of x, scaling and rounding) some 3900 of the four schedulers.
-// So eight warps take each of the two heads (of the same group, so that they share C, B and G), a thread having half of
-// a row; one thread issues the products; two warps run ahead with the gates and the loads of x. (65536 tokens x 32 heads
-// x 128, pieces of 1024: 573 us, 9800 cycles for two heads' tile, tensor cores 36 % and the L1 pipes 53 % busy; with
-// tiles of 64 tokens on warp-level products 1.2 ms.) A tile's outputs
-// are finished in the next tile, between the two halves of its parts, so that no product is waited for
-// while there is work, and nothing but Y's first product waits for the state.
+// What bounds it: for two heads' tile the products take 2600 cycles, the elements' traffic with shared memory and TMEM
+// 4100, their instructions (L . G, the parts of x, scaling and rounding) 3900 of each scheduler, HBM 3000 (68 KB); what is
+// left is the chain from one tile's state to the next. So eight warps take each of two heads (of the same group, so that
+// they share C, B and G, and one product with N = 128 reads C or B^T once for both), a thread having half of a row; one
+// thread issues the products; two warps run ahead with the gates and the loads of x. A tile's outputs are finished in the
+// next tile, between the two halves of its parts, so that no product is waited for while there is work, and nothing but
+// Y1 waits for the state. (65536 tokens x 32 heads x 128 in pieces: 565 us, 9650 cycles for two heads' tile; with Y1 and U
+// by head 584; warp-level products with tiles of 64 tokens 1.2 ms.)
 //
 // L . G is formed without one exponential per element: with a_b = Gamma at the end of a block of 32 columns,
 // L_ts = e^(Gamma_t - a_b) e^(a_b - Gamma_s), a factor per row and one per column, both at most 1 for the
@@ -57,19 +56,18 @@ struct Smem {
     static constexpr uint32_t kC = 0, kB = 2 * kBlock, kX = 4 * kBlock;    // x: [head][stage]
     static constexpr uint32_t kState = kX + 4 * kBlock;                    // [head]: the state in bf16
     static constexpr uint32_t kPart = 64 * 128;                            // 64 tokens of one part
-    static constexpr uint32_t kParts = kState + 2 * kBlock;                // [head][S]
+    static constexpr uint32_t kParts = kState + 2 * kBlock;                // [S][head]
     static constexpr uint32_t kGates = kParts + 2 * S * kPart;             // [head][stage]
     static constexpr uint32_t kBars = kGates + 4 * sizeof(TcGates);
     static constexpr uint32_t kBytes = kBars + 512;
     static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
 };
 
-// TMEM columns: G, then per head U, Y1 and Y2. M (L . G d in bf16 pairs) takes U's place once that has been read.
-constexpr uint32_t kColG = 0, kColU = 128, kColY1 = 192, kColY2 = 256, kColHead = 192, kCols = 512;
+// TMEM columns: G, then both heads' U, Y1 and Y2. M (L . G d in bf16 pairs) takes U's place once that has been read.
+constexpr uint32_t kColG = 0, kColU = 128, kColY1 = 256, kColY2 = 384, kColHead = 64, kCols = 512;
 
 constexpr uint32_t kIdG = idesc_f16(128, 128, 1, 0, 0);   // C and B, both K-major
-constexpr uint32_t kIdY = idesc_f16(128, 64, 1, 0, 1);    // C or M K-major, state copy or x MN-major
-constexpr uint32_t kIdU = idesc_f16(128, 64, 1, 1, 1);    // B^T and the parts of x, both MN-major
+constexpr uint32_t kIdY = idesc_f16(128, 64, 1, 0, 1);    // M K-major, x MN-major
 
 struct Maps {
     CUtensorMap x, b, c;
@@ -81,16 +79,16 @@ enum : int {
     kG = 2,             // G is there
     kXFull = 3,         // [head][stage] x
     kGates = 7,         // [head][stage] the gates
-    kPFree = 11,        // [head] the first half's product is done
-    kU = 13,            // [head] U is there
-    kY = 15,            // [head] Y1 and Y2 are there
-    kByHead = 17,       // from here on: the head's eight warps arrive
-    kXFree = 17,        // [head][stage] the tile's x and gates have been used
-    kS = 21,            // [head] the state's copy is written
-    kYFree = 23,        // [head] Y1 and Y2 have been read
-    kP0 = 25, kP1 = 27, // [head] the parts of the tile's first, second 64 tokens are written
-    kM = 29,            // [head] M is written
-    kBarCount = 31
+    kPFree = 11,        // the first half's product is done
+    kU = 12,            // U is there
+    kY = 13,            // [head] Y1 and Y2 are there
+    kByHead = 15,       // from here on: the head's eight warps arrive
+    kXFree = 15,        // [head][stage] the tile's x and gates have been used
+    kS = 19,            // [head] the state's copy is written
+    kYFree = 21,        // [head] Y1 and Y2 have been read
+    kP0 = 23, kP1 = 25, // [head] the parts of the tile's first, second 64 tokens are written
+    kM = 27,            // [head] M is written
+    kBarCount = 29
 };
 
 // the steps of a lane's tokens 4l .. 4l + 3 before bias and softplus (0 behind the tile)
@@ -194,7 +192,7 @@ __global__ void __launch_bounds__(NT, 1)
             const uint32_t tU = tmem + kColU + hd * kColHead + 32 * hf + lanes, tG = tmem + kColG + lanes;
             const uint32_t tY1 = tmem + kColY1 + hd * kColHead + 32 * hf + lanes;
             const uint32_t tY2 = tmem + kColY2 + hd * kColHead + 32 * hf + lanes;
-            uint8_t *st = smem + L::kState + hd * kBlock, *parts = smem + L::kParts + hd * S * L::kPart;
+            uint8_t *st = smem + L::kState + hd * kBlock, *parts = smem + L::kParts + hd * L::kPart;
             const int64_t sn = static_cast<int64_t>(N) * p.P;
             const float Dh = p.D ? p.D[h] : 0.f;
             float2 s[16];         // this thread's part of the state
@@ -254,7 +252,7 @@ __global__ void __launch_bounds__(NT, 1)
                     }
 #pragma unroll
                     for (int e = 0; e < S; ++e)
-                        sts(parts + e * L::kPart + sw128(t256 >> 2, chunk), make_uint4(o[e][0], o[e][1], o[e][2], o[e][3]));
+                        sts(parts + e * 2 * L::kPart + sw128(t256 >> 2, chunk), make_uint4(o[e][0], o[e][1], o[e][2], o[e][3]));
                 }
                 fence_proxy_async_smem();
                 x.arrive((half ? kP1 : kP0) + hd);
@@ -331,11 +329,11 @@ __global__ void __launch_bounds__(NT, 1)
                     ok = finish(i - 1);
                     if (!ok) break;
                 }
-                ok = x.wait(kPFree + hd, ph);
+                ok = x.wait(kPFree, ph);
                 if (!ok) break;
                 write_parts(1, xt, g, cnt);
                 // S = e^(Gamma_end) S + U
-                ok = x.wait(kU + hd, ph);
+                ok = x.wait(kU, ph);
                 if (!ok) break;
                 tc_fence_after();
                 {
@@ -426,6 +424,8 @@ __global__ void __launch_bounds__(NT, 1)
     } else if (warp == kIssuer) {
         // ---------------------------------------------------------------- loads of C and B, and the products
         const int bcol = grp * N;
+        const uint32_t id_y = idesc_f16(128, 64 * heads, 1, 0, 1);   // C K-major, the states' copies MN-major
+        const uint32_t id_u = idesc_f16(128, 64 * heads, 1, 1, 1);   // B^T and the parts of x, both MN-major
         auto load_bc = [&](int i) {
             if (!elect_one()) return;
             const int32_t row = static_cast<int32_t>(start_of(i));
@@ -456,52 +456,47 @@ __global__ void __launch_bounds__(NT, 1)
                 }
                 __syncwarp();
             }
-            auto product_u = [&](int hd, int half) {
+            // both heads side by side, so that C and B^T are read once for the two
+            auto product_u = [&](int half) {
                 if (elect_one()) {
-                    const uint32_t parts = base + L::kParts + hd * S * L::kPart;
+                    const uint32_t parts = base + L::kParts;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
                         for (int e = S - 1; e >= 0; --e)
-                            mma_f16(tmem + kColU + hd * kColHead,
-                                    smem_desc(bt + (half * 4 + k) * 2048, kBlock, 1024, kSwizzle128),
-                                    smem_desc(parts + e * L::kPart + k * 2048, kBlock, 1024, kSwizzle128), kIdU,
+                            mma_f16(tmem + kColU, smem_desc(bt + (half * 4 + k) * 2048, kBlock, 1024, kSwizzle128),
+                                    smem_desc(parts + e * 2 * L::kPart + k * 2048, L::kPart, 1024, kSwizzle128), id_u,
                                     !(half == 0 && k == 0 && e == S - 1));
-                    mma_commit(x.bar((half ? kU : kPFree) + hd));
+                    mma_commit(x.bar(half ? kU : kPFree));
                 }
                 __syncwarp();
             };
-            for (int hd = 0; hd < heads && ok; ++hd) {
-                // U takes the place of the last tile's M, which has been multiplied
-                ok = x.wait(kP0 + hd, ph) && (i == 0 || x.wait(kY + hd, (i - 1) & 1));
-                if (!ok) break;
-                tc_fence_after();
-                product_u(hd, 0);
-            }
-            for (int hd = 0; hd < heads && ok; ++hd) {
-                {
-                    ok = x.wait(kS + hd, ph) && (i == 0 || x.wait(kYFree + hd, (i - 1) & 1));
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
+            // U takes the place of the last tile's M, which has been multiplied
+            for (int hd = 0; hd < heads && ok; ++hd) ok = x.wait(kP0 + hd, ph) && (i == 0 || x.wait(kY + hd, (i - 1) & 1));
+            if (!ok) break;
+            __syncwarp();
+            tc_fence_after();
+            product_u(0);
+            for (int hd = 0; hd < heads && ok; ++hd) ok = x.wait(kS + hd, ph) && (i == 0 || x.wait(kYFree + hd, (i - 1) & 1));
+            if (!ok) break;
+            __syncwarp();
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_f16(tmem + kColY1 + hd * kColHead,
-                                    smem_desc(base + L::kC + (k >> 2) * kBlock + (k & 3) * 32, 16, 1024, kSwizzle128),
-                                    smem_desc(base + L::kState + hd * kBlock + k * 2048, kBlock, 1024, kSwizzle128), kIdY,
-                                    k > 0);
-                    }
-                    __syncwarp();
-                }
-                ok = x.wait(kP1 + hd, ph);
-                if (!ok) break;
-                tc_fence_after();
-                product_u(hd, 1);
+                for (int k = 0; k < 8; ++k)
+                    mma_f16(tmem + kColY1, smem_desc(base + L::kC + (k >> 2) * kBlock + (k & 3) * 32, 16, 1024, kSwizzle128),
+                            smem_desc(base + L::kState + k * 2048, kBlock, 1024, kSwizzle128), id_y, k > 0);
             }
+            __syncwarp();
+            for (int hd = 0; hd < heads && ok; ++hd) ok = x.wait(kP1 + hd, ph);
+            if (!ok) break;
+            __syncwarp();
+            tc_fence_after();
+            product_u(1);
             if (!ok) break;
             // the last commit covers every product so far: C and B are free
             if (i + 1 < tiles) {
-                ok = x.wait(kU + heads - 1, ph);
+                ok = x.wait(kU, ph);
                 if (!ok) break;
                 __syncwarp();
                 load_bc(i + 1);
