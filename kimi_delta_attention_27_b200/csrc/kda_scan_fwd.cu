@@ -479,11 +479,11 @@ int64_t fwd_piece_tokens(int64_t rows, int64_t n, bool packed, int32_t H, int32_
                                          : piece_tokens(rows, n, packed, columns, 2 * 148, T);
 }
 // The backward's runs of the state, both directions at once; at a state size of 128 their tiles take so little that
-// packed sequences, too, are cut only below half of the slots (the gradients of 2 packed ones, 13493 tokens x 64 heads:
-// 656 us whole, 827 cut).
+// packed sequences, too, are cut only below half of the slots (the gradients of 2 packed ones, 13493 tokens x 64 heads,
+// with tiles of 64 tokens: 656 us whole, 827 cut).
 int64_t state_piece_tokens(int64_t rows, int64_t n, bool packed, int32_t H, int32_t P, int32_t N) {
     const int64_t columns = static_cast<int64_t>(H) * (P / PC);
-    return N == 128 ? piece_tokens(rows, n, false, (columns + 1) / 2 * 2, 148, T)
+    return N == 128 ? piece_tokens(rows, n, false, (columns + 1) / 2 * 2, 148, kScanTcTile)
                     : piece_tokens(rows, n, packed, 2 * columns, 3 * 148, T);
 }
 

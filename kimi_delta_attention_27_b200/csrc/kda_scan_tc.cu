@@ -17,7 +17,7 @@
 // thread issues the products; two warps run ahead with the gates and the loads of x. A tile's outputs are finished in the
 // next tile, between the two halves of its parts, so that no product is waited for while there is work, and nothing but
 // Y1 waits for the state. (65536 tokens x 32 heads x 128 in pieces: 565 us, 9650 cycles for two heads' tile; with Y1 and U
-// by head 584; warp-level products with tiles of 64 tokens 1.2 ms.)
+// by head 584; warp-level products with tiles of 64 tokens 1.13 ms.)
 //
 // L . G is formed without one exponential per element: with a_b = Gamma at the end of a block of 32 columns,
 // L_ts = e^(Gamma_t - a_b) e^(a_b - Gamma_s), a factor per row and one per column, both at most 1 for the

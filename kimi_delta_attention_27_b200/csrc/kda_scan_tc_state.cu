@@ -1,20 +1,20 @@
 // kda_scan_tc_state.cu -- the scan's state alone, state size 128, on tcgen05, sm_100a.
 //
 // Two uses: what each piece of a cut sequence adds to the state (kda_scan_fwd.cu), and, for the backward, the
-// state S entering every cell of 128 tokens, two tiles, and the gradient R of the state leaving it:
+// state S entering every tile of 128 tokens and the gradient R of the state leaving it:
 //
 //   S_end = e^(Gamma_end) S_0 + B^T Diag(d e^(Gamma_end - Gamma)) x          tiles in order
 //   R_0   = e^(Gamma_end) R_end + C^T Diag(e^Gamma) dy                       tiles backwards (blockIdx.y 1)
 //
-// per 64 columns of a head, U = rows^T Diag(weight) cols being one tcgen05 product (128 x 64, K 64), with the
+// per 64 columns of a head, U = rows^T Diag(weight) cols being one tcgen05 product (128 x 64, K 128), with the
 // weighted columns in S bf16 parts (three: 24 bits). The state stays fp32 in the registers of 256 threads.
 //
-// Bound by the product: its operands come from shared memory, 128 bytes a cycle. So a CTA takes two heads of a
-// group side by side (one product with N = 128 reads the rows once for both: 64 cycles per K step and
-// part instead of 2 x 48), 768 cycles per tile with three parts. Eight warps per head form the parts of the
-// next tile while this one's product runs, then add U to the state; four warps run ahead with gates and loads.
-// (2 x 4096 tokens x 64 heads x 64, both directions, states stored every 128 tokens: 123 us, 3400 cycles for two heads'
-// tile, the L1 pipes 62 % busy.)
+// A CTA takes two heads of a group side by side: one product with N = 128 reads the rows once for both, 64 cycles per
+// K step and part instead of 2 x 48, 1536 per tile with three parts. Eight warps per head form the parts of the next tile,
+// half by half, while this one's product runs, then add U to the state; four warps run ahead with gates and loads. Bound
+// by the elements' chain: parts, fence, U, state. (65536 tokens x 32 heads x 128, two parts: 224 us, 3850 cycles for two
+// heads' tile; with tiles of 64 tokens 277. 2 x 4096 tokens x 64 heads x 64, both directions, every tile's states stored:
+// 113 us; 123.)
 //
 // Every wait is bounded; one that runs out raises kErrTimeout and winds the CTA down.
 #include <cuda_bf16.h>
@@ -29,34 +29,41 @@ namespace tc {
 __device__ unsigned int g_scan_state_error = 0;
 
 constexpr int kIssuer = 16, kFeeder = 17, NT = 32 * 21;
-constexpr int kRowStages = 3;
+constexpr int TT = kScanTcTile;
 
 struct StateGates {
-    float weight[T];
+    float weight[TT];
     float total;
     float pad[3];
 };
 
-constexpr uint32_t kTile = T * 128;       // 64 rows of 128 bytes
+struct StateRest {
+    Two decay[4];
+    uint32_t tmem, abort;
+};
+
+constexpr uint32_t kHalf = 64 * 128;      // 64 rows of 128 bytes
 template <int S>
 struct StateSmem {
-    static constexpr uint32_t kRows = 0;                                   // [stage] 64 x 128: two blocks of columns
-    static constexpr uint32_t kCols = kRows + kRowStages * 2 * kTile;      // [head][stage]
-    static constexpr uint32_t kParts = kCols + 4 * kTile;                  // [stage][S][head]
-    static constexpr uint32_t kGates = kParts + 2 * S * 2 * kTile;         // [head][4]
-    static constexpr uint32_t kBars = kGates + 8 * sizeof(StateGates);
-    static constexpr uint32_t kBytes = kBars + 256;
-    static_assert(kBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
+    static constexpr uint32_t kRows = 0;                                   // [stage] 128 x 128: two blocks of columns
+    static constexpr uint32_t kCols = kRows + 4 * kBlock;                  // [head][stage]
+    static constexpr uint32_t kParts = kCols + 4 * kBlock;                 // [half][S][head] 64 tokens
+    static constexpr uint32_t kGates = kParts + 2 * S * 2 * kHalf;         // [head][stage]
+    static constexpr uint32_t kBars = kGates + 4 * sizeof(StateGates);
+    static constexpr uint32_t kRest = kBars + 8 * 20;                      // StateRest
+    static constexpr uint32_t kBytes = kRest + 64;
+    static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
 };
 
 enum : int {
     kRowsFull = 0,      // [stage]
-    kColsFull = 3,      // [head][stage]
-    kGatesFull = 7,     // [head][4]
-    kU = 15,            // [stage] the product is done
-    kColsFree = 17,     // [head][stage], the head's eight warps: the columns and gates have been used
-    kParts = 21,        // [stage], all element warps: the parts are written
-    kBarCount = 23
+    kColsFull = 2,      // [head][stage]
+    kGatesFull = 6,     // [head][stage]
+    kPFree = 10,        // the first half's product is done
+    kU = 11,            // [stage] the tile's products are done
+    kColsFree = 13,     // [head][stage], the head's eight warps: the columns and gates have been used
+    kParts = 17,        // [half], all element warps: the parts are written
+    kBarCount = 19
 };
 
 struct StateMaps {
@@ -70,11 +77,10 @@ __global__ void __launch_bounds__(NT, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     using L = StateSmem<S>;
     const uint32_t base = smem_u32(smem);
-    __shared__ uint32_t s_tmem, s_abort;
-    __shared__ Two s_decay[4];
+    StateRest &rest = *reinterpret_cast<StateRest *>(smem + L::kRest);
     Ctx x;
     x.bars = base + L::kBars;
-    x.abort = &s_abort;
+    x.abort = &rest.abort;
     x.error = &g_scan_state_error;
     StateGates *gates = reinterpret_cast<StateGates *>(smem + L::kGates);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -89,24 +95,29 @@ __global__ void __launch_bounds__(NT, 1)
     const Piece u = find_piece(p.seqs, unit, seg);
     const bool head = rev ? u.last : u.first, tail = rev ? u.first : u.last;
     if (u.none || (run.leave && tail)) return;
-    const int64_t lo = u.a / T;
-    const int tiles = static_cast<int>(u.b > u.a ? (u.b + T - 1) / T - lo : 0);
+    const int64_t lo = u.a / TT;
+    const int tiles = static_cast<int>(u.b > u.a ? (u.b + TT - 1) / TT - lo : 0);
     auto cell = [&](int i) { return rev ? lo + tiles - 1 - i : lo + i; };
+    auto start_of = [&](int i) { return cell(i) * TT > u.a ? cell(i) * TT : u.a; };
+    auto count_of = [&](int i) {
+        const int64_t e = (cell(i) + 1) * TT < u.b ? (cell(i) + 1) * TT : u.b;
+        return static_cast<int>(e - start_of(i));
+    };
 
     if (warp == kIssuer) {
         if (lane == 0) {
             for (int i = 0; i < kBarCount; ++i) mbar_init(x.bar(i), i < kColsFree ? 1 : i < kParts ? 8 : 8 * heads);
-            s_abort = 0;
+            rest.abort = 0;
             fence_mbar_init();
         }
         __syncwarp();
-        tmem_alloc(smem_u32(&s_tmem), 256);
+        tmem_alloc(smem_u32(&rest.tmem), 256);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = rest.tmem;
 
     if (warp < kIssuer) {
         // ---------------------------------------------------------------- a head's elements
@@ -140,23 +151,26 @@ __global__ void __launch_bounds__(NT, 1)
                 for (int m = 0; m < 16; ++m) *reinterpret_cast<float2 *>(dst + place(m)) = s[m];
             };
             float total = 0.f, next_total = 0.f;
-            // the weighted columns of tile i in parts; four threads per token
-            auto write_parts = [&](int i) {
-                const int64_t c = cell(i);
-                const int cnt = tile_count(u, c), row = t256 >> 2;
-                if (!x.wait(kColsFull + hd * 2 + (i & 1), (i >> 1) & 1) || !x.wait(kGatesFull + hd * 4 + (i & 3), (i >> 2) & 1))
-                    return false;
-                if (cnt < T && hd == 0) {
-                    // rows behind the piece: whatever they hold would multiply zeros below
-                    if (!x.wait(kRowsFull + i % kRowStages, (i / kRowStages) & 1)) return false;
-                    uint8_t *rt = smem + L::kRows + (i % kRowStages) * 2 * kTile + row * 128;
-                    if (row >= cnt)
+            // the weighted columns of half a tile in parts; four threads per token
+            auto write_parts = [&](int i, int half) {
+                const int cnt = count_of(i), st = i & 1, row = half * 64 + (t256 >> 2);
+                const uint32_t ph = (i >> 1) & 1;
+                if (half == 0) {
+                    if (!x.wait(kColsFull + hd * 2 + st, ph) || !x.wait(kGatesFull + hd * 2 + st, ph)) return false;
+                    if (cnt < TT && hd == 0) {
+                        // rows behind the piece: whatever they hold would multiply zeros below
+                        if (!x.wait(kRowsFull + st, ph)) return false;
+                        uint8_t *rt = smem + L::kRows + st * 2 * kBlock + (t256 & 1) * kBlock + (t256 >> 1) * 128;
+                        if ((t256 >> 1) >= cnt)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) sts(rt + (j >> 1) * kTile + ((t256 & 3) * 2 + (j & 1)) * 16, make_uint4(0u, 0u, 0u, 0u));
+                            for (int j = 0; j < 8; ++j) sts(rt + j * 16, make_uint4(0u, 0u, 0u, 0u));
+                    }
                 }
-                const StateGates &g = gates[hd * 4 + (i & 3)];
-                const uint8_t *ct = smem + L::kCols + (hd * 2 + (i & 1)) * kTile;
-                uint8_t *parts = smem + L::kParts + (i & 1) * S * 2 * kTile + hd * kTile;
+                // the last tile's have been multiplied
+                if (i > 0 && !(half ? x.wait(kU + (st ^ 1), ((i - 1) >> 1) & 1) : x.wait(kPFree, (i - 1) & 1))) return false;
+                const StateGates &g = gates[hd * 2 + st];
+                const uint8_t *ct = smem + L::kCols + (hd * 2 + st) * kBlock;
+                uint8_t *parts = smem + L::kParts + half * S * 2 * kHalf + hd * kHalf;
                 const float w = g.weight[row];
                 next_total = g.total;
                 const float2 w2 = make_float2(w, w), minus1 = make_float2(-1.f, -1.f);
@@ -182,24 +196,20 @@ __global__ void __launch_bounds__(NT, 1)
                     }
 #pragma unroll
                     for (int e = 0; e < S; ++e)
-                        sts(parts + e * 2 * kTile + sw128(row, chunk), make_uint4(o[e][0], o[e][1], o[e][2], o[e][3]));
+                        sts(parts + e * 2 * kHalf + sw128(t256 >> 2, chunk), make_uint4(o[e][0], o[e][1], o[e][2], o[e][3]));
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                x.arrive(kParts + (i & 1));
-                x.arrive(kColsFree + hd * 2 + (i & 1));
+                x.arrive(kParts + half);
+                if (half) x.arrive(kColsFree + hd * 2 + st);
                 return true;
             };
-            bool ok = tiles == 0 || write_parts(0);
+            bool ok = tiles == 0 || (write_parts(0, 0) && write_parts(0, 1));
             for (int i = 0; i < tiles && ok; ++i) {
                 total = next_total;
-                if (i + 1 < tiles) ok = write_parts(i + 1);
+                if (i + 1 < tiles) ok = write_parts(i + 1, 0) && write_parts(i + 1, 1);
                 if (!ok) break;
-                if (run.states) {
-                    // of the two tiles of a cell the one that the direction enters first
-                    const int64_t c = cell(i);
-                    if ((c & 1) == (rev ? 1 : 0) || (head && i == 0)) store(run.states + ((u.i + c / 2) * p.H + h) * sn + at_r);
-                }
+                if (run.states) store(run.states + ((u.i + cell(i)) * p.H + h) * sn + at_r);
                 ok = x.wait(kU + (i & 1), (i >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
@@ -219,11 +229,11 @@ __global__ void __launch_bounds__(NT, 1)
         // ---------------------------------------------------------------- loads of the rows, and the products
         auto load_rows = [&](int i) {
             if (elect_one()) {
-                const int st = i % kRowStages;
-                const uint32_t bar = x.bar(kRowsFull + st), dst = base + L::kRows + st * 2 * kTile;
-                const int32_t row = static_cast<int32_t>(tile_start(u, cell(i)));
-                mbar_arrive_expect_tx(bar, 2 * kTile);
-                for (int k = 0; k < 2; ++k) tma_load_2d(dst + k * kTile, &maps.rows[rev], bar, grp * N + 64 * k, row);
+                const int st = i & 1;
+                const uint32_t bar = x.bar(kRowsFull + st), dst = base + L::kRows + st * 2 * kBlock;
+                const int32_t row = static_cast<int32_t>(start_of(i));
+                mbar_arrive_expect_tx(bar, 2 * kBlock);
+                for (int k = 0; k < 2; ++k) tma_load_2d(dst + k * kBlock, &maps.rows[rev], bar, grp * N + 64 * k, row);
             }
             __syncwarp();
         };
@@ -232,26 +242,28 @@ __global__ void __launch_bounds__(NT, 1)
         for (int i = 0; i < 2 && i < tiles; ++i) load_rows(i);
         for (int i = 0; i < tiles && ok; ++i) {
             const int st = i & 1;
-            ok = x.wait(kRowsFull + i % kRowStages, (i / kRowStages) & 1) && x.wait(kParts + st, (i >> 1) & 1);
-            if (!ok) break;
-            __syncwarp();
-            tc_fence_after();
-            if (elect_one()) {
-                const uint32_t rt = base + L::kRows + (i % kRowStages) * 2 * kTile;
-                const uint32_t parts = base + L::kParts + st * S * 2 * kTile;
+            ok = x.wait(kRowsFull + st, (i >> 1) & 1);
+            for (int half = 0; half < 2 && ok; ++half) {
+                ok = x.wait(kParts + half, i & 1);
+                if (!ok) break;
+                __syncwarp();
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t rt = base + L::kRows + st * 2 * kBlock + half * 4 * 2048;
+                    const uint32_t parts = base + L::kParts + half * S * 2 * kHalf;
 #pragma unroll
-                for (int k = 0; k < T / 16; ++k)
+                    for (int k = 0; k < 4; ++k)
 #pragma unroll
-                    for (int e = S - 1; e >= 0; --e)
-                        mma_f16(tmem + st * 128, smem_desc(rt + k * 2048, kTile, 1024, kSwizzle128),
-                                smem_desc(parts + e * 2 * kTile + k * 2048, kTile, 1024, kSwizzle128), id,
-                                !(k == 0 && e == S - 1));
-                mma_commit(x.bar(kU + st));
+                        for (int e = S - 1; e >= 0; --e)
+                            mma_f16(tmem + st * 128, smem_desc(rt + k * 2048, kBlock, 1024, kSwizzle128),
+                                    smem_desc(parts + e * 2 * kHalf + k * 2048, kHalf, 1024, kSwizzle128), id,
+                                    !(half == 0 && k == 0 && e == S - 1));
+                    mma_commit(x.bar(half ? kU + st : kPFree));
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            if (i + 2 < tiles) {
-                // its stage held the last tile's rows
-                if (i > 0) ok = x.wait(kU + ((i - 1) & 1), ((i - 1) >> 1) & 1);
+            if (ok && i + 2 < tiles) {
+                ok = x.wait(kU + st, (i >> 1) & 1);   // this tile's rows have been multiplied
                 if (!ok) break;
                 __syncwarp();
                 load_rows(i + 2);
@@ -259,46 +271,61 @@ __global__ void __launch_bounds__(NT, 1)
         }
     } else {
         // ---------------------------------------------------------------- a head's gates and columns, every other tile
-        const int f = warp - kFeeder, hd = f >> 1, v = v0 + hd;
+        const int f = warp - kFeeder, hd = f >> 1, v = v0 + hd, t4 = 4 * lane;
         if (hd < heads) {
             const int h = v / slices;
             const Two rate = log2_rate(p.A[h]);
+            const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
             Two decay = {0.f, 0.f};
             bool ok = true;
-            float d0 = 0.f, d1 = 0.f;
+            float dt[4] = {0.f, 0.f, 0.f, 0.f};
             auto steps = [&](int i) {
-                const int64_t c = cell(i);
-                load_steps(p, tile_start(u, c), tile_count(u, c), h, d0, d1);
+                const int cnt = count_of(i);
+                const float *src = p.dt + start_of(i) * p.H + h;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) dt[j] = t4 + j < cnt ? src[static_cast<int64_t>(t4 + j) * p.H] : 0.f;
             };
             if ((f & 1) < tiles) steps(f & 1);
             for (int i = f & 1; i < tiles; i += 2) {
-                StateGates &g = gates[hd * 4 + (i & 3)];
-                const Two l0 = log_decay(d0, rate), l1 = log_decay(d1, rate);
-                const Two sum = scan_lanes(l0 + l1), all = shfl(sum, 31);
-                const Two before = {__shfl_up_sync(0xffffffffu, sum.hi, 1), __shfl_up_sync(0xffffffffu, sum.lo, 1)};
-                const Two first = lane ? before + l0 : l0;
-                const float w0 = rev ? ex2(first) : d0 * ex2(minus(all, first));
-                const float w1 = rev ? ex2(sum) : d1 * ex2(minus(all, sum));
-                reinterpret_cast<float2 *>(g.weight)[lane] = make_float2(w0, w1);
-                if (lane == 0) g.total = ex2(all);
-                decay = decay + all;
-                x.arrive(kGatesFull + hd * 4 + (i & 3));
-                if (i >= 2) ok = x.wait(kColsFree + hd * 2 + (i & 1), ((i - 2) >> 1) & 1);
+                const int st = i & 1, cnt = count_of(i);
+                if (i >= 2) ok = x.wait(kColsFree + hd * 2 + st, ((i - 2) >> 1) & 1);
                 if (!ok) break;
                 __syncwarp();
                 if (elect_one()) {
-                    const int bar = kColsFull + hd * 2 + (i & 1);
-                    mbar_arrive_expect_tx(x.bar(bar), kTile);
-                    tma_load_2d(base + L::kCols + (hd * 2 + (i & 1)) * kTile, &maps.cols[rev], x.bar(bar), v * PC,
-                                static_cast<int32_t>(tile_start(u, cell(i))));
+                    const int bar = kColsFull + hd * 2 + st;
+                    mbar_arrive_expect_tx(x.bar(bar), kBlock);
+                    tma_load_2d(base + L::kCols + (hd * 2 + st) * kBlock, &maps.cols[rev], x.bar(bar), v * PC,
+                                static_cast<int32_t>(start_of(i)));
                 }
                 __syncwarp();
+                StateGates &g = gates[hd * 2 + st];
+                float d[4], w[4];
+                Two c[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float arg;
+                    d[j] = t4 + j < cnt ? step_of(dt[j], bias, p.softplus, &arg) : 0.f;
+                    c[j] = log_decay(d[j], rate);
+                    if (j) c[j] = c[j - 1] + c[j];
+                }
                 if (i + 2 < tiles) steps(i + 2);
+                const Two sum = scan_lanes(c[3]), all = shfl(sum, 31);
+                Two before = {__shfl_up_sync(0xffffffffu, sum.hi, 1), __shfl_up_sync(0xffffffffu, sum.lo, 1)};
+                if (lane == 0) before = {0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const Two at = before + c[j];
+                    w[j] = rev ? ex2(at) : d[j] * ex2(minus(all, at));
+                }
+                reinterpret_cast<float4 *>(g.weight)[lane] = make_float4(w[0], w[1], w[2], w[3]);
+                if (lane == 0) g.total = ex2(all);
+                decay = decay + all;
+                x.arrive(kGatesFull + hd * 2 + st);
             }
-            if (lane == 0) s_decay[f] = decay;
+            if (lane == 0) rest.decay[f] = decay;
         }
     }
-    if (s_abort) {
+    if (rest.abort) {
         // copies may still be in flight into this CTA's shared memory
         const uint64_t t0 = globaltimer();
         while (globaltimer() - t0 < 20000000ull) {
@@ -309,7 +336,7 @@ __global__ void __launch_bounds__(NT, 1)
     tc_fence_after();
     if (warp == kIssuer) tmem_dealloc(tmem, 256);
     if (run.leave && tid < heads && (v0 + tid) % slices == 0)
-        run.leave_decay[unit * p.H + (v0 + tid) / slices] = ex2(s_decay[2 * tid] + s_decay[2 * tid + 1]);
+        run.leave_decay[unit * p.H + (v0 + tid) / slices] = ex2(rest.decay[2 * tid] + rest.decay[2 * tid + 1]);
 }
 
 template <int S>
@@ -318,10 +345,10 @@ cudaError_t state_launch(const ScanParams &p, int directions, int64_t seg, int64
     StateMaps maps;
     memset(&maps, 0, sizeof(maps));
     const int64_t hp = static_cast<int64_t>(p.H) * p.P, gn = static_cast<int64_t>(p.G) * N;
-    if (p.rows > 0 && (!encode(&maps.rows[0], p.B, gn, p.rows, p.b_stride, T) ||
-                       !encode(&maps.cols[0], p.x, hp, p.rows, p.x_stride, T) ||
-                       (directions > 1 && (!encode(&maps.rows[1], p.C, gn, p.rows, p.c_stride, T) ||
-                                           !encode(&maps.cols[1], p.dout, hp, p.rows, p.dout_stride, T)))))
+    if (p.rows > 0 && (!encode(&maps.rows[0], p.B, gn, p.rows, p.b_stride, TT) ||
+                       !encode(&maps.cols[0], p.x, hp, p.rows, p.x_stride, TT) ||
+                       (directions > 1 && (!encode(&maps.rows[1], p.C, gn, p.rows, p.c_stride, TT) ||
+                                           !encode(&maps.cols[1], p.dout, hp, p.rows, p.dout_stride, TT)))))
         return cudaErrorInvalidValue;
     cudaError_t err = allow_smem(scan_state_tc_kernel<S>, StateSmem<S>::kBytes);
     if (err != cudaSuccess) return err;
