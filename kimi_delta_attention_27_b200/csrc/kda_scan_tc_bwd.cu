@@ -103,12 +103,12 @@ enum : int {
     kSumsFree = 11,   // the helper has read a head's sums
     kByAll = 12,
     kQReady = 12,     // the place of Qt is free, x and dy end in zeros
-    kScaled = 13,     // the scaled rows are written, the last head's x and dy used
-    kSParts = 14, kRParts = 15,
-    kMk = 16,         // Mt and Kt are written
-    kSums = 17,       // a head's sums are written
-    kQRead = 18,      // [quarter] its four warps have read Qt
-    kBarCount = 22
+    kSParts = 13,     // S_0's parts and the scaled rows are written, the last head's x and dy used
+    kRParts = 14,     // R's parts are written
+    kMk = 15,         // Mt and Kt are written
+    kSums = 16,       // a head's sums are written
+    kQRead = 17,      // [quarter] its four warps have read Qt
+    kBarCount = 21
 };
 
 // The gates of a head, by one warp: lane l has tokens 4 l .. 4 l + 3 (u: their steps before softplus).
@@ -344,7 +344,6 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
-            x.arrive(kScaled);
             x.arrive(kSParts);
             // ---- Mt, Kt (where S_0 was) and the sums of Mt . Qt
             ok = x.wait(kSParts, ph ^ 1) && x.wait(kQ, ph ^ 1) && (k == 0 || sl > 0 || x.wait(kSumsFree, (hh - 1) & 1));
@@ -608,7 +607,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
                 mma_commit(x.bar(kQ));
             }
             __syncwarp();
-            ok = x.wait(kScaled, ph) && x.wait(kSParts, ph ^ 1);
+            ok = x.wait(kSParts, ph ^ 1);
             if (!ok) break;
             __syncwarp();
             tc_fence_after();
