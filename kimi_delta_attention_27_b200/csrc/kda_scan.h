@@ -65,8 +65,8 @@ cudaError_t read_and_clear_scan_error(unsigned int *value);
 size_t scan_states_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N);
 cudaError_t launch_scan_states(const ScanParams &p, float *states, float *grads, float *ws, cudaStream_t stream);
 
-// The kernels for a state size of 128 (kda_scan_tc.cu, kda_scan_tc_state.cu). The main run over pieces, from the
-// states in `entering` or from h0:
+// On tcgen05 (kda_scan_tc.cu, kda_scan_tc_state.cu). The main run over pieces, state size 128, from the states in
+// `entering` or from h0:
 cudaError_t launch_scan_tc(const ScanParams &p, int64_t seg, int64_t units, const float *entering, cudaStream_t stream);
 // and the state alone, with its weighted columns in 2 or 3 bf16 parts, over the tokens (fwd) and, with two
 // directions, over dy and C backwards (rev).

@@ -23,7 +23,7 @@
 // latency of a tile's chain: one sequence of 200 tokens x 32 heads, four tiles, 19 us.
 //
 // Few long sequences make few CTAs. Then sequences are cut into pieces of whole tiles: a first launch
-// finds each piece's own contribution to the state it leaves (from zero), scan_join_kernel adds those up
+// (kda_scan_tc_state.cu) finds each piece's own contribution to the state it leaves (from zero), scan_join_kernel adds those up
 // along each sequence, and the main launch runs all pieces at once from the states they enter with. Pieces
 // lie on a global grid of `seg` tokens, so sequence i's piece in cell c has number i + c, no matter how
 // the lengths fall, and a CTA finds its sequence by one search.
@@ -329,91 +329,6 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p, int64_t s
         write_state<MT>(acc, p.hT, (static_cast<int64_t>(u.i) * p.H + h) * sn + col, p.hT_fp32, p.P, n0);
 }
 
-// The state alone. Forwards: from zero (or `entering`) over the piece's tiles with rows B, columns x and
-// weights d e^(Gamma_end - Gamma). Reverse: the gradient of the state, over the tiles backwards, with rows
-// C, columns dy and weights e^Gamma:  R_start = e^(Gamma_end) R_end + C^T Diag(e^Gamma) dy.
-// `leave`: what each piece adds (leave[unit], and its decay leave_decay[unit, h]); pieces behind which
-// nothing follows need none. `states`: the state at every cell's entry (reverse: exit). State size 64; at 128 it is
-// kda_scan_tc_state.cu. (Both directions of 5 packed sequences, 5001 tokens x 32 heads x 128: 77 us, 117 in two launches.)
-template <int S>
-__global__ void __launch_bounds__(NT, 3) scan_state_kernel(ScanParams p, int64_t seg, ScanStateRun run0, ScanStateRun run1) {
-    extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr int N = 64, MT = N / 64, ROWB = N * 2, kR = T * N * 2, kX = T * PC * 2, kStage = kR + kX;
-    Gates *gates = reinterpret_cast<Gates *>(smem + 2 * kStage);
-    const uint32_t base = smem_addr(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int slices = p.P / PC, hs = static_cast<int>(blockIdx.x % (p.H * slices));
-    const int h = hs / slices, col = (hs % slices) * PC;
-    const int64_t unit = blockIdx.x / (p.H * slices);
-    const bool rev = blockIdx.y == 1;
-    const float *entering = rev ? run1.entering : run0.entering;
-    float *leave = rev ? run1.leave : run0.leave, *leave_decay = rev ? run1.leave_decay : run0.leave_decay;
-    float *states = rev ? run1.states : run0.states;
-    if (blockIdx.x == 0 && !rev) check_offsets(p.seqs, &g_scan_error);
-    const Piece u = find_piece(p.seqs, unit, seg);
-    const bool head = rev ? u.last : u.first, tail = rev ? u.first : u.last;
-    if (u.none || (leave && tail)) return;
-    const int n0 = warp * (N / 4);
-    const int64_t grp = h / (p.H / p.G);
-    const uint16_t *cols = rev ? p.dout : p.x, *rows = rev ? p.C : p.B;
-    const int64_t cstr = rev ? p.dout_stride : p.x_stride, rstr = rev ? p.c_stride : p.b_stride;
-    cols += static_cast<int64_t>(h) * p.P + col;
-    rows += grp * N;
-    const float A = p.A[h];
-    const int64_t sn = static_cast<int64_t>(N) * p.P, at_seq = (static_cast<int64_t>(u.i) * p.H + h) * sn + col;
-    float acc[MT][8][4];
-    if (entering)
-        read_state<MT>(acc, entering, (unit * p.H + h) * sn + col, true, p.P, n0);
-    else if (head && !leave)
-        read_state<MT>(acc, rev ? static_cast<const void *>(p.dhT) : p.h0, at_seq, rev || p.h0_fp32, p.P, n0);
-    else
-        read_state<MT>(acc, nullptr, 0, true, p.P, n0);
-    const int64_t lo = u.a / T, n_tiles = u.b > u.a ? (u.b + T - 1) / T - lo : 0;
-    auto cell = [&](int64_t k) { return rev ? lo + n_tiles - 1 - k : lo + k; };
-    auto fetch = [&](int64_t c, int stage) {
-        const int64_t s = tile_start(u, c);
-        const int cnt = tile_count(u, c);
-        const uint32_t d = base + stage * kStage;
-        load_tile<ROWB, NT>(d, rows + s * rstr, rstr, cnt);
-        load_tile<PC * 2, NT>(d + kR, cols + s * cstr, cstr, cnt);
-        cp_async_commit();
-    };
-    Two decay = {0.f, 0.f};
-    float d0 = 0.f, d1 = 0.f;
-    const bool gate_warp = warp == static_cast<int>(blockIdx.x & 3);
-    if (n_tiles > 0) {
-        fetch(cell(0), 0);
-        if (gate_warp) {
-            load_steps(p, tile_start(u, cell(0)), tile_count(u, cell(0)), h, d0, d1);
-            decay = decay + make_gates(gates[0], d0, d1, A);
-            if (n_tiles > 1) load_steps(p, tile_start(u, cell(1)), tile_count(u, cell(1)), h, d0, d1);
-        }
-    }
-    int stage = 0;
-    for (int64_t k = 0; k < n_tiles; ++k, stage ^= 1) {
-        cp_async_wait_all();
-        __syncthreads();
-        if (k + 1 < n_tiles) fetch(cell(k + 1), stage ^ 1);
-        if (gate_warp && k + 1 < n_tiles) {
-            decay = decay + make_gates(gates[(k + 1) & 1], d0, d1, A);
-            if (k + 2 < n_tiles) load_steps(p, tile_start(u, cell(k + 2)), tile_count(u, cell(k + 2)), h, d0, d1);
-        }
-        // of the two tiles of a cell the one that the direction enters first
-        const int64_t c = cell(k);
-        if (states && ((c & 1) == (rev ? 1 : 0) || (head && k == 0)))
-            write_state<MT>(acc, states, ((u.i + c / 2) * p.H + h) * sn + col, true, p.P, n0);
-        const Gates &g = gates[k & 1];
-        const uint32_t rt = base + stage * kStage;
-        add_tile<ROWB, MT, S>(acc, g.total, rt, rt + kR, rev ? g.from : g.weight, n0);
-    }
-    if (leave) {
-        write_state<MT>(acc, leave, (unit * p.H + h) * sn + col, true, p.P, n0);
-        if (gate_warp && lane == 0 && col == 0) leave_decay[unit * p.H + h] = ex2(decay);
-    } else if (rev && tail && p.dh0) {
-        write_state<MT>(acc, p.dh0, at_seq, true, p.P, n0);
-    }
-}
-
 // Along every sequence: pieces' own contributions become the states they enter with, in place:
 // S = init;  for each piece: (its contribution, S) <- (S, decay S + contribution).
 // grid (sequences * H, elements / 1024): a thread has four elements of the state.
@@ -467,8 +382,8 @@ __global__ void __launch_bounds__(256) scan_join_kernel(ScanParams p, int64_t se
 // two more launches, 1.5 times the work where the pieces are long and over twice that where they are not. So sequences
 // are cut where equal ones fill less than half of the slots, and packed ones, of which the longest is taken to be twice
 // the mean, fewer than all. (4096 tokens x 64 heads x 64: 2 sequences, 64 CTAs, 176 us whole, 181 cut; 3 sequences 181
-// and 231. One of 65536 tokens x 32 heads x 128, 32 CTAs: 2.62 ms whole, 0.86 cut. The states of 5 packed ones for the
-// gradients, one direction's 320 CTAs of 296: 61 us whole, 81 cut.)
+// and 231. One of 65536 tokens x 32 heads x 128, 32 CTAs: 2.62 ms whole, 0.86 cut. 2 packed ones, 13493
+// tokens x 64 heads x 64, 64 CTAs: 286 and 244.)
 int64_t piece_tokens(int64_t rows, int64_t n, bool packed, int64_t ctas, int slots, int tile) {
     if (n == 0 || (packed ? 1 : 2) * n * ctas >= slots) return 0;
     const int64_t want = 2 * slots;
@@ -488,13 +403,11 @@ int64_t fwd_piece_tokens(int64_t rows, int64_t n, bool packed, int32_t H, int32_
     return takes_tc(rows, n, columns, N) ? piece_tokens(rows, n, packed, (columns + 1) / 2, 148, kScanTcTile)
                                          : piece_tokens(rows, n, packed, columns, 2 * 148, T);
 }
-// The backward's runs of the state, both directions at once; at a state size of 128 their tiles take so little that
-// packed sequences, too, are cut only below half of the slots (the gradients of 2 packed ones, 13493 tokens x 64 heads,
+// The backward's runs of the state, both directions at once; their tiles take so little that packed sequences, too, are cut only below half of the slots (the gradients of 2 packed ones, 13493 tokens x 64 heads,
 // with tiles of 64 tokens: 656 us whole, 827 cut).
-int64_t state_piece_tokens(int64_t rows, int64_t n, bool packed, int32_t H, int32_t P, int32_t N) {
+int64_t state_piece_tokens(int64_t rows, int64_t n, int32_t H, int32_t P) {
     const int64_t columns = static_cast<int64_t>(H) * (P / PC);
-    return N == 128 ? piece_tokens(rows, n, false, (columns + 1) / 2 * 2, 148, kScanTcTile)
-                    : piece_tokens(rows, n, packed, 2 * columns, 3 * 148, T);
+    return piece_tokens(rows, n, false, (columns + 1) / 2 * 2, 148, kScanTcTile);
 }
 
 int64_t piece_count(int64_t rows, int64_t n, int64_t seg) { return seg ? rows / seg + n : n; }
@@ -502,25 +415,6 @@ int64_t piece_count(int64_t rows, int64_t n, int64_t seg) { return seg ? rows / 
 size_t piece_bytes(int64_t rows, int64_t n, int64_t seg, int32_t H, int32_t P, int32_t N) {
     if (!seg) return 0;
     return static_cast<size_t>(piece_count(rows, n, seg)) * H * (static_cast<size_t>(N) * P + 4) * sizeof(float);
-}
-
-template <int S>
-cudaError_t state_launch(const ScanParams &p, int directions, int64_t seg, int64_t units, const ScanStateRun &fwd,
-                         const ScanStateRun &rev, cudaStream_t s) {
-    constexpr int bytes = 2 * (T * 64 * 2 + T * PC * 2) + 2 * static_cast<int>(sizeof(Gates));
-    cudaError_t err = allow_smem(scan_state_kernel<S>, bytes);
-    if (err != cudaSuccess) return err;
-    const dim3 grid(static_cast<unsigned>(units * p.H * (p.P / PC)), static_cast<unsigned>(directions));
-    scan_state_kernel<S><<<grid, NT, bytes, s>>>(p, seg, fwd, rev);
-    return cudaGetLastError();
-}
-
-// The state alone (see launch_scan_tc_state)
-cudaError_t launch_state(const ScanParams &p, int parts, int directions, int64_t seg, int64_t units, const ScanStateRun &fwd,
-                         const ScanStateRun &rev, cudaStream_t s) {
-    if (p.N == 128) return launch_scan_tc_state(p, parts, directions, seg, units, fwd, rev, s);
-    return parts == 3 ? state_launch<3>(p, directions, seg, units, fwd, rev, s)
-                      : state_launch<2>(p, directions, seg, units, fwd, rev, s);
 }
 
 template <bool kReverse>
@@ -540,7 +434,7 @@ size_t scan_fwd_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, i
 
 size_t scan_states_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N) {
     // both directions' pieces
-    return 2 * scan::piece_bytes(rows, n, scan::state_piece_tokens(rows, n, true, H, P, N), H, P, N);
+    return 2 * scan::piece_bytes(rows, n, scan::state_piece_tokens(rows, n, H, P), H, P, N);
 }
 
 template <int N>
@@ -560,7 +454,7 @@ cudaError_t launch_scan_fwd(const ScanParams &p, cudaStream_t s) {
     if (units * p.H * (p.P / PC) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     if (cut) {
         float *decay = p.ws + units * p.H * p.N * p.P;
-        cudaError_t err = launch_state(p, p.hT && p.hT_fp32 ? 3 : 2, 1, seg, units, {nullptr, p.ws, decay, nullptr}, {}, s);
+        cudaError_t err = launch_scan_tc_state(p, p.hT && p.hT_fp32 ? 3 : 2, 1, seg, units, {nullptr, p.ws, decay, nullptr}, {}, s);
         if (err == cudaSuccess) err = join_launch<false>(p, seg, p.ws, decay, s);
         if (err != cudaSuccess) return err;
     }
@@ -571,7 +465,7 @@ cudaError_t launch_scan_fwd(const ScanParams &p, cudaStream_t s) {
 
 cudaError_t launch_scan_states(const ScanParams &p, float *states, float *grads, float *ws, cudaStream_t s) {
     using namespace scan;
-    const int64_t cut = state_piece_tokens(p.rows, p.seqs.n, p.seqs.cu != nullptr, p.H, p.P, p.N), seg = cut ? cut : kWhole;
+    const int64_t cut = state_piece_tokens(p.rows, p.seqs.n, p.H, p.P), seg = cut ? cut : kWhole;
     const int64_t units = piece_count(p.rows, p.seqs.n, cut);
     if (units == 0) return cudaSuccess;
     if (units * p.H * (p.P / PC) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -580,7 +474,7 @@ cudaError_t launch_scan_states(const ScanParams &p, float *states, float *grads,
     auto run = [&](bool local) {
         const ScanStateRun f = local ? ScanStateRun{nullptr, wf, df, nullptr} : ScanStateRun{cut ? wf : nullptr, nullptr, nullptr, states};
         const ScanStateRun r = local ? ScanStateRun{nullptr, wr, dr, nullptr} : ScanStateRun{cut ? wr : nullptr, nullptr, nullptr, grads};
-        return launch_state(p, 3, 2, seg, units, f, r, s);
+        return launch_scan_tc_state(p, 3, 2, seg, units, f, r, s);
     };
     cudaError_t err = cudaSuccess;
     if (cut) {

@@ -1,4 +1,4 @@
-// kda_scan_tc_state.cu -- the scan's state alone, state size 128, on tcgen05, sm_100a.
+// kda_scan_tc_state.cu -- the scan's state alone on tcgen05, sm_100a.
 //
 // Two uses: what each piece of a cut sequence adds to the state (kda_scan_fwd.cu), and, for the backward, the
 // state S entering every tile of 128 tokens and the gradient R of the state leaving it:
@@ -6,7 +6,8 @@
 //   S_end = e^(Gamma_end) S_0 + B^T Diag(d e^(Gamma_end - Gamma)) x          tiles in order
 //   R_0   = e^(Gamma_end) R_end + C^T Diag(e^Gamma) dy                       tiles backwards (blockIdx.y 1)
 //
-// per 64 columns of a head, U = rows^T Diag(weight) cols being one tcgen05 product (128 x 64, K 128), with the
+// per 64 columns of a head, U = rows^T Diag(weight) cols being one tcgen05 product (128 x 64, K 128; at a state size of 64
+// half of its rows are of no use, but the product is not what bounds it), with the
 // weighted columns in S bf16 parts (three: 24 bits). The state stays fp32 in the registers of 256 threads.
 //
 // A CTA takes two heads of a group side by side: one product with N = 128 reads the rows once for both, 64 cycles per
@@ -14,7 +15,7 @@
 // half by half, while this one's product runs, then add U to the state; four warps run ahead with gates and loads. Bound
 // by the elements' chain: parts, fence, U, state. (65536 tokens x 32 heads x 128, two parts: 224 us, 3850 cycles for two
 // heads' tile; with tiles of 64 tokens 277. 2 x 4096 tokens x 64 heads x 64, both directions, every tile's states stored:
-// 113 us; 123.)
+// 113 us; 123. The same of 5 packed sequences, 5001 tokens x 32 heads x 128, state size 64: 65 us; warp-level products, 77.)
 //
 // Every wait is bounded; one that runs out raises kErrTimeout and winds the CTA down.
 #include <cuda_bf16.h>
@@ -70,7 +71,8 @@ struct StateMaps {
     CUtensorMap rows[2], cols[2];   // B and x; C and dy
 };
 
-template <int S>
+// NS: state size. At 64 the products' upper 64 rows are of no use (their operand is whatever lies there).
+template <int S, int NS>
 __global__ void __launch_bounds__(NT, 1)
     scan_state_tc_kernel(ScanParams p, const __grid_constant__ StateMaps maps, int64_t seg, ScanStateRun run0,
                          ScanStateRun run1) {
@@ -127,12 +129,13 @@ __global__ void __launch_bounds__(NT, 1)
         if (hd < heads) {
             const int v = v0 + hd, h = v / slices, col = v % slices * PC + 32 * hf;
             const uint32_t tU = tmem + hd * 64 + 32 * hf + (static_cast<uint32_t>(wq * 32) << 16);
-            const int64_t sn = static_cast<int64_t>(N) * p.P, at_r = static_cast<int64_t>(wq * 32 + (lane >> 2)) * p.P + col + (lane & 3) * 2;
+            const bool mine = wq * 32 < NS;
+            const int64_t sn = static_cast<int64_t>(NS) * p.P, at_r = static_cast<int64_t>(wq * 32 + (lane >> 2)) * p.P + col + (lane & 3) * 2;
             float2 s[16];   // [8 i + 2 j + k]: row 16 i + 8 k + lane / 4, columns 8 j + 2 (lane % 4) and the next
             auto place = [&](int m) { return static_cast<int64_t>((m >> 3) * 16 + (m & 1) * 8) * p.P + ((m >> 1) & 3) * 8; };
             {
                 const void *init = rev ? static_cast<const void *>(p.dhT) : p.h0;
-                const void *src = run.entering ? run.entering : head && !run.leave ? init : nullptr;
+                const void *src = !mine ? nullptr : run.entering ? run.entering : head && !run.leave ? init : nullptr;
                 const bool fp32 = run.entering || rev || p.h0_fp32;
                 const int64_t e = ((run.entering ? unit : static_cast<int64_t>(u.i)) * p.H + h) * sn + at_r;
 #pragma unroll
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(NT, 1)
                         // rows behind the piece: whatever they hold would multiply zeros below
                         if (!x.wait(kRowsFull + st, ph)) return false;
                         uint8_t *rt = smem + L::kRows + st * 2 * kBlock + (t256 & 1) * kBlock + (t256 >> 1) * 128;
-                        if ((t256 >> 1) >= cnt)
+                        if ((t256 >> 1) >= cnt && (t256 & 1) < NS / 64)
 #pragma unroll
                             for (int j = 0; j < 8; ++j) sts(rt + j * 16, make_uint4(0u, 0u, 0u, 0u));
                     }
@@ -209,9 +212,10 @@ __global__ void __launch_bounds__(NT, 1)
                 total = next_total;
                 if (i + 1 < tiles) ok = write_parts(i + 1, 0) && write_parts(i + 1, 1);
                 if (!ok) break;
-                if (run.states) store(run.states + ((u.i + cell(i)) * p.H + h) * sn + at_r);
+                if (run.states && mine) store(run.states + ((u.i + cell(i)) * p.H + h) * sn + at_r);
                 ok = x.wait(kU + (i & 1), (i >> 1) & 1);
                 if (!ok) break;
+                if (!mine) continue;
                 tc_fence_after();
                 uint32_t a[2][16];
                 tmem_ld_frag(tU + (i & 1) * 128, a[0]);
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(NT, 1)
                 for (int m = 0; m < 16; ++m)
                     s[m] = fma2(s[m], tot, make_float2(f32(a[m >> 3][2 * (m & 7)]), f32(a[m >> 3][2 * (m & 7) + 1])));
             }
-            float *dst = run.leave ? run.leave : rev && tail ? p.dh0 : nullptr;
+            float *dst = !mine ? nullptr : run.leave ? run.leave : rev && tail ? p.dh0 : nullptr;
             if (ok && dst) store(dst + ((run.leave ? unit : static_cast<int64_t>(u.i)) * p.H + h) * sn + at_r);
         }
     } else if (warp == kIssuer) {
@@ -232,8 +236,8 @@ __global__ void __launch_bounds__(NT, 1)
                 const int st = i & 1;
                 const uint32_t bar = x.bar(kRowsFull + st), dst = base + L::kRows + st * 2 * kBlock;
                 const int32_t row = static_cast<int32_t>(start_of(i));
-                mbar_arrive_expect_tx(bar, 2 * kBlock);
-                for (int k = 0; k < 2; ++k) tma_load_2d(dst + k * kBlock, &maps.rows[rev], bar, grp * N + 64 * k, row);
+                mbar_arrive_expect_tx(bar, NS / 64 * kBlock);
+                for (int k = 0; k < NS / 64; ++k) tma_load_2d(dst + k * kBlock, &maps.rows[rev], bar, grp * NS + 64 * k, row);
             }
             __syncwarp();
         };
@@ -339,22 +343,22 @@ __global__ void __launch_bounds__(NT, 1)
         run.leave_decay[unit * p.H + (v0 + tid) / slices] = ex2(rest.decay[2 * tid] + rest.decay[2 * tid + 1]);
 }
 
-template <int S>
+template <int S, int NS>
 cudaError_t state_launch(const ScanParams &p, int directions, int64_t seg, int64_t units, const ScanStateRun &fwd,
                          const ScanStateRun &rev, cudaStream_t s) {
     StateMaps maps;
     memset(&maps, 0, sizeof(maps));
-    const int64_t hp = static_cast<int64_t>(p.H) * p.P, gn = static_cast<int64_t>(p.G) * N;
+    const int64_t hp = static_cast<int64_t>(p.H) * p.P, gn = static_cast<int64_t>(p.G) * NS;
     if (p.rows > 0 && (!encode(&maps.rows[0], p.B, gn, p.rows, p.b_stride, TT) ||
                        !encode(&maps.cols[0], p.x, hp, p.rows, p.x_stride, TT) ||
                        (directions > 1 && (!encode(&maps.rows[1], p.C, gn, p.rows, p.c_stride, TT) ||
                                            !encode(&maps.cols[1], p.dout, hp, p.rows, p.dout_stride, TT)))))
         return cudaErrorInvalidValue;
-    cudaError_t err = allow_smem(scan_state_tc_kernel<S>, StateSmem<S>::kBytes);
+    cudaError_t err = allow_smem(scan_state_tc_kernel<S, NS>, StateSmem<S>::kBytes);
     if (err != cudaSuccess) return err;
     const int64_t pairs = (p.H / p.G * (p.P / PC) + 1) / 2;
     const dim3 grid(static_cast<unsigned>(units * p.G * pairs), static_cast<unsigned>(directions));
-    scan_state_tc_kernel<S><<<grid, NT, StateSmem<S>::kBytes, s>>>(p, maps, seg, fwd, rev);
+    scan_state_tc_kernel<S, NS><<<grid, NT, StateSmem<S>::kBytes, s>>>(p, maps, seg, fwd, rev);
     return cudaGetLastError();
 }
 
@@ -364,8 +368,11 @@ cudaError_t state_launch(const ScanParams &p, int directions, int64_t seg, int64
 cudaError_t launch_scan_tc_state(const ScanParams &p, int parts, int directions, int64_t seg, int64_t units,
                                  const ScanStateRun &fwd, const ScanStateRun &rev, cudaStream_t s) {
     using namespace scan::tc;
-    return parts == 3 ? state_launch<3>(p, directions, seg, units, fwd, rev, s)
-                      : state_launch<2>(p, directions, seg, units, fwd, rev, s);
+    return scan::by_state(p.N, [&](auto n) {
+        constexpr int NS = decltype(n)::value;
+        return parts == 3 ? state_launch<3, NS>(p, directions, seg, units, fwd, rev, s)
+                          : state_launch<2, NS>(p, directions, seg, units, fwd, rev, s);
+    });
 }
 
 cudaError_t read_and_clear_scan_state_error(unsigned int *value) {
