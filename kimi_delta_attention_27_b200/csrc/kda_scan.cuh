@@ -72,15 +72,13 @@ struct Gates {
     float hi[T], lo[T];   // log2 of the decay from the tile's start through token t
     float d[T];           // the steps
     float from[T];        // decay from the tile's start through t
-    float to[T];          // decay from t (exclusive) to the tile's end
-    float weight[T];      // d to: what a token adds to the state that leaves the tile
+    float weight[T];      // d times the decay from t (exclusive) to the tile's end
     float total;          // decay of the whole tile
     float pad[3];
 };
 
-// By one warp: lane l has tokens 2l and 2l + 1 (steps d0, d1; 0 behind the tile's last token). Returns
-// log2 of the tile's decay.
-__device__ __forceinline__ Two make_gates(Gates &g, float d0, float d1, float A) {
+// By one warp: lane l has tokens 2l and 2l + 1 (steps d0, d1; 0 behind the tile's last token).
+__device__ __forceinline__ void make_gates(Gates &g, float d0, float d1, float A) {
     const int lane = threadIdx.x & 31;
     const Two a2 = log2_rate(A), l0 = log_decay(d0, a2), l1 = log_decay(d1, a2);
     const Two s = scan_lanes(l0 + l1), total = shfl(s, 31);
@@ -95,12 +93,9 @@ __device__ __forceinline__ Two make_gates(Gates &g, float d0, float d1, float A)
         g.lo[t] = c[j].lo;
         g.d[t] = d;
         g.from[t] = ex2(c[j]);
-        const float to = ex2(minus(total, c[j]));
-        g.to[t] = to;
-        g.weight[t] = d * to;
+        g.weight[t] = d * ex2(minus(total, c[j]));
     }
     if (lane == 0) g.total = ex2(total);
-    return total;
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
