@@ -3,7 +3,8 @@
 //
 // A call's rows are the tokens of `n` sequences one behind the other: batch rows of `len` tokens
 // each (cu == nullptr) or packed ones behind the offsets cu[0 .. n]. Offsets are clamped into
-// [0, len], so a malformed table makes wrong results but no access out of bounds; check_offsets
+// [0, len] and the first sequence begins at 0 whatever cu[0] holds, so that every row has a sequence that
+// begins at or before it: a malformed table makes wrong results but no access out of bounds. check_offsets
 // raises the error bit for it.
 #pragma once
 
@@ -22,7 +23,7 @@ struct Seqs {
 
     __device__ __forceinline__ int64_t begin(int32_t i) const {
         if (!cu) return static_cast<int64_t>(i) * len;
-        const int64_t c = cu[i];
+        const int64_t c = i ? cu[i] : 0;
         return c < 0 ? 0 : (c > len ? len : c);
     }
     // never before begin(i)
