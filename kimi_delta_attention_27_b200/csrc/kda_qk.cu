@@ -522,6 +522,13 @@ cudaError_t launch_qk_fwd(const QkParams &p, cudaStream_t s) {
 }
 
 cudaError_t launch_qk_bwd(const QkParams &p, cudaStream_t s) {
+    if (p.rows == 0) {
+        // no token, so the weights' gradients are zero; the other inputs may be NULL, and no kernel reads them
+        cudaError_t err = cudaSuccess;
+        for (float *dw : {p.dq_weight, p.dk_weight})
+            if (dw && err == cudaSuccess) err = cudaMemsetAsync(dw, 0, p.D * sizeof(float), s);
+        return err;
+    }
     const int32_t heads = p.Hq + p.Hk;
     const int per = qk::warps_per_token(p.rows, heads, p.D);
     const int32_t blocks = qk_bwd_blocks(p.rows, heads, p.D);

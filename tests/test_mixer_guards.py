@@ -40,3 +40,23 @@ def test_conv_table_that_does_not_begin_at_zero_reads_no_other_state(lib, bad):
     r = kda.kda_conv_bwd(x, w, dy, cu_seqlens=cu, initial_state=init, dfinal_state=init, want_dinitial_state=True, dx=dx)
     assert kda.device_error() == 12
     assert all(bool(torch.isfinite(r[k]).all()) for k in ("dx", "dweight", "dinitial_state"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rot", [0, 64])
+def test_qk_bwd_of_no_rows_reads_nothing(lib, rot):
+    """Positions, frequencies, q and k may be NULL where there are no rows; the weights' gradients are zeros."""
+    D = 128
+    P = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    dqw, dkw = torch.full((D,), 7.0, device="cuda"), torch.full((D,), 7.0, device="cuda")
+    ws = torch.zeros(lib.kda_qk_bwd_workspace(0, 4, 2, D), dtype=torch.uint8, device="cuda")
+    st = lib.kda_qk_bwd(None, 0, None, 0, 0, 4, 2, D, 1, 1e-6, None, None, None, None, rot, 0, 1.0, None, 0, None, 0, 1, None, 0,
+                        None, 0, P(dqw), P(dkw), P(ws), ws.numel(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert st == 0 and bool((dqw == 0).all()) and bool((dkw == 0).all()) and kda.device_error() == 0
+    # and through the binding, with rows of no tokens
+    q = torch.zeros(2, 0, 4, D, dtype=BF, device="cuda")
+    w, f = torch.ones(D, device="cuda"), torch.ones(rot // 2, device="cuda")
+    pos = torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    r = kda.kda_qk_bwd(q, q, q, q, q_weight=w, k_weight=w, positions=pos, inv_freq=f)
+    assert r["dq"].shape == q.shape and bool((r["dq_weight"] == 0).all()) and bool((r["dk_weight"] == 0).all())
