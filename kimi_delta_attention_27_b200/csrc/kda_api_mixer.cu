@@ -72,7 +72,7 @@ kda_status check_sequences(const int32_t *cu, int32_t num_seqs, int32_t batch, i
     if (batch < 0 || seq_len < 0 || num_seqs < 0) return KDA_ERR_BAD_SHAPE;
     if (cu && batch != 1) return KDA_ERR_VARLEN_BATCH;
     if (!aligned(cu, 4)) return KDA_ERR_BAD_ALIGNMENT;
-    if (seq_len > kMaxElements) return KDA_ERR_TOO_LARGE;
+    if (seq_len > kMaxElements / (batch > 1 ? batch : 1)) return KDA_ERR_TOO_LARGE;   // before their product is formed
     s->cu = cu;
     s->n = cu ? num_seqs : batch;
     s->len = seq_len;
@@ -204,6 +204,11 @@ bool scan_too_large(int64_t rows, int64_t n, int32_t H, int32_t P) {
     return 2 * kda::scan_cells(rows, n) > 0x7fffffffLL / (static_cast<int64_t>(H) * (P / 64));
 }
 
+// the gradients': the kept states' rows, too, are 32-bit coordinates
+bool scan_bwd_too_large(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N) {
+    return scan_too_large(rows, n, H, P) || kda::scan_cells(rows, n) > 0x7fffffffLL / (static_cast<int64_t>(H) * N);
+}
+
 kda_status check_workspace(const void *ws, size_t have, size_t need) {
     if (need == 0) return KDA_OK;
     if (!ws) return KDA_ERR_NULL_PTR;
@@ -248,7 +253,9 @@ kda_status kda_conv_fwd(const void *x, kda_dtype dtype, int64_t x_stride, const 
 }
 
 size_t kda_conv_bwd_workspace(int64_t total_tokens, int32_t channels, int32_t taps) {
-    if (total_tokens < 0 || channels < 8 || channels % 8 || taps < kda::kConvMinTaps || taps > kda::kConvMaxTaps) return 0;
+    if (total_tokens < 0 || channels < 8 || channels % 8 || taps < kda::kConvMinTaps || taps > kda::kConvMaxTaps ||
+        total_tokens > kMaxElements / channels)
+        return 0;
     return static_cast<size_t>(kda::conv_bwd_blocks(total_tokens, channels)) * (taps + 1) * channels * sizeof(float);
 }
 
@@ -371,7 +378,9 @@ kda_status kda_qk_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_
 
 size_t kda_qk_bwd_workspace(int64_t rows, int32_t q_heads, int32_t k_heads, int32_t head_dim) {
     if (rows < 0 || q_heads < 1 || k_heads < 0 || (head_dim != 64 && head_dim != 128 && head_dim != 256)) return 0;
-    if (q_heads > (1 << 20) || k_heads > (1 << 20)) return 0;
+    if (q_heads > (1 << 20) || k_heads > (1 << 20) ||
+        rows > kMaxElements / (static_cast<int64_t>(q_heads + k_heads) * head_dim))
+        return 0;
     return static_cast<size_t>(kda::qk_bwd_blocks(rows, q_heads + k_heads, head_dim)) * 2 * head_dim * sizeof(float);
 }
 
@@ -430,7 +439,8 @@ size_t kda_scan_fwd_workspace(int64_t total_tokens, int32_t num_seqs, int32_t nu
                               int32_t state_dim) {
     if (total_tokens < 0 || num_seqs < 0 || num_heads < 1 || (head_dim != 64 && head_dim != 128) ||
         (state_dim != 64 && state_dim != 128) || num_heads > (1 << 20) ||
-        total_tokens > kMaxElements / (static_cast<int64_t>(num_heads) * head_dim))
+        total_tokens > kMaxElements / (static_cast<int64_t>(num_heads) * head_dim) ||
+        scan_too_large(total_tokens, num_seqs, num_heads, head_dim))
         return 0;
     return kda::scan_fwd_workspace_bytes(total_tokens, num_seqs, num_heads, head_dim, state_dim);
 }
@@ -484,7 +494,8 @@ size_t kda_scan_bwd_workspace(int64_t total_tokens, int32_t num_seqs, int32_t nu
                               int32_t head_dim, int32_t state_dim) {
     if (total_tokens < 0 || num_seqs < 0 || num_heads < 1 || num_groups < 1 || num_heads % num_groups ||
         (head_dim != 64 && head_dim != 128) || (state_dim != 64 && state_dim != 128) || num_heads > (1 << 20) ||
-        total_tokens > kMaxElements / (static_cast<int64_t>(num_heads) * head_dim))
+        total_tokens > kMaxElements / (static_cast<int64_t>(num_heads) * head_dim) ||
+        scan_bwd_too_large(total_tokens, num_seqs, num_heads, head_dim, state_dim))
         return 0;
     return kda::scan_bwd_workspace_bytes(total_tokens, num_seqs, num_heads, num_groups, head_dim, state_dim);
 }
@@ -514,9 +525,7 @@ kda_status kda_scan_bwd(const void *x, int64_t x_stride, const float *dt, const 
     KDA_TRY(check_stride(rows, dx_stride, hp, 2));
     KDA_TRY(check_stride(rows, db_stride, gn, 2));
     KDA_TRY(check_stride(rows, dc_stride, gn, 2));
-    if (scan_too_large(rows, s.n, num_heads, head_dim) ||
-        kda::scan_cells(rows, s.n) > 0x7fffffffLL / (static_cast<int64_t>(num_heads) * state_dim))
-        return KDA_ERR_TOO_LARGE;   // the states' rows, too, are 32-bit coordinates
+    if (scan_bwd_too_large(rows, s.n, num_heads, head_dim, state_dim)) return KDA_ERR_TOO_LARGE;
     const size_t need = kda::scan_bwd_workspace_bytes(rows, s.n, num_heads, num_groups, head_dim, state_dim);
     KDA_TRY(check_workspace(workspace, workspace_bytes, need));
     const int64_t st = static_cast<int64_t>(s.n) * num_heads * state_dim * head_dim;

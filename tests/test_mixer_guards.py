@@ -60,3 +60,21 @@ def test_qk_bwd_of_no_rows_reads_nothing(lib, rot):
     pos = torch.zeros(2, 0, dtype=torch.int32, device="cuda")
     r = kda.kda_qk_bwd(q, q, q, q, q_weight=w, k_weight=w, positions=pos, inv_freq=f)
     assert r["dq"].shape == q.shape and bool((r["dq_weight"] == 0).all()) and bool((r["dk_weight"] == 0).all())
+
+
+def test_sizes_whose_product_passes_64_bits_are_refused(lib):
+    """batch * seq_len = 2^64 rows are not 0 rows; workspaces of sizes that a call refuses are 0."""
+    TOO_LARGE, far = 8, [ctypes.c_void_p((i + 1) << 36) for i in range(12)]   # aligned, never dereferenced
+    big = (1 << 24, 1 << 40)
+    assert lib.kda_conv_fwd(far[0], 1, 64, far[1], None, 1, None, 0, *big, 64, 4, None, far[3], far[2], 64, None) == TOO_LARGE
+    assert lib.kda_conv_bwd(far[0], 1, 64, far[1], None, 1, None, 0, *big, 64, 4, None, far[3], 1, 64, None, far[4], 64,
+                            far[5], None, None, far[6], 1 << 30, None) == TOO_LARGE
+    assert lib.kda_scan_fwd(far[0], 256, far[1], far[2], far[3], 128, far[4], 128, None, None, 1, None, 0, *big, 4, 1, 64,
+                            128, None, 0, far[7], 2, far[5], 256, far[6], 1 << 34, None) == TOO_LARGE
+    assert lib.kda_scan_bwd(far[0], 256, far[1], far[2], far[3], 128, far[4], 128, None, None, 1, None, 0, *big, 4, 1, 64,
+                            128, None, 0, far[5], 256, None, far[6], 256, far[7], far[8], far[9], 128, far[10], 128, None,
+                            None, None, far[11], 1 << 34, None) == TOO_LARGE
+    most = (1 << 63) - 1
+    assert lib.kda_conv_bwd_workspace(most, 64, 4) == 0 and lib.kda_qk_bwd_workspace(most, 1, 0, 128) == 0
+    assert lib.kda_scan_fwd_workspace(1 << 32, 1, 1, 64, 64) == 0
+    assert lib.kda_scan_bwd_workspace(0, (1 << 31) - 1, 1 << 20, 1, 128, 128) == 0
