@@ -424,7 +424,8 @@ kda_status kda_qk_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_
  *
  *   x, out : bf16 [batch, seq_len, num_heads, head_dim] (rows strided)
  *   dt     : fp32 [batch, seq_len, num_heads]
- *   A      : fp32 [num_heads], negative (d_t A is the log decay);  D, dt_bias: fp32 [num_heads] or NULL (0)
+ *   A      : fp32 [num_heads], negative (d_t A is the log decay);  D, dt_bias: fp32 [num_heads] or NULL (0).
+ *            Steps below zero are taken as they stand, as long as the state grows by less than 2^60 over 128 tokens.
  *   B, C   : bf16 [batch, seq_len, num_groups, state_dim] (rows strided); head h takes group
  *            h / (num_heads / num_groups)
  *   initial_state, final_state : [num_seqs_eff, num_heads, state_dim, head_dim], head channel fastest, bf16 or

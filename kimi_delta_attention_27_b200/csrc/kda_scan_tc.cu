@@ -21,8 +21,9 @@
 //
 // L . G is formed without one exponential per element: with a_b = Gamma at the end of a block of 32 columns,
 // L_ts = e^(Gamma_t - a_b) e^(a_b - Gamma_s), a factor per row and one per column, both at most 1 for the
-// rows behind the block. In the block on the diagonal the row's factor is above 1; where the block decays by
-// more than 2^60 its elements take an exponential each instead.
+// rows behind the block. In the block on the diagonal the row's factor is above 1; where the sums lie more than 2^60 from
+// the block's end (they may on either side: a negative step lets the state grow) its elements take an exponential each
+// instead.
 //
 // Every wait is bounded; one that runs out raises kErrTimeout and winds the CTA down.
 #include <cuda_bf16.h>
@@ -47,7 +48,7 @@ struct TcGates {
     float from[TT];         // e^Gamma
     float weight[TT];       // d e^(Gamma_end - Gamma)
     float total;
-    uint32_t steep;         // bit b: block b of 32 decays by more than 2^60
+    uint32_t steep;         // bit b: the decays within block b of 32 span more than 2^60
     float pad[2];
 };
 
@@ -114,17 +115,19 @@ __device__ __forceinline__ void make_tc_gates(TcGates &g, const float (&dt)[4], 
     Two before = {__shfl_up_sync(0xffffffffu, s.hi, 1), __shfl_up_sync(0xffffffffu, s.lo, 1)};
     if (lane == 0) before = {0.f, 0.f};
     const Two anchor = shfl(s, lane | 7), opens = shfl(before, lane & 24);   // the block's end and start
-    const unsigned steep = __ballot_sync(0xffffffffu, minus(opens, anchor) > 60.f);
-    float hi[4], lo[4], col[4], from[4], weight[4];
+    float hi[4], lo[4], col[4], from[4], weight[4], span = fabsf(minus(opens, anchor));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const Two v = before + c[j];
         hi[j] = v.hi;
         lo[j] = v.lo;
-        col[j] = d[j] * ex2(minus(anchor, v));
+        const float to_end = minus(anchor, v);
+        span = fmaxf(span, fabsf(to_end));
+        col[j] = d[j] * ex2(to_end);
         from[j] = ex2(v);
         weight[j] = d[j] * ex2(minus(total, v));
     }
+    const unsigned steep = __ballot_sync(0xffffffffu, span > 60.f);   // by eight lanes of a block each
     reinterpret_cast<float4 *>(g.hi)[lane] = make_float4(hi[0], hi[1], hi[2], hi[3]);
     reinterpret_cast<float4 *>(g.lo)[lane] = make_float4(lo[0], lo[1], lo[2], lo[3]);
     reinterpret_cast<float4 *>(g.d)[lane] = make_float4(d[0], d[1], d[2], d[3]);
@@ -133,7 +136,7 @@ __device__ __forceinline__ void make_tc_gates(TcGates &g, const float (&dt)[4], 
     reinterpret_cast<float4 *>(g.weight)[lane] = make_float4(weight[0], weight[1], weight[2], weight[3]);
     if (lane == 0) {
         g.total = ex2(total);
-        g.steep = (steep & 1u) | ((steep >> 7) & 2u) | ((steep >> 14) & 4u) | ((steep >> 21) & 8u);
+        g.steep = steep_blocks(steep);
     }
 }
 
@@ -390,8 +393,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
                                     const int sc = 32 * b + 2 * j + k;
-                                    const float q = f32(a[2 * j + k]) * g.d[sc] *
-                                                    ex2(fminf((gh - g.hi[sc]) + (glo - g.lo[sc]), 0.f));
+                                    const float q = f32(a[2 * j + k]) * g.d[sc] * ex2((gh - g.hi[sc]) + (glo - g.lo[sc]));
                                     m[k] = 2 * j + k <= lane ? q : 0.f;
                                 }
                                 o[j] = bf_pair(m[0], m[1]);

@@ -58,6 +58,11 @@ __device__ __forceinline__ uint4 lds(const uint8_t *p) { return *reinterpret_cas
 __device__ __forceinline__ void sts(uint8_t *p, uint4 v) { *reinterpret_cast<uint4 *>(p) = v; }
 __device__ __forceinline__ float f32(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t sw128(int r, int j) { return static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4)); }
+// bit b: any of the eight lanes of block b of 32 tokens, of a ballot
+__device__ __forceinline__ uint32_t steep_blocks(unsigned ballot) {
+    return (ballot & 0xffu ? 1u : 0u) | (ballot & 0xff00u ? 2u : 0u) | (ballot & 0xff0000u ? 4u : 0u) |
+           (ballot & 0xff000000u ? 8u : 0u);
+}
 // Whether the phase of the given parity has completed. Acquire at CTA scope: nothing here comes from another CTA.
 __device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity) {
     uint32_t ok;

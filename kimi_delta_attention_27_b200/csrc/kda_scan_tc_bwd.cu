@@ -49,7 +49,7 @@ struct HeadGates {
     float col[TT];          // decay from the start of the token's quarter through it
     float open_hi[4], open_lo[4];   // Gamma at the quarters' starts
     float total, A, D;
-    uint32_t steep;         // bit c: quarter c decays by more than 2^60
+    uint32_t steep;         // bit c: the decays within quarter c span more than 2^60, down or up
 };
 
 // sums over parts of the tile, for the helper: [which][token]
@@ -131,8 +131,7 @@ __device__ __forceinline__ void make_head_gates(HeadGates &g, const float (&dt)[
     Two before = {__shfl_up_sync(0xffffffffu, s.hi, 1), __shfl_up_sync(0xffffffffu, s.lo, 1)};
     if (lane == 0) before = {0.f, 0.f};
     const Two opens = shfl(before, lane & 24), closes = shfl(s, lane | 7);   // the quarter's start and end
-    const unsigned steep = __ballot_sync(0xffffffffu, minus(opens, closes) > 60.f);
-    float hi[4], lo[4], from[4], to[4], col[4];
+    float hi[4], lo[4], from[4], to[4], col[4], span = fabsf(minus(opens, closes));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const Two v = before + c[j];
@@ -140,8 +139,11 @@ __device__ __forceinline__ void make_head_gates(HeadGates &g, const float (&dt)[
         lo[j] = v.lo;
         from[j] = ex2(v);
         to[j] = ex2(minus(total, v));
-        col[j] = ex2(minus(v, opens));
+        const float from_start = minus(v, opens);
+        span = fmaxf(span, fabsf(from_start));
+        col[j] = ex2(from_start);
     }
+    const unsigned steep = __ballot_sync(0xffffffffu, span > 60.f);   // by eight lanes of a quarter each
     auto put = [&](float *dst, float a, float b, float e, float f) {
         reinterpret_cast<float4 *>(dst)[lane] = make_float4(a, b, e, f);
     };
@@ -161,7 +163,7 @@ __device__ __forceinline__ void make_head_gates(HeadGates &g, const float (&dt)[
         g.total = ex2(total);
         g.A = A;
         g.D = D;
-        g.steep = (steep & 1u) | ((steep >> 7) & 2u) | ((steep >> 14) & 4u) | ((steep >> 21) & 8u);
+        g.steep = steep_blocks(steep);
     }
 }
 
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             tc_fence_after();
             uint32_t m_out[16];
             auto k_at = [&](int j) { return smem + L::kK + (cq >> 1) * kBlock + sw128(r, (cq & 1) * 4 + j); };
-            // kind 0: t > s throughout; 1: the diagonal block; 2: that, where it decays by more than 2^60
+            // kind 0: t > s throughout; 1: the diagonal block; 2: that, where it spans more than 2^60
             auto block = [&](auto kind) {
                 constexpr int kKind = decltype(kind)::value;
                 const float gh = g.hi[r], gl = g.lo[r], ds = g.d[r];
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
                             if constexpr (kKind == 2) {
                                 const float2 th = *reinterpret_cast<const float2 *>(g.hi + 32 * cq + c);
                                 const float2 tl = *reinterpret_cast<const float2 *>(g.lo + 32 * cq + c);
-                                l = make_float2(ex2(fminf((th.x - gh) + (tl.x - gl), 0.f)), ex2(fminf((th.y - gh) + (tl.y - gl), 0.f)));
+                                l = make_float2(ex2((th.x - gh) + (tl.x - gl)), ex2((th.y - gh) + (tl.y - gl)));
                             } else {
                                 l = mul2(*reinterpret_cast<const float2 *>(g.col + 32 * cq + c), rf2);
                             }

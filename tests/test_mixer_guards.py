@@ -78,3 +78,30 @@ def test_sizes_whose_product_passes_64_bits_are_refused(lib):
     assert lib.kda_conv_bwd_workspace(most, 64, 4) == 0 and lib.kda_qk_bwd_workspace(most, 1, 0, 128) == 0
     assert lib.kda_scan_fwd_workspace(1 << 32, 1, 1, 64, 64) == 0
     assert lib.kda_scan_bwd_workspace(0, (1 << 31) - 1, 1 << 20, 1, 128, 128) == 0
+
+
+def terms_of_steps_of_both_signs(d, softplus, lengths, grads=False):
+    """What the terms of each result add up to: the recurrence on absolute values, with x given the sign of its step so
+    that d x is positive (no D, no bias)."""
+    ab = lambda n: None if d[n] is None else d[n].double().abs()  # noqa: E731
+    x = ab("x") * d["dt"].double().sign()[..., None]
+    m = ref.scan(x, d["dt"], d["A"], ab("B"), ab("C"), None, None, False, lengths, ab("h0"), ab("dout") if grads else None,
+                 ab("dhT") if grads else None)
+    return {k: v.abs() for k, v in m.items()}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lengths,N", [([600], 128), ([90, 41], 128), ([300, 70], 64)])
+def test_scan_steps_below_zero_among_steep_ones(lib, monkeypatch, lengths, N):
+    """Every third step is below zero (its decay is up to e^0.8), in blocks whose decay is far below 2^-60."""
+    import test_scan as base
+    monkeypatch.setattr(base, "mags", terms_of_steps_of_both_signs)
+    d = base.make(lengths, 4, 2, 64, N, seed=N)
+    d["bias"] = d["D"] = None
+    d["dt"] = 0.2 + d["dt"].abs()
+    d["dt"][1::3] *= -0.04
+    d["A"] = -(1 + 7 * torch.arange(4) / 3)
+    out, hT = base.call_fwd(d, lengths, False, final_state_dtype=torch.float32)
+    base.check_fwd(d, lengths, False, out, hT)
+    base.check_bwd(d, lengths, False, base.call_bwd(d, lengths, False))
+    assert kda.device_error() == 0
