@@ -433,7 +433,8 @@ kda_status kda_qk_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_
  *            initial_state (in place).
  * head_dim and state_dim are 64 or 128; num_heads a multiple of num_groups. States are carried in fp32. The
  * tokens are taken up to 128 at a time: a NaN or infinity in x, B or C can reach outputs up to 127 tokens before
- * its own, of the same sequence and group.
+ * its own, of the same sequence and group. One in A, D, dt or dt_bias makes NaN or infinities of what depends on it, and of no other
+ * output.
  *
  * Long sequences of few heads are cut into pieces that run at once (as in kda_fwd_segmented, but a
  * scalar decay needs no second run for a transition matrix); their states go to `workspace`,

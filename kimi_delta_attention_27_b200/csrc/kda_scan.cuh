@@ -11,7 +11,6 @@ constexpr int PC = 64;            // head channels per CTA (the columns of the s
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2eHi = 1.44269502f, kLog2eLo = static_cast<float>(1.4426950408889634 - 1.44269502162933349609375);
 constexpr float kMinLog2 = -1442.695f;   // log2(e^-1000)
-constexpr float kMinLog = -1000.f;
 
 __device__ __forceinline__ float ex2(float y) {
     float r;
@@ -54,10 +53,11 @@ __device__ __forceinline__ Two scan_lanes(Two v) {
     return v;
 }
 // log2 of a step's decay, d A log2(e). A step whose decay is below e^-1000 leaves nothing of the state even in
-// 64 bits; the floor keeps the sums exact enough where one step of a tile decays by 10^30.
+// 64 bits; the floor keeps the sums exact enough where one step of a tile decays by 10^30. Only numbers below it are
+// replaced: a NaN, of A or of the step, stays one.
 __device__ __forceinline__ Two log_decay(float d, Two a2) {
     const float hi = d * a2.hi, lo = fmaf(d, a2.hi, -hi) + d * a2.lo;
-    return hi > kMinLog2 ? Two{hi, lo} : Two{kMinLog2, 0.f};
+    return hi <= kMinLog2 ? Two{kMinLog2, 0.f} : Two{hi, lo};
 }
 // A log2(e) to two floats
 __device__ __forceinline__ Two log2_rate(float A) {
@@ -77,10 +77,12 @@ struct Gates {
     float pad[3];
 };
 
-// By one warp: lane l has tokens 2l and 2l + 1 (steps d0, d1; 0 behind the tile's last token).
-__device__ __forceinline__ void make_gates(Gates &g, float d0, float d1, float A) {
+// By one warp: lane l has tokens 2l and 2l + 1 of cnt (steps d0, d1; 0 behind the tile's last token, where nothing
+// decays whatever A is).
+__device__ __forceinline__ void make_gates(Gates &g, float d0, float d1, int cnt, float A) {
     const int lane = threadIdx.x & 31;
-    const Two a2 = log2_rate(A), l0 = log_decay(d0, a2), l1 = log_decay(d1, a2);
+    const Two a2 = log2_rate(A), none = {0.f, 0.f};
+    const Two l0 = 2 * lane < cnt ? log_decay(d0, a2) : none, l1 = 2 * lane + 1 < cnt ? log_decay(d1, a2) : none;
     const Two s = scan_lanes(l0 + l1), total = shfl(s, 31);
     // through the lane's first token: the sum through the lane before, and its own
     const Two before = {__shfl_up_sync(0xffffffffu, s.hi, 1), __shfl_up_sync(0xffffffffu, s.lo, 1)};

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kFp32 ? 256 : 128) scan_decode_kernel(ScanDeco
     }
     float u;
     const float d = step_of(p.dt[bh], p.dt_bias ? p.dt_bias[h] : 0.f, p.softplus, &u);
-    const float a = expf(fmaxf(d * p.A[h], kMinLog));
+    const float a = expf(d * p.A[h]);
     float xd[E], y[E];
     const uint16_t *x = p.x + b * p.x_stride + static_cast<int64_t>(h) * P;
 #pragma unroll

@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p, int64_t s
         publish();
         if (rb == 0) {
             load_steps(p, tile_start(u, c_first), tile_count(u, c_first), h, d0, d1);
-            make_gates(gates[c_first & 1], d0, d1, A);
+            make_gates(gates[c_first & 1], d0, d1, tile_count(u, c_first), A);
             if (c_first + 1 < c_end) load_steps(p, tile_start(u, c_first + 1), tile_count(u, c_first + 1), h, d0, d1);
         }
     }
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(NT, 2) scan_fwd_kernel(ScanParams p, int64_t s
         __syncthreads();   // the tile, its gates and the state's copy are there; the other stage is free
         if (c + 1 < c_end) fetch(c + 1, stage ^ 1);
         if (rb == 0 && c + 1 < c_end) {
-            make_gates(gates[(c + 1) & 1], d0, d1, A);
+            make_gates(gates[(c + 1) & 1], d0, d1, tile_count(u, c + 1), A);
             if (c + 2 < c_end) load_steps(p, tile_start(u, c + 2), tile_count(u, c + 2), h, d0, d1);
         }
         const Gates &g = gates[c & 1];

@@ -108,14 +108,16 @@ __device__ __forceinline__ void make_tc_gates(TcGates &g, const float (&dt)[4], 
     for (int j = 0; j < 4; ++j) {
         float u;
         d[j] = 4 * lane + j < cnt ? step_of(dt[j], bias, softplus, &u) : 0.f;
-        c[j] = log_decay(d[j], a2);
+        c[j] = 4 * lane + j < cnt ? log_decay(d[j], a2) : Two{0.f, 0.f};
         if (j) c[j] = c[j - 1] + c[j];
     }
     const Two s = scan_lanes(c[3]), total = shfl(s, 31);
     Two before = {__shfl_up_sync(0xffffffffu, s.hi, 1), __shfl_up_sync(0xffffffffu, s.lo, 1)};
     if (lane == 0) before = {0.f, 0.f};
     const Two anchor = shfl(s, lane | 7), opens = shfl(before, lane & 24);   // the block's end and start
-    float hi[4], lo[4], col[4], from[4], weight[4], span = fabsf(minus(opens, anchor));
+    float hi[4], lo[4], col[4], from[4], weight[4];
+    const float whole = minus(opens, anchor);
+    float span = fabsf(whole);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const Two v = before + c[j];
@@ -127,7 +129,8 @@ __device__ __forceinline__ void make_tc_gates(TcGates &g, const float (&dt)[4], 
         from[j] = ex2(v);
         weight[j] = d[j] * ex2(minus(total, v));
     }
-    const unsigned steep = __ballot_sync(0xffffffffu, span > 60.f);   // by eight lanes of a block each
+    // by eight lanes of a block each; a NaN counts, for it must not reach the tokens before it
+    const unsigned steep = __ballot_sync(0xffffffffu, span > 60.f || isnan(whole));
     reinterpret_cast<float4 *>(g.hi)[lane] = make_float4(hi[0], hi[1], hi[2], hi[3]);
     reinterpret_cast<float4 *>(g.lo)[lane] = make_float4(lo[0], lo[1], lo[2], lo[3]);
     reinterpret_cast<float4 *>(g.d)[lane] = make_float4(d[0], d[1], d[2], d[3]);

@@ -124,14 +124,16 @@ __device__ __forceinline__ void make_head_gates(HeadGates &g, const float (&dt)[
         d[j] = step_of(dt[j], bias, softplus, &u);
         if (4 * lane + j >= cnt) d[j] = 0.f;
         slope[j] = softplus ? 1.f / (1.f + expf(-u)) : 1.f;
-        c[j] = log_decay(d[j], a2);
+        c[j] = 4 * lane + j < cnt ? log_decay(d[j], a2) : Two{0.f, 0.f};
         if (j) c[j] = c[j - 1] + c[j];
     }
     const Two s = scan_lanes(c[3]), total = shfl(s, 31);
     Two before = {__shfl_up_sync(0xffffffffu, s.hi, 1), __shfl_up_sync(0xffffffffu, s.lo, 1)};
     if (lane == 0) before = {0.f, 0.f};
     const Two opens = shfl(before, lane & 24), closes = shfl(s, lane | 7);   // the quarter's start and end
-    float hi[4], lo[4], from[4], to[4], col[4], span = fabsf(minus(opens, closes));
+    float hi[4], lo[4], from[4], to[4], col[4];
+    const float whole = minus(opens, closes);
+    float span = fabsf(whole);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const Two v = before + c[j];
@@ -143,7 +145,8 @@ __device__ __forceinline__ void make_head_gates(HeadGates &g, const float (&dt)[
         span = fmaxf(span, fabsf(from_start));
         col[j] = ex2(from_start);
     }
-    const unsigned steep = __ballot_sync(0xffffffffu, span > 60.f);   // by eight lanes of a quarter each
+    // by eight lanes of a quarter each; a NaN counts, for it must reach no token that does not depend on it
+    const unsigned steep = __ballot_sync(0xffffffffu, span > 60.f || isnan(whole));
     auto put = [&](float *dst, float a, float b, float e, float f) {
         reinterpret_cast<float4 *>(dst)[lane] = make_float4(a, b, e, f);
     };

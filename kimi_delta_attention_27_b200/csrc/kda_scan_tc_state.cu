@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(NT, 1)
                 for (int j = 0; j < 4; ++j) {
                     float arg;
                     d[j] = t4 + j < cnt ? step_of(dt[j], bias, p.softplus, &arg) : 0.f;
-                    c[j] = log_decay(d[j], rate);
+                    c[j] = t4 + j < cnt ? log_decay(d[j], rate) : Two{0.f, 0.f};
                     if (j) c[j] = c[j - 1] + c[j];
                 }
                 if (i + 2 < tiles) steps(i + 2);

@@ -105,3 +105,102 @@ def test_scan_steps_below_zero_among_steep_ones(lib, monkeypatch, lengths, N):
     base.check_fwd(d, lengths, False, out, hT)
     base.check_bwd(d, lengths, False, base.call_bwd(d, lengths, False))
     assert kda.device_error() == 0
+
+
+# lengths, H, G, state size: the tcgen05 kernel whole and in pieces, the warp-level one whole and in pieces
+SCANS = {"tc": ([300, 290, 310] * 4, 32, 4, 128), "tc_pieces": ([900, 700], 4, 2, 128), "warp": ([70, 64, 1], 4, 2, 128),
+         "small_state": ([130, 5], 4, 2, 64), "small_state_pieces": ([2000, 90], 4, 2, 64)}
+
+
+def lost(got, want):
+    """Values that are not finite in the reference and are in the result."""
+    return int((torch.isfinite(got.detach().cpu()) & ~torch.isfinite(want)).sum())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", list(SCANS))
+def test_scan_nan_rate_of_one_head(lib, name):
+    """A NaN in one head's A: NaN in all that the 64-bit recurrence makes NaN of; the other heads bit for bit as without."""
+    import test_scan as base
+    lengths, H, G, N = SCANS[name]
+    assert (kda.scan_workspace_bytes(sum(lengths), len(lengths), H, 64, N) > 0) == name.endswith("pieces")
+    d = base.make(lengths, H, G, 64, N, seed=3)
+    e = dict(d, A=d["A"].clone())
+    bad, rest = 1, [h for h in range(H) if h != 1]
+    e["A"][bad] = NAN
+    r = ref.scan(e["x"], e["dt"], e["A"], e["B"], e["C"], e["D"], e["bias"], True, lengths, e["h0"], e["dout"], e["dhT"])
+    for dtype in (torch.float32, None):
+        f = dict(e, h0=e["h0"] if dtype else None)
+        out, hT = base.call_fwd(f, lengths, final_state_dtype=dtype)
+        want, wT = base.call_fwd(dict(f, A=d["A"]), lengths, final_state_dtype=dtype)
+        assert lost(out[0], r["out"]) == 0 and torch.equal(out[:, :, rest], want[:, :, rest])
+        assert dtype is None or (lost(hT, r["state"]) == 0 and torch.equal(hT[:, rest], wT[:, rest]))
+    got, want = base.call_bwd(e, lengths), base.call_bwd(d, lengths)
+    for k in ("dx", "dB", "dC", "ddt", "dA", "ddt_bias", "dh0"):
+        g = got[k][0] if k in ("dx", "dB", "dC", "ddt") else got[k]
+        assert lost(g, r[k]) == 0 and not bool(torch.isfinite(g).all()), k
+    for k, at in (("dx", 2), ("ddt", 2), ("dA", 0), ("ddt_bias", 0), ("dh0", 1)):
+        pick = torch.tensor(rest, device="cuda")
+        assert torch.equal(got[k].index_select(at, pick), want[k].index_select(at, pick)), k
+    for k in ("dB", "dC"):
+        assert torch.equal(got[k][:, :, 1:], want[k][:, :, 1:]), k
+    assert torch.equal(got["dD"], want["dD"]) and kda.device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", list(SCANS))
+def test_scan_nan_step_of_one_token(lib, name):
+    """A NaN in one token's dt reaches every later output of its head and sequence, no earlier one, and no other sequence."""
+    import test_scan as base
+    lengths, H, G, N = SCANS[name]
+    d = base.make(lengths, H, G, 64, N, seed=4)
+    want, _ = base.call_fwd(d, lengths, final_state_dtype=torch.float32)
+    t, h = 33, 2
+    d["dt"][t, h] = NAN
+    r = ref.scan(d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], d["bias"], True, lengths, d["h0"], d["dout"], d["dhT"])
+    out, hT = base.call_fwd(d, lengths, final_state_dtype=torch.float32)
+    assert torch.equal(torch.isnan(out[0]).cpu(), torch.isnan(r["out"]))
+    assert torch.equal(torch.isnan(hT).cpu(), torch.isnan(r["state"]))
+    assert torch.equal(out[0, lengths[0]:], want[0, lengths[0]:])
+    got = base.call_bwd(d, lengths)
+    for k in ("dx", "dB", "dC", "ddt", "dA", "ddt_bias", "dh0"):
+        g = got[k][0] if k in ("dx", "dB", "dC", "ddt") else got[k]
+        assert lost(g, r[k]) == 0, k
+    assert bool(torch.isfinite(got["dx"][0, lengths[0]:]).all()) and bool(torch.isfinite(got["dh0"][1:]).all())
+    assert kda.device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", list(SCANS))
+def test_scan_rate_of_minus_infinity_forgets_everything(lib, name):
+    """The same as a rate of -1e30, in partly filled tiles too."""
+    import test_scan as base
+    lengths, H, G, N = SCANS[name]
+    d = base.make(lengths, H, G, 64, N, seed=5)
+    res = []
+    for a in (-1e30, -INF):
+        d["A"][1] = a
+        res.append(base.call_fwd(d, lengths, final_state_dtype=torch.float32))
+    assert bool(torch.isfinite(res[0][0]).all()) and bool(torch.isfinite(res[0][1]).all())
+    assert all(torch.equal(a, b) for a, b in zip(*res)) and kda.device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("state", [torch.float32, BF])
+@pytest.mark.parametrize("N", [64, 128])
+def test_scan_decode_nan_rate_and_step(lib, N, state):
+    import test_scan as base
+    d = base.make([1] * 5, 4, 2, 64, N, seed=N, state=state)
+    kw = dict(D=base.dev(d["D"]), dt_bias=base.dev(d["bias"]), dt_softplus=True)
+
+    def call(d):
+        S = base.dev(d["h0"]).clone()
+        return kda.kda_scan_decode(*(base.dev(d[k]) for k in ("x", "dt", "A", "B", "C")), S, S, **kw)
+
+    want, wS = call(d)
+    e = dict(d, A=d["A"].clone(), dt=d["dt"].clone())
+    e["A"][1], e["dt"][3, 2] = NAN, NAN
+    r = ref.scan(e["x"], e["dt"], e["A"], e["B"], e["C"], e["D"], e["bias"], True, [1] * 5, e["h0"])
+    out, S = call(e)
+    assert torch.equal(torch.isnan(out).cpu(), torch.isnan(r["out"])) and torch.equal(torch.isnan(S).cpu(), torch.isnan(r["state"]))
+    assert torch.equal(out[:, [0, 3]], want[:, [0, 3]]) and torch.equal(S[:, [0, 3]], wS[:, [0, 3]])
