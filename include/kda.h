@@ -380,8 +380,10 @@ kda_status kda_conv_decode(const void *x, kda_dtype dtype, int64_t x_stride, con
  *                  r = (mean x^2 + eps)^(-1/2)  KDA_NORM_RMS,     r = 1   KDA_NORM_NONE,
  *     pairs (z_a, z_b) of the first rot_dim channels -> factor (z_a cos - z_b sin, z_b cos + z_a sin),
  * pair i being channels (2 i, 2 i + 1) if `interleaved`, else (i, i + rot_dim / 2), and its angle
- * positions[row] * inv_freq[i], formed and reduced in 64 bits. Any scaling for long contexts is in the caller's
- * inv_freq and factor. A zero vector with eps == 0 stays zero.
+ * positions[row] * inv_freq[i], formed and reduced in 64 bits (a NaN or infinite inv_freq[i] makes NaN of its pair at
+ * every position). Any scaling for long contexts is in the caller's inv_freq and factor. A zero vector with eps == 0
+ * stays zero. The sum of squares is fp32: heads with channels beyond 10^18 (it can overflow, and they then come out
+ * as zeros), or with eps == 0 and no channel above 10^-18 (it loses bits, then all), are not in its range.
  *
  *   q, q_out : bf16 [rows, q_heads, head_dim] (rows strided); k, k_out: [rows, k_heads, head_dim] (k_heads may
  *              be 0). q_out may be q, and k_out k, with the same stride (in place).

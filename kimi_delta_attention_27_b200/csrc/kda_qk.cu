@@ -98,13 +98,16 @@ __device__ __forceinline__ Pairs weights(const float *w, const Place &q) {
 struct Freq {
     uint64_t f[4];
 };
+// in the place of a frequency that is not finite: the 53 bits of an fp64 fraction of a turn leave the low bits of one
+// from a half on 0, so no finite frequency has this value
+constexpr uint64_t kNoFreq = (uint64_t(1) << 63) | 1;
 __device__ __forceinline__ void make_freq(const QkParams &p, int l, const Place &q, Freq &r) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         r.f[j] = 0;
         if (q.turned) {
             const double turns = static_cast<double>(p.inv_freq[4 * l + j]) * 0.15915494309189533577;
-            r.f[j] = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+            r.f[j] = isfinite(turns) ? __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0) : kNoFreq;
         }
     }
 }
@@ -128,6 +131,7 @@ __device__ __forceinline__ void make_turn(const QkParams &p, int64_t row, const 
             sincospif(static_cast<float>(top) * 0x1p-31f, &s[j], &c[j]);
             c[j] *= p.factor;
             s[j] *= sign * p.factor;
+            if (r.f[j] == kNoFreq) c[j] = s[j] = __int_as_float(0x7fffffff);   // a NaN at every position
         }
     }
     t.c[0] = make_float2(c[0], c[1]);

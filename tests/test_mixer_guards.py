@@ -204,3 +204,29 @@ def test_scan_decode_nan_rate_and_step(lib, N, state):
     out, S = call(e)
     assert torch.equal(torch.isnan(out).cpu(), torch.isnan(r["out"])) and torch.equal(torch.isnan(S).cpu(), torch.isnan(r["state"]))
     assert torch.equal(out[:, [0, 3]], want[:, [0, 3]]) and torch.equal(S[:, [0, 3]], wS[:, [0, 3]])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rot,norm", [(128, 64, "l2"), (64, 64, "none"), (256, 112, "rms")])
+def test_qk_frequencies_that_are_not_finite(lib, D, rot, norm, interleaved):
+    """NaN in their pairs, as the 64-bit form has it (and through the norm in a head's whole gradient); the other pairs bit
+    for bit as without."""
+    T, H = 21, 3
+    g = torch.Generator().manual_seed(D)
+    q, dy = torch.randn(1, T, H, D, generator=g).to(BF), torch.randn(1, T, H, D, generator=g).to(BF)
+    pos = torch.arange(T, dtype=torch.int32)[None]
+    f = torch.rand(rot // 2, generator=g)
+    bad = f.clone()
+    bad[0], bad[5], bad[rot // 2 - 1] = NAN, INF, -INF
+    x = q[0].to(ref.F64).requires_grad_()
+    y = ref.qk(x, None, norm, 1e-6, pos[0], bad, interleaved, 1.0)
+    dx, = torch.autograd.grad(y, x, dy[0].to(ref.F64))
+    opt = dict(norm=norm, positions=pos.cuda(), interleaved=interleaved)
+    got, _ = kda.kda_qk_fwd(q.cuda(), inv_freq=bad.cuda(), **opt)
+    clean, _ = kda.kda_qk_fwd(q.cuda(), inv_freq=f.cuda(), **opt)
+    nan = torch.isnan(y)
+    assert torch.equal(torch.isnan(got[0]).cpu(), nan) and bool(nan.any()) and torch.equal(got[0].cpu()[~nan], clean[0].cpu()[~nan])
+    got = kda.kda_qk_bwd(q.cuda(), None, dy.cuda(), None, inv_freq=bad.cuda(), **opt)["dq"][0].cpu()
+    clean = kda.kda_qk_bwd(q.cuda(), None, dy.cuda(), None, inv_freq=f.cuda(), **opt)["dq"][0].cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(dx)) and torch.equal(got[~torch.isnan(dx)], clean[~torch.isnan(dx)])
