@@ -506,8 +506,10 @@ def _stream_of(dev, stream):
     here = raw(dev.index) if raw else torch.cuda.current_stream(dev).cuda_stream
     handle = here if stream is None else int(stream)
     if handle != here:
+        # handle 0 is the default stream, of which ExternalStream(0) would make one of torch's pool;
         # torch.cuda.stream makes the stream's device current, too
-        return handle, torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev))
+        other = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+        return handle, torch.cuda.stream(other)
     return handle, _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 

@@ -230,3 +230,37 @@ def test_qk_frequencies_that_are_not_finite(lib, D, rot, norm, interleaved):
     got = kda.kda_qk_bwd(q.cuda(), None, dy.cuda(), None, inv_freq=bad.cuda(), **opt)["dq"][0].cpu()
     clean = kda.kda_qk_bwd(q.cuda(), None, dy.cuda(), None, inv_freq=f.cuda(), **opt)["dq"][0].cpu()
     assert torch.equal(torch.isnan(got), torch.isnan(dx)) and torch.equal(got[~torch.isnan(dx)], clean[~torch.isnan(dx)])
+
+
+@pytest.mark.gpu
+def test_what_a_call_allocates_belongs_to_the_stream_it_is_given(lib, monkeypatch):
+    """Outputs and workspaces too, and for the default stream's handle, which is 0, while another stream is current: else
+    their memory could be given out again while the kernels on the default stream still use it."""
+    seen = []
+    for name in ("empty", "empty_like"):
+        real = getattr(torch, name)
+
+        def noted(*a, real=real, **k):
+            seen.append(torch.cuda.current_stream().cuda_stream)
+            return real(*a, **k)
+        monkeypatch.setattr(torch, name, noted)
+    x, w = torch.ones(1, 9, 16, dtype=BF, device="cuda"), torch.ones(16, 4, device="cuda")
+    q = torch.ones(1, 9, 2, 64, dtype=BF, device="cuda")
+    dt, A, B = torch.ones(1, 9, 2, device="cuda"), -torch.ones(2, device="cuda"), torch.ones(1, 9, 1, 64, dtype=BF, device="cuda")
+    calls = (lambda s: kda.kda_conv_fwd(x, w, want_final_state=True, stream=s), lambda s: kda.kda_conv_bwd(x, w, x, stream=s),
+             lambda s: kda.kda_conv_decode(x[0], w, stream=s), lambda s: kda.kda_qk_fwd(q, q, stream=s),
+             lambda s: kda.kda_qk_bwd(q, None, q, None, q_weight=torch.ones(64, device="cuda"), stream=s),
+             lambda s: kda.kda_scan_fwd(q, dt, A, B, B, final_state_dtype=torch.float32, stream=s),
+             lambda s: kda.kda_scan_bwd(q, dt, A, B, B, q, stream=s),
+             lambda s: kda.kda_scan_decode(q[0], dt[0], A, B[0], B[0], state_dtype=torch.float32, stream=s))
+    side, third = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for given, want in ((None, side.cuda_stream), (0, 0), (third.cuda_stream, third.cuda_stream)):
+        for call in calls:
+            with torch.cuda.stream(side):
+                seen.clear()
+                call(given)
+                assert seen and set(seen) == {want}, (given, seen)
+                assert torch.cuda.current_stream() == side
+        torch.cuda.synchronize()
+    assert kda.device_error() == 0
