@@ -247,18 +247,17 @@ def _fwd(entry, q, k, v, g, beta, scale, cu_seqlens, initial_state, final_state,
         _check("final_state", final_state, None, shape=state_shape)
     dev = _check_devices(q=q, k=k, v=v, g=g, beta=beta, cu_seqlens=cu_seqlens, initial_state=initial_state,
                          out=out, final_state=final_state)
-    if out is None:
-        out = torch.empty((B, T, H, Dv), dtype=torch.bfloat16, device=dev)
-    if final_state is None and final_state_dtype is not None:
-        final_state = torch.empty(state_shape, dtype=final_state_dtype, device=dev)
     if scale is None:
         scale = Dk ** -0.5
-    if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
     lib = load_library()
-    ic, fc = _dtype_code(initial_state), _dtype_code(final_state)
     # the library works on the current device: make it q's
-    with torch.cuda.device(dev):
+    stream, ctx = _stream_of(dev, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty((B, T, H, Dv), dtype=torch.bfloat16, device=dev)
+        if final_state is None and final_state_dtype is not None:
+            final_state = torch.empty(state_shape, dtype=final_state_dtype, device=dev)
+        ic, fc = _dtype_code(initial_state), _dtype_code(final_state)
         if entry == "kda_fwd_ex":
             st = lib.kda_fwd_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(g), int(gate_kind), _ptr(beta), float(scale),
                                 _ptr(cu_seqlens), int(N), int(B), int(T), int(H), int(Dk), int(Dv),
@@ -304,18 +303,17 @@ def kda_fwd_segmented(q, k, v, g, beta, segment_len: int, scale: float | None = 
         _check("workspace", workspace, torch.uint8, 1)
     dev = _check_devices(q=q, k=k, v=v, g=g, beta=beta, initial_state=initial_state, out=out,
                          final_state=final_state, workspace=workspace)
-    if out is None:
-        out = torch.empty((B, T, H, Dv), dtype=torch.bfloat16, device=dev)
-    if final_state is None and final_state_dtype is not None:
-        final_state = torch.empty(state_shape, dtype=final_state_dtype, device=dev)
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     if scale is None:
         scale = Dk ** -0.5
-    if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
-    ic, fc = _dtype_code(initial_state), _dtype_code(final_state)
-    with torch.cuda.device(dev):
+    stream, ctx = _stream_of(dev, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty((B, T, H, Dv), dtype=torch.bfloat16, device=dev)
+        if final_state is None and final_state_dtype is not None:
+            final_state = torch.empty(state_shape, dtype=final_state_dtype, device=dev)
+        if workspace is None:
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        ic, fc = _dtype_code(initial_state), _dtype_code(final_state)
         st = lib.kda_fwd_segmented(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), int(B), int(T),
                                    int(H), int(Dk), int(Dv), _ptr(initial_state), ic if ic >= 0 else 99,
                                    _ptr(final_state), fc if fc >= 0 else 99, _ptr(out), int(segment_len),
@@ -359,19 +357,18 @@ def kda_bwd(q, k, v, g, beta, dout, scale: float | None = None, cu_seqlens=None,
                          initial_state=initial_state, dfinal_state=dfinal_state, workspace=workspace)
     lib = load_library()
     rows = T if cu_seqlens is not None else B * T
-    if workspace is None:
-        workspace = torch.empty(max(1, int(lib.kda_bwd_workspace(int(rows), int(N), int(H)))),
-                                dtype=torch.uint8, device=dev)
-    out = {n: torch.empty((B, T, H, Dk if n != "dv" else Dv), dtype=torch.float32, device=dev)
-           for n in ("dq", "dk", "dv", "dg")}
-    out["dbeta"] = torch.empty((B, T, H), dtype=torch.float32, device=dev)
-    out["dh0"] = torch.empty(state_shape, dtype=torch.float32, device=dev) if want_dinitial_state else None
     if scale is None:
         scale = Dk ** -0.5
-    if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
+    stream, ctx = _stream_of(dev, stream)
     ic = _dtype_code(initial_state)
-    with torch.cuda.device(dev):
+    with ctx:
+        if workspace is None:
+            workspace = torch.empty(max(1, int(lib.kda_bwd_workspace(int(rows), int(N), int(H)))),
+                                    dtype=torch.uint8, device=dev)
+        out = {n: torch.empty((B, T, H, Dk if n != "dv" else Dv), dtype=torch.float32, device=dev)
+               for n in ("dq", "dk", "dv", "dg")}
+        out["dbeta"] = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+        out["dh0"] = torch.empty(state_shape, dtype=torch.float32, device=dev) if want_dinitial_state else None
         st = lib.kda_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), _ptr(cu_seqlens), int(N),
                          int(B), int(T), int(H), int(Dk), int(Dv), _ptr(initial_state), ic if ic >= 0 else 99,
                          _ptr(dout), _ptr(dfinal_state), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
@@ -419,20 +416,20 @@ def kda_decode(q, k, v, g, beta, state_in=None, state_out=None, scale: float | N
     if out is not None:
         _check("out", out, torch.bfloat16, shape=(B, H, Dv))
     dev = _check_devices(q=q, k=k, v=v, g=g, beta=beta, state_in=state_in, state_out=state_out, out=out)
-    if state_out is None and state_dtype is not None:
-        state_out = torch.empty(state_shape, dtype=state_dtype, device=dev)
-    if state_in is not None and state_out is not None and state_in.dtype != state_out.dtype:
+    kept = state_dtype if state_out is None else state_out.dtype
+    if state_in is not None and kept is not None and state_in.dtype != kept:
         raise ValueError("state_in and state_out must have the same dtype")
-    st_t = state_in if state_in is not None else state_out
-    code = _dtype_code(st_t)
-    if out is None:
-        out = torch.empty((B, H, Dv), dtype=torch.bfloat16, device=dev)
     if scale is None:
         scale = Dk ** -0.5
-    if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
     lib = load_library()
-    with torch.cuda.device(dev):
+    stream, ctx = _stream_of(dev, stream)
+    with ctx:
+        if state_out is None and state_dtype is not None:
+            state_out = torch.empty(state_shape, dtype=state_dtype, device=dev)
+        if out is None:
+            out = torch.empty((B, H, Dv), dtype=torch.bfloat16, device=dev)
+        st_t = state_in if state_in is not None else state_out
+        code = _dtype_code(st_t)
         st = lib.kda_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), int(B), int(H),
                             int(Dk), int(Dv), _ptr(state_in), _ptr(state_out), code if code >= 0 else 99,
                             _ptr(out), ctypes.c_void_p(int(stream)))

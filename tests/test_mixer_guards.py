@@ -264,3 +264,37 @@ def test_what_a_call_allocates_belongs_to_the_stream_it_is_given(lib, monkeypatc
                 assert torch.cuda.current_stream() == side
         torch.cuda.synchronize()
     assert kda.device_error() == 0
+
+
+@pytest.mark.gpu
+def test_what_the_recurrence_allocates_belongs_to_the_stream_it_is_given(lib, monkeypatch):
+    """The same of kda_fwd, kda_fwd_segmented, kda_bwd and kda_decode."""
+    from kimi_delta_attention_27_b200.inputs import make_inputs
+    inp = make_inputs({"B": 1, "T": 128, "H": 1, "lengths": None, "g_mu": 3.0, "init": None, "final": "fp32", "seed": 8},
+                      device="cuda")
+    args = [inp[k] for k in ("q", "k", "v", "g", "beta")]
+    one = [t[:, 0].contiguous() for t in args]
+    seen, real = [], torch.empty
+
+    def noted(*a, **k):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        return real(*a, **k)
+    monkeypatch.setattr(torch, "empty", noted)
+    f32 = torch.float32
+    calls = (lambda s: kda.kda_fwd(*args, final_state_dtype=f32, stream=s), lambda s: kda.kda_bwd(*args, inp["v"], stream=s),
+             lambda s: kda.kda_fwd_segmented(*args, segment_len=64, final_state_dtype=f32, stream=s),
+             lambda s: kda.kda_decode(*one, state_dtype=f32, stream=s))
+    side, third = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    want = [c(None) for c in calls]
+    torch.cuda.synchronize()
+    for given, handle in ((None, side.cuda_stream), (0, 0), (third.cuda_stream, third.cuda_stream)):
+        for call, w in zip(calls, want):
+            with torch.cuda.stream(side):
+                seen.clear()
+                got = call(given)
+                assert seen and set(seen) == {handle}, (given, seen)
+            torch.cuda.synchronize()
+            pairs = zip(w.values(), got.values()) if isinstance(w, dict) else zip(w, got)
+            assert all(a is b or torch.allclose(a.float(), b.float(), rtol=1e-3, atol=1e-3) for a, b in pairs)
+    assert kda.device_error() == 0
