@@ -383,14 +383,17 @@ __global__ void __launch_bounds__(256) scan_join_kernel(ScanParams p, int64_t se
 // are cut where equal ones fill less than half of the slots, and packed ones, of which the longest is taken to be twice
 // the mean, fewer than all. (4096 tokens x 64 heads x 64: 2 sequences, 64 CTAs, 176 us whole, 181 cut; 3 sequences 181
 // and 231. One of 65536 tokens x 32 heads x 128, 32 CTAs: 2.62 ms whole, 0.86 cut. 2 packed ones, 13493
-// tokens x 64 heads x 64, 64 CTAs: 286 and 244.)
-int64_t piece_tokens(int64_t rows, int64_t n, bool packed, int64_t ctas, int slots, int tile) {
+// tokens x 64 heads x 64, 64 CTAs: 286 and 244.) And only where the longest makes two pieces and has `least` tokens:
+// below that the launches cost more than the pieces save. (32 heads x 64, state size 128, us whole and cut: 2 rows of 200
+// tokens 25 and 41, of 400 33 and 45, of 600 43 and 46, of 800 49 and 43; state size 64: 21 and 31, 31 and 33, 41 and 37,
+// 51 and 37.)
+int64_t piece_tokens(int64_t rows, int64_t n, bool packed, int64_t ctas, int slots, int tile, int64_t least) {
     if (n == 0 || (packed ? 1 : 2) * n * ctas >= slots) return 0;
-    const int64_t want = 2 * slots;
+    const int64_t want = 2 * slots, longest = packed && n > 1 ? 2 * rows / n : rows / n;
     int64_t seg = (rows * ctas + want - 1) / want;
     seg = (seg + tile - 1) / tile * tile;
     if (seg < 256) seg = 256;
-    return seg >= rows ? 0 : seg;
+    return longest < 2 * seg || longest < least ? 0 : seg;
 }
 // State size 128: the tcgen05 kernel takes sequences of more than 160 tokens on average, or, where the CTAs of the
 // warp-level one fit the SMs at once, of more than 256: a first tile takes it some 3 us longer. (16 sequences x 64 heads:
@@ -400,14 +403,16 @@ bool takes_tc(int64_t rows, int64_t n, int64_t columns, int32_t N) {
 }
 int64_t fwd_piece_tokens(int64_t rows, int64_t n, bool packed, int32_t H, int32_t P, int32_t N) {
     const int64_t columns = static_cast<int64_t>(H) * (P / PC);
-    return takes_tc(rows, n, columns, N) ? piece_tokens(rows, n, packed, (columns + 1) / 2, 148, kScanTcTile)
-                                         : piece_tokens(rows, n, packed, columns, 2 * 148, T);
+    return takes_tc(rows, n, columns, N) ? piece_tokens(rows, n, packed, (columns + 1) / 2, 148, kScanTcTile, 512)
+                                         : piece_tokens(rows, n, packed, columns, 2 * 148, T, 512);
 }
-// The backward's runs of the state, both directions at once; their tiles take so little that packed sequences, too, are cut only below half of the slots (the gradients of 2 packed ones, 13493 tokens x 64 heads,
-// with tiles of 64 tokens: 656 us whole, 827 cut).
-int64_t state_piece_tokens(int64_t rows, int64_t n, int32_t H, int32_t P) {
-    const int64_t columns = static_cast<int64_t>(H) * (P / PC);
-    return piece_tokens(rows, n, false, (columns + 1) / 2 * 2, 148, kScanTcTile);
+// The backward's runs of the state, both directions at once; their tiles take so little that packed sequences, too, are
+// cut only below half of the slots (the gradients of 2 packed ones, 13493 tokens x 64 heads, with tiles of 64 tokens: 656
+// us whole, 827 cut), and from 1024 tokens on (8 heads x 64, state size 128, the gradients whole and cut: 2 rows of 200
+// tokens 51 and 64 us, of 600 61 and 66, of 1200 80 and 72).
+int64_t state_piece_tokens(int64_t rows, int64_t n, bool packed, int32_t H, int32_t P) {
+    const int64_t columns = static_cast<int64_t>(H) * (P / PC), ctas = (columns + 1) / 2 * 2;
+    return 2 * n * ctas >= 148 ? 0 : piece_tokens(rows, n, packed, ctas, 148, kScanTcTile, 1024);
 }
 
 int64_t piece_count(int64_t rows, int64_t n, int64_t seg) { return seg ? rows / seg + n : n; }
@@ -433,8 +438,8 @@ size_t scan_fwd_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, i
 }
 
 size_t scan_states_workspace_bytes(int64_t rows, int64_t n, int32_t H, int32_t P, int32_t N) {
-    // both directions' pieces
-    return 2 * scan::piece_bytes(rows, n, scan::state_piece_tokens(rows, n, H, P), H, P, N);
+    // both directions' pieces; the larger need again
+    return 2 * scan::piece_bytes(rows, n, scan::state_piece_tokens(rows, n, true, H, P), H, P, N);
 }
 
 template <int N>
@@ -465,7 +470,7 @@ cudaError_t launch_scan_fwd(const ScanParams &p, cudaStream_t s) {
 
 cudaError_t launch_scan_states(const ScanParams &p, float *states, float *grads, float *ws, cudaStream_t s) {
     using namespace scan;
-    const int64_t cut = state_piece_tokens(p.rows, p.seqs.n, p.H, p.P), seg = cut ? cut : kWhole;
+    const int64_t cut = state_piece_tokens(p.rows, p.seqs.n, p.seqs.cu != nullptr, p.H, p.P), seg = cut ? cut : kWhole;
     const int64_t units = piece_count(p.rows, p.seqs.n, cut);
     if (units == 0) return cudaSuccess;
     if (units * p.H * (p.P / PC) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

@@ -298,3 +298,62 @@ def test_what_the_recurrence_allocates_belongs_to_the_stream_it_is_given(lib, mo
             pairs = zip(w.values(), got.values()) if isinstance(w, dict) else zip(w, got)
             assert all(a is b or torch.allclose(a.float(), b.float(), rtol=1e-3, atol=1e-3) for a, b in pairs)
     assert kda.device_error() == 0
+
+
+def test_scan_cuts_no_sequence_that_makes_no_two_pieces(lib):
+    """Several short sequences are not worth a cut: no state run, no join, no workspace. Equal rows ask for no more than
+    packed ones of the same number and length, whose need is what the query returns."""
+    need = kda.scan_workspace_bytes
+    for n, tokens in ((2, 200), (4, 200), (8, 128), (1, 400), (3, 250)):
+        for H, N in ((8, 64), (8, 128), (32, 64), (32, 128)):
+            assert need(n * tokens, n, H, 64, N) == 0 and need(n * tokens, n, H // 2, 128, N) == 0, (n, tokens, H, N)
+    for N in (64, 128):
+        assert need(65536, 1, 32, 128, N) > 0 and need(2 * 4096, 2, 8, 64, N) > 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("n,tokens,H,N", [(2, 200, 4, 128), (4, 129, 3, 64), (2, 640, 2, 128), (2, 1100, 2, 64), (1, 1030, 2, 128)])
+def test_scan_rows_below_and_above_the_cut(lib, n, tokens, H, N, packed):
+    """Equal rows, as a batch and packed, in one workspace of the size that the query gives, to its last byte."""
+    import test_scan as base
+    lengths = [tokens] * n
+    d = base.make(lengths, H, 1, 64, N, seed=tokens)
+    rows = (1, n * tokens) if packed else (n, tokens)
+    v = lambda k: base.dev(d[k]).view(*rows, *d[k].shape[1:])  # noqa: E731
+    kw = dict(D=base.dev(d["D"]), dt_bias=base.dev(d["bias"]), dt_softplus=True, initial_state=base.dev(d["h0"]),
+              cu_seqlens=base.cu_of(lengths) if packed else None)
+    args = (v("x"), v("dt"), base.dev(d["A"]), v("B"), v("C"))
+    sizes = (kda.scan_workspace_bytes(n * tokens, n, H, 64, N), lib.kda_scan_bwd_workspace(n * tokens, n, H, 1, 64, N))
+    spaces = [torch.full((s + 1024,), 165, dtype=torch.uint8, device="cuda") for s in sizes]
+    out, hT = kda.kda_scan_fwd(*args, final_state_dtype=torch.float32, workspace=spaces[0][:sizes[0]], **kw)
+    base.check_fwd(d, lengths, True, out.view(1, n * tokens, H, 64), hT)
+    g = kda.kda_scan_bwd(*args, v("dout"), dfinal_state=base.dev(d["dhT"]), workspace=spaces[1][:sizes[1]], **kw)
+    g = {k: t.view(1, n * tokens, *t.shape[2:]) if k in ("dx", "dB", "dC", "ddt") else t for k, t in g.items()}
+    base.check_bwd(d, lengths, True, g)
+    assert all(bool((w[s:] == 165).all()) for w, s in zip(spaces, sizes)) and kda.device_error() == 0
+
+
+# lengths, H, G, P; runs of 64 columns per group: 3, 2, 1, 4. Longest (twice the mean) 1024 tokens or more: the states of
+# the gradients in pieces
+CUT_BWD = {
+    "odd_runs": ([1500, 129, 1, 0, 1100], 6, 2, 64),
+    "two_runs_of_one_head": ([0, 257, 0, 2100], 1, 1, 128),
+    "one_run": ([127, 128, 2000], 2, 2, 64),
+    "four_runs": ([985, 783], 2, 1, 128),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [64, 128])
+@pytest.mark.parametrize("name", list(CUT_BWD))
+def test_scan_bwd_of_long_sequences_in_pieces(lib, name, N):
+    import test_scan as base
+    lengths, H, G, P = CUT_BWD[name]
+    d = base.make(lengths, H, G, P, N, seed=len(name), state=None if name == "one_run" else torch.float32, sharp=name == "one_run")
+    softplus = name != "four_runs"
+    if not softplus:
+        d["dt"], d["D"], d["bias"] = d["dt"].abs() * 0.2, None, None
+    g, again = base.call_bwd(d, lengths, softplus), base.call_bwd(d, lengths, softplus)
+    assert kda.device_error() == 0 and all(g[k] is None or torch.equal(g[k], again[k]) for k in g)
+    base.check_bwd(d, lengths, softplus, g)
