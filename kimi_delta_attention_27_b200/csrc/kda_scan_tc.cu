@@ -36,6 +36,11 @@ namespace scan {
 namespace tc {
 
 __device__ unsigned int g_scan_tc_error = 0;
+#ifdef KDA_TEST_HOOKS
+// Test-only build (never the product library): the gates of this tile of every CTA are not signalled, so that the bounded
+// waits for them run out.
+__device__ int g_scan_tc_stall = -1;
+#endif
 
 constexpr int TT = kScanTcTile;           // tokens per tile
 constexpr int NT = 608;                   // eight warps for each head, an issuing warp, two for the gates
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(NT, 1)
             auto finish = [&](int i) {
                 const int stage = i & 1, cnt = count_of(i);
                 uint8_t *xt = smem + L::kX + (hd * 2 + stage) * kBlock;
-                if (!x.wait(kY + hd, i & 1)) return false;
+                if (!x.met(x.wait(kY + hd, i & 1))) return false;
                 tc_fence_after();
                 const float f = gates[hd * 2 + stage].from[r];
                 const float2 f2 = make_float2(f, f), D2 = make_float2(Dh, Dh);
@@ -319,11 +324,11 @@ __global__ void __launch_bounds__(NT, 1)
                 const uint32_t ph = i & 1, ph2 = (i >> 1) & 1;
                 uint8_t *xt = smem + L::kX + (hd * 2 + stage) * kBlock;
                 const TcGates &g = gates[hd * 2 + stage];
-                ok = x.wait(kXFull + hd * 2 + stage, ph2) && x.wait(kGates + hd * 2 + stage, ph2);
+                ok = x.met(x.wait(kXFull + hd * 2 + stage, ph2) && x.wait(kGates + hd * 2 + stage, ph2));
                 if (!ok) break;
                 if (cnt < TT && hd == 0) {
                     // rows of B behind the piece: whatever they hold would multiply zeros below
-                    ok = x.wait(kBcFull, ph);
+                    ok = x.met(x.wait(kBcFull, ph));
                     if (!ok) break;
                     uint8_t *bt = smem + L::kB + hf * kBlock;
                     if (r >= cnt)
@@ -335,11 +340,11 @@ __global__ void __launch_bounds__(NT, 1)
                     ok = finish(i - 1);
                     if (!ok) break;
                 }
-                ok = x.wait(kPFree, ph);
+                ok = x.met(x.wait(kPFree, ph));
                 if (!ok) break;
                 write_parts(1, xt, g, cnt);
                 // S = e^(Gamma_end) S + U
-                ok = x.wait(kU, ph);
+                ok = x.met(x.wait(kU, ph));
                 if (!ok) break;
                 tc_fence_after();
                 {
@@ -353,7 +358,7 @@ __global__ void __launch_bounds__(NT, 1)
                 // the state's copy: C S_0 of this tile has been computed, as the product behind it has
                 if (i + 1 < tiles) publish();
                 // M = L . G d in U's place: rows r, blocks of 32 columns, two for each half
-                ok = x.wait(kG, ph);
+                ok = x.met(x.wait(kG, ph));
                 if (!ok) break;
                 tc_fence_after();
                 const float gh = g.hi[r], glo = g.lo[r];
@@ -444,9 +449,8 @@ __global__ void __launch_bounds__(NT, 1)
         if (tiles > 0) load_bc(0);
         for (int i = 0; i < tiles && ok; ++i) {
             const uint32_t ph = i & 1, bt = base + L::kB;
-            ok = x.wait(kBcFull, ph);
+            ok = x.met(x.wait(kBcFull, ph));
             if (!ok) break;
-            __syncwarp();
             {
                 // G: the last tile's has been read (its M is written)
                 tc_fence_after();
@@ -478,13 +482,13 @@ __global__ void __launch_bounds__(NT, 1)
             };
             // U takes the place of the last tile's M, which has been multiplied
             for (int hd = 0; hd < heads && ok; ++hd) ok = x.wait(kP0 + hd, ph) && (i == 0 || x.wait(kY + hd, (i - 1) & 1));
+            ok = x.met(ok);
             if (!ok) break;
-            __syncwarp();
             tc_fence_after();
             product_u(0);
             for (int hd = 0; hd < heads && ok; ++hd) ok = x.wait(kS + hd, ph) && (i == 0 || x.wait(kYFree + hd, (i - 1) & 1));
+            ok = x.met(ok);
             if (!ok) break;
-            __syncwarp();
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -494,22 +498,21 @@ __global__ void __launch_bounds__(NT, 1)
             }
             __syncwarp();
             for (int hd = 0; hd < heads && ok; ++hd) ok = x.wait(kP1 + hd, ph);
+            ok = x.met(ok);
             if (!ok) break;
-            __syncwarp();
             tc_fence_after();
             product_u(1);
             if (!ok) break;
             // the last commit covers every product so far: C and B are free
             if (i + 1 < tiles) {
-                ok = x.wait(kU, ph);
+                ok = x.met(x.wait(kU, ph));
                 if (!ok) break;
-                __syncwarp();
                 load_bc(i + 1);
                 __syncwarp();
             }
             {
                 for (int hd = 0; hd < heads && ok; ++hd) {
-                    ok = x.wait(kM + hd, ph);
+                    ok = x.met(x.wait(kM + hd, ph));
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__(NT, 1)
         if (tiles > 0) load_dt(p, start_of(0), count_of(0), h, dt);
         for (int i = 0; i < tiles; ++i) {
             const int stage = i & 1;
-            if (i >= 2) ok = x.wait(kXFree + hd * 2 + stage, ((i - 2) >> 1) & 1);
+            if (i >= 2) ok = x.met(x.wait(kXFree + hd * 2 + stage, ((i - 2) >> 1) & 1));
             if (!ok) break;
             __syncwarp();
             if (elect_one()) {
@@ -547,6 +550,9 @@ __global__ void __launch_bounds__(NT, 1)
             const float now[4] = {dt[0], dt[1], dt[2], dt[3]};
             if (i + 1 < tiles) load_dt(p, start_of(i + 1), count_of(i + 1), h, dt);
             make_tc_gates(gates[hd * 2 + stage], now, count_of(i), bias, p.softplus, rate);
+#ifdef KDA_TEST_HOOKS
+            if (i != g_scan_tc_stall)
+#endif
             x.arrive(kGates + hd * 2 + stage);
         }
     }
@@ -591,5 +597,11 @@ cudaError_t read_and_clear_scan_tc_error(unsigned int *value) {
     const unsigned int zero = 0;
     return cudaMemcpyToSymbol(scan::tc::g_scan_tc_error, &zero, sizeof(zero));
 }
+
+#ifdef KDA_TEST_HOOKS
+extern "C" int kda_test_set_scan_tc_stall(int at) {
+    return static_cast<int>(cudaMemcpyToSymbol(scan::tc::g_scan_tc_stall, &at, sizeof(int)));
+}
+#endif
 
 }  // namespace kda

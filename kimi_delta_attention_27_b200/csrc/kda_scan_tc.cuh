@@ -17,7 +17,11 @@ using namespace ptx;
 
 constexpr int N = 128;                    // state size
 constexpr uint32_t kBlock = 16384;        // 128 rows of 128 bytes: 64 bf16 columns
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+#ifdef KDA_TEST_HOOKS
+constexpr uint64_t kWaitLimitNs = 100000000ull;    // 100 ms in the test-only build
+#else
+constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far above any legitimate wait
+#endif
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1) {
     asm volatile(
@@ -93,6 +97,9 @@ struct Ctx {
             }
         }
     }
+    // Whether all lanes' waits were met; the warp is converged behind it. What follows a wait (elect, TMEM loads and stores,
+    // arrivals) takes the whole warp, and a lane that had given up alone would leave the others waiting for it.
+    static __device__ __forceinline__ bool met(bool ok) { return __all_sync(0xffffffffu, ok); }
     // by a converged warp, once for all its lanes
     __device__ __forceinline__ void arrive(int i) const {
         __syncwarp();

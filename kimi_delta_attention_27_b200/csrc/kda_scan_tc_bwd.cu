@@ -35,6 +35,11 @@ namespace scan {
 namespace tc {
 
 __device__ unsigned int g_scan_tc_bwd_error = 0;
+#ifdef KDA_TEST_HOOKS
+// Test-only build (never the product library): the gates of this head of every CTA are not signalled, so that the bounded
+// waits for them run out.
+__device__ int g_scan_tc_bwd_stall = -1;
+#endif
 
 constexpr int TT = kScanTcTile;
 constexpr int kIssuer = 16, NT = 32 * 18;   // warp 17: gates and sums
@@ -238,7 +243,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
         const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
         const uint32_t tQ = tmem + kColQ + 32 * cq + lanes, tM = tmem + kColM + 16 * cq + lanes;
         const uint32_t tX = tmem + kColX + 16 * cq + lanes, tY = tmem + kColY + 16 * cq + lanes;
-        bool ok = x.wait(kBcFull, 0);
+        bool ok = x.met(x.wait(kBcFull, 0));
         if (ok) {
             // rows behind the piece: of other tokens, or none
             uint8_t *t = smem + (cq >> 1 ? L::kB : L::kC) + r * 128 + (NS == 128 ? (cq & 1) * kBlock : (cq & 1) * 64);
@@ -251,7 +256,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
         // the same of x and dy, and leave to compute Qt
         auto ready = [&](int k) {
             if (cnt < TT) {
-                if (!x.wait(kXFull + (k & 1), (k >> 1) & 1)) return false;
+                if (!x.met(x.wait(kXFull + (k & 1), (k >> 1) & 1))) return false;
                 uint8_t *t = smem + L::kXY + ((k & 1) * 2 + (cq >> 1)) * kBlock + r * 128 + (cq & 1) * 64;
                 if (r >= cnt)
 #pragma unroll
@@ -299,7 +304,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
         };
         auto add_to = [](float &dst, float v, bool more) { dst = more ? dst + v : v; };
         float2 gt[16];   // Gt, columns 32 cq .. + 32
-        ok = ok && x.wait(kQ, 0);
+        ok = ok && x.met(x.wait(kQ, 0));
         if (ok) {
             tc_fence_after();
             uint32_t a[32];
@@ -314,8 +319,8 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             const uint32_t ph = k & 1;
             const HeadGates &g = gates[hh & 1];
             uint8_t *xt = smem + L::kXY + stage * 2 * kBlock, *dyt = xt + kBlock;
-            ok = x.wait(kXFull + stage, (k >> 1) & 1) && x.wait(kGatesFull + (hh & 1), (hh >> 1) & 1) &&
-                 (k == 0 || x.wait(kEnd, ph ^ 1));
+            ok = x.met(x.wait(kXFull + stage, (k >> 1) & 1) && x.wait(kGatesFull + (hh & 1), (hh >> 1) & 1) &&
+                       (k == 0 || x.wait(kEnd, ph ^ 1)));
             if (!ok) break;
             tc_fence_after();
             // e^Gamma dy and d e^(Gamma_end - Gamma) x: the first operands with S_0^T and R^T, 32 columns for this thread
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
                 tmem_st16(tmem + (cq >> 1 ? kColSx : kColDy) + 16 * (cq & 1) + lanes, o);
             }
             // S_0 in parts
-            ok = x.wait(kSFull, ph);
+            ok = x.met(x.wait(kSFull, ph));
             if (!ok) break;
 #pragma unroll
             for (int j = 0; j < JS; ++j) {
@@ -351,7 +356,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             tc_fence_before();
             x.arrive(kSParts);
             // ---- Mt, Kt (where S_0 was) and the sums of Mt . Qt
-            ok = x.wait(kSParts, ph ^ 1) && x.wait(kQ, ph ^ 1) && (k == 0 || sl > 0 || x.wait(kSumsFree, (hh - 1) & 1));
+            ok = x.met(x.wait(kSParts, ph ^ 1) && x.wait(kQ, ph ^ 1) && (k == 0 || sl > 0 || x.wait(kSumsFree, (hh - 1) & 1)));
             if (!ok) break;
             tc_fence_after();
             uint32_t m_out[16];
@@ -435,7 +440,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             // Mt lies where the four warps of these lanes have read Qt
             tc_fence_before();
             x.arrive(kQRead + wq);
-            ok = x.wait(kQRead + wq, ph);
+            ok = x.met(x.wait(kQRead + wq, ph));
             if (!ok) break;
             tc_fence_after();
             tmem_st16(tM, m_out);
@@ -444,7 +449,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             tc_fence_before();
             x.arrive(kMk);
             // ---- the dots with C S_0; R in parts where S_0's were, and the two's product
-            ok = x.wait(kSDone, ph);
+            ok = x.met(x.wait(kSDone, ph));
             if (!ok) break;
             tc_fence_after();
             {
@@ -453,7 +458,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
                 tmem_wait_ld();
                 add_to(sums.leave[cq][r], dot_row(a, dyt), sl > 0);
             }
-            ok = x.wait(kRFull, ph);
+            ok = x.met(x.wait(kRFull, ph));
             if (!ok) break;
             float2 rs2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
                 if (lane == 0) add_to(sums.rs[warp], rs, sl > 0);
             }
             // ---- dx, and the dots with B R
-            ok = x.wait(kZ, ph);
+            ok = x.met(x.wait(kZ, ph));
             if (!ok) break;
             tc_fence_after();
             {
@@ -519,7 +524,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             }
             if (sl == slices - 1) x.arrive(kSums);
         }
-        ok = ok && x.wait(kEnd, (work - 1) & 1);
+        ok = ok && x.met(x.wait(kEnd, (work - 1) & 1));
         tc_fence_after();
         // ---- dB and dC: this CTA's share, or the result where it has the whole group
         if (ok) {
@@ -588,9 +593,8 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
         __syncwarp();
         load_xy(0);
         load_state(0, &maps.states, kSFull, L::kK);
-        bool ok = x.wait(kBcFull, 0) && x.wait(kSParts, 0);
+        bool ok = x.met(x.wait(kBcFull, 0) && x.wait(kSParts, 0));
         if (ok) {
-            __syncwarp();
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -602,9 +606,8 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
         for (int k = 0; k < work && ok; ++k) {
             const int stage = k & 1;
             const uint32_t ph = k & 1, xt = base + L::kXY + stage * 2 * kBlock, dyt = xt + kBlock;
-            ok = x.wait(kXFull + stage, (k >> 1) & 1) && x.wait(kQReady, ph);
+            ok = x.met(x.wait(kXFull + stage, (k >> 1) & 1) && x.wait(kQReady, ph));
             if (!ok) break;
-            __syncwarp();
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -612,9 +615,8 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
                 mma_commit(x.bar(kQ));
             }
             __syncwarp();
-            ok = x.wait(kSParts, ph ^ 1);
+            ok = x.met(x.wait(kSParts, ph ^ 1));
             if (!ok) break;
-            __syncwarp();
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -632,9 +634,8 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             }
             __syncwarp();
             load_state(k, &maps.grads, kRFull, L::kXY + (stage ^ 1) * 2 * kBlock);
-            ok = x.wait(kMk, ph);
+            ok = x.met(x.wait(kMk, ph));
             if (!ok) break;
-            __syncwarp();
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -647,9 +648,8 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
                     mma_f16(tmem + kColDb, k_major(kt, j), mn_major(ct, j), kIdDb, !(k == 0 && j == 0));
             }
             __syncwarp();
-            ok = x.wait(kRParts, ph);
+            ok = x.met(x.wait(kRParts, ph));
             if (!ok) break;
-            __syncwarp();
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -668,9 +668,8 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             __syncwarp();
             if (k + 1 < work) {
                 load_xy(k + 1);
-                ok = x.wait(kEnd, ph);   // Kt has been multiplied
+                ok = x.met(x.wait(kEnd, ph));   // Kt has been multiplied
                 if (!ok) break;
-                __syncwarp();
                 load_state(k + 1, &maps.states, kSFull, L::kK);
             }
         }
@@ -691,6 +690,9 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
         for (int hh = 0; hh < heads + 1 && ok; ++hh) {
             if (hh < heads) {
                 make_head_gates(gates[hh & 1], dt, cnt, A, bias, D, p.softplus);
+#ifdef KDA_TEST_HOOKS
+                if (hh != g_scan_tc_bwd_stall)
+#endif
                 x.arrive(kGatesFull + (hh & 1));
                 if (hh + 1 < heads) {
                     fetch(hb + hh + 1);
@@ -700,7 +702,7 @@ __global__ void __launch_bounds__(NT, 1) scan_tc_bwd_kernel(ScanParams p, BwdWor
             // the head before: its gates, and then the place of the next one's
             const int h = hb + hh - 1;
             const HeadGates &g = gates[(hh - 1) & 1];
-            ok = x.wait(kSums, (hh - 1) & 1);
+            ok = x.met(x.wait(kSums, (hh - 1) & 1));
             if (!ok) break;
             // Pairs s < t <= u of dlog a_t: within t's quarter they are what its later rows have more than its later
             // columns, and only there is anything subtracted; with one of the two or both in other quarters they are sums.
@@ -862,5 +864,11 @@ cudaError_t read_and_clear_scan_tc_bwd_error(unsigned int *value) {
     const unsigned int zero = 0;
     return cudaMemcpyToSymbol(scan::tc::g_scan_tc_bwd_error, &zero, sizeof(zero));
 }
+
+#ifdef KDA_TEST_HOOKS
+extern "C" int kda_test_set_scan_tc_bwd_stall(int at) {
+    return static_cast<int>(cudaMemcpyToSymbol(scan::tc::g_scan_tc_bwd_stall, &at, sizeof(int)));
+}
+#endif
 
 }  // namespace kda

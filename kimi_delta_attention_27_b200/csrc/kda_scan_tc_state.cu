@@ -28,6 +28,11 @@ namespace scan {
 namespace tc {
 
 __device__ unsigned int g_scan_state_error = 0;
+#ifdef KDA_TEST_HOOKS
+// Test-only build (never the product library): the gates of this tile of every CTA are not signalled, so that the bounded
+// waits for them run out.
+__device__ int g_scan_tc_state_stall = -1;
+#endif
 
 constexpr int kIssuer = 16, kFeeder = 17, NT = 32 * 21;
 constexpr int TT = kScanTcTile;
@@ -159,10 +164,10 @@ __global__ void __launch_bounds__(NT, 1)
                 const int cnt = count_of(i), st = i & 1, row = half * 64 + (t256 >> 2);
                 const uint32_t ph = (i >> 1) & 1;
                 if (half == 0) {
-                    if (!x.wait(kColsFull + hd * 2 + st, ph) || !x.wait(kGatesFull + hd * 2 + st, ph)) return false;
+                    if (!x.met(x.wait(kColsFull + hd * 2 + st, ph) && x.wait(kGatesFull + hd * 2 + st, ph))) return false;
                     if (cnt < TT && hd == 0) {
                         // rows behind the piece: whatever they hold would multiply zeros below
-                        if (!x.wait(kRowsFull + st, ph)) return false;
+                        if (!x.met(x.wait(kRowsFull + st, ph))) return false;
                         uint8_t *rt = smem + L::kRows + st * 2 * kBlock + (t256 & 1) * kBlock + (t256 >> 1) * 128;
                         if ((t256 >> 1) >= cnt && (t256 & 1) < NS / 64)
 #pragma unroll
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(NT, 1)
                     }
                 }
                 // the last tile's have been multiplied
-                if (i > 0 && !(half ? x.wait(kU + (st ^ 1), ((i - 1) >> 1) & 1) : x.wait(kPFree, (i - 1) & 1))) return false;
+                if (i > 0 && !x.met(half ? x.wait(kU + (st ^ 1), ((i - 1) >> 1) & 1) : x.wait(kPFree, (i - 1) & 1))) return false;
                 const StateGates &g = gates[hd * 2 + st];
                 const uint8_t *ct = smem + L::kCols + (hd * 2 + st) * kBlock;
                 uint8_t *parts = smem + L::kParts + half * S * 2 * kHalf + hd * kHalf;
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(NT, 1)
                 if (i + 1 < tiles) ok = write_parts(i + 1, 0) && write_parts(i + 1, 1);
                 if (!ok) break;
                 if (run.states && mine) store(run.states + ((u.i + cell(i)) * p.H + h) * sn + at_r);
-                ok = x.wait(kU + (i & 1), (i >> 1) & 1);
+                ok = x.met(x.wait(kU + (i & 1), (i >> 1) & 1));
                 if (!ok) break;
                 if (!mine) continue;
                 tc_fence_after();
@@ -246,11 +251,10 @@ __global__ void __launch_bounds__(NT, 1)
         for (int i = 0; i < 2 && i < tiles; ++i) load_rows(i);
         for (int i = 0; i < tiles && ok; ++i) {
             const int st = i & 1;
-            ok = x.wait(kRowsFull + st, (i >> 1) & 1);
+            const bool rows = x.wait(kRowsFull + st, (i >> 1) & 1);
             for (int half = 0; half < 2 && ok; ++half) {
-                ok = x.wait(kParts + half, i & 1);
+                ok = x.met(rows && x.wait(kParts + half, i & 1));
                 if (!ok) break;
-                __syncwarp();
                 tc_fence_after();
                 if (elect_one()) {
                     const uint32_t rt = base + L::kRows + st * 2 * kBlock + half * 4 * 2048;
@@ -267,9 +271,8 @@ __global__ void __launch_bounds__(NT, 1)
                 __syncwarp();
             }
             if (ok && i + 2 < tiles) {
-                ok = x.wait(kU + st, (i >> 1) & 1);   // this tile's rows have been multiplied
+                ok = x.met(x.wait(kU + st, (i >> 1) & 1));   // this tile's rows have been multiplied
                 if (!ok) break;
-                __syncwarp();
                 load_rows(i + 2);
             }
         }
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(NT, 1)
             if ((f & 1) < tiles) steps(f & 1);
             for (int i = f & 1; i < tiles; i += 2) {
                 const int st = i & 1, cnt = count_of(i);
-                if (i >= 2) ok = x.wait(kColsFree + hd * 2 + st, ((i - 2) >> 1) & 1);
+                if (i >= 2) ok = x.met(x.wait(kColsFree + hd * 2 + st, ((i - 2) >> 1) & 1));
                 if (!ok) break;
                 __syncwarp();
                 if (elect_one()) {
@@ -324,6 +327,9 @@ __global__ void __launch_bounds__(NT, 1)
                 reinterpret_cast<float4 *>(g.weight)[lane] = make_float4(w[0], w[1], w[2], w[3]);
                 if (lane == 0) g.total = ex2(all);
                 decay = decay + all;
+#ifdef KDA_TEST_HOOKS
+                if (i != g_scan_tc_state_stall)
+#endif
                 x.arrive(kGatesFull + hd * 2 + st);
             }
             if (lane == 0) rest.decay[f] = decay;
@@ -381,5 +387,11 @@ cudaError_t read_and_clear_scan_state_error(unsigned int *value) {
     const unsigned int zero = 0;
     return cudaMemcpyToSymbol(scan::tc::g_scan_state_error, &zero, sizeof(zero));
 }
+
+#ifdef KDA_TEST_HOOKS
+extern "C" int kda_test_set_scan_tc_state_stall(int at) {
+    return static_cast<int>(cudaMemcpyToSymbol(scan::tc::g_scan_tc_state_stall, &at, sizeof(int)));
+}
+#endif
 
 }  // namespace kda
