@@ -65,8 +65,8 @@ __device__ __forceinline__ void ring_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// 1 / (1 + e^-x) by the hardware's 2^y and 1/y (relative errors about 2^-22 each). With the flushing forms: those
-// that keep denormals bring three times the instructions, which then bound the kernel.
+// 1 / (1 + e^-x) by the hardware's 2^y and 1/y (relative errors about 2^-22 each, and |x| 2^-24 of the rounding of 2^y's
+// argument). With the flushing forms: those that keep denormals bring three times the instructions, which then bound the kernel.
 __device__ __forceinline__ float sigmoidf(float x) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));

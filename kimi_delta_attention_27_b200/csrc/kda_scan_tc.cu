@@ -16,7 +16,7 @@
 // they share C, B and G, and one product with N = 128 reads C or B^T once for both), a thread having half of a row; one
 // thread issues the products; two warps run ahead with the gates and the loads of x. A tile's outputs are finished in the
 // next tile, between the two halves of its parts, so that no product is waited for while there is work, and nothing but
-// Y1 waits for the state. (65536 tokens x 32 heads x 128 in pieces: 565 us, 9650 cycles for two heads' tile; with Y1 and U
+// Y1 waits for the state. (65536 tokens x 32 heads x 128 in pieces: 553 us, 9700 cycles for two heads' tile; with Y1 and U
 // by head 584; warp-level products with tiles of 64 tokens 1.13 ms.)
 //
 // L . G is formed without one exponential per element: with a_b = Gamma at the end of a block of 32 columns,

@@ -1,4 +1,4 @@
-// kda_scan_tc_bwd.cu -- gradients of the selective state space scan on tcgen05, state size 128, sm_100a.
+// kda_scan_tc_bwd.cu -- gradients of the selective state space scan on tcgen05, state sizes 64 and 128, sm_100a.
 //
 // The formulas are those of kda_scan_bwd.cu, with tiles of 128 tokens and the products between tokens transposed, so
 // that a thread has one row s of them and the sums over t that make dB and dx need no transposed operand:
@@ -19,9 +19,9 @@
 // instructions 5200 of each scheduler. Sixteen warps do the elements: they turn S_0 into parts, then, while its products
 // run, form Mt and Kt, then turn R into parts in the same place. One warp issues the products and loads; one makes the
 // gates of the next head and finishes the sums of the last. What is left is the chain of those phases: 2 x 4096 tokens x
-// 64 heads x 64 take 261 us, 13500 cycles per tile and head, tensor cores 34 % and the L1 pipes 49 % busy. (Warp-level
+// 64 heads x 64 take 264 us, 13500 cycles per tile and head, tensor cores 34 % and the L1 pipes 49 % busy. (Warp-level
 // products with tiles of 64 tokens: 536 us. R taken in between the two halves of Mt and Kt, so that its products run
-// under the second: 280 us. States loaded to registers rather than by TMA: 422 us.) At 64: 5 packed sequences, 5001
+// under the second: 280 us. States loaded to registers rather than by TMA: 422 us.) At 64: 5 packed sequences, 3802
 // tokens x 32 heads x 128, 2 groups: 129 us.
 //
 // Every wait is bounded; one that runs out raises kErrTimeout and winds the CTA down.

@@ -13,9 +13,9 @@
 // A CTA takes two heads of a group side by side: one product with N = 128 reads the rows once for both, 64 cycles per
 // K step and part instead of 2 x 48, 1536 per tile with three parts. Eight warps per head form the parts of the next tile,
 // half by half, while this one's product runs, then add U to the state; four warps run ahead with gates and loads. Bound
-// by the elements' chain: parts, fence, U, state. (65536 tokens x 32 heads x 128, two parts: 224 us, 3850 cycles for two
+// by the elements' chain: parts, fence, U, state. (65536 tokens x 32 heads x 128, two parts: 227 us, 4000 cycles for two
 // heads' tile; with tiles of 64 tokens 277. 2 x 4096 tokens x 64 heads x 64, both directions, every tile's states stored:
-// 113 us; 123. The same of 5 packed sequences, 5001 tokens x 32 heads x 128, state size 64: 65 us; warp-level products, 77.)
+// 114 us; 123. The same of 5 packed sequences, 3802 tokens x 32 heads x 128, state size 64: 69 us; warp-level products, 77.)
 //
 // Every wait is bounded; one that runs out raises kErrTimeout and winds the CTA down.
 #include <cuda_bf16.h>
