@@ -232,7 +232,7 @@ kda_status kda_conv_fwd(const void *x, kda_dtype dtype, int64_t x_stride, const 
     const int64_t e = size_of(dtype), row = channels * e, st = static_cast<int64_t>(p.seqs.n) * (taps - 1) * row;
     KDA_TRY(check_stride(p.rows, out_stride, channels, e));
     const Span outs[] = {{out, p.rows, row, out_stride * e}, whole(final_state, st)};
-    const Span ins[] = {{x, p.rows, row, x_stride * e}, whole(initial_state, st), whole(weight, channels * taps * 4LL),
+    const Span ins[] = {{x, p.rows, row, x_stride * e}, whole(initial_state, st), whole(weight, 4LL * channels * taps),
                         whole(bias, channels * 4LL)};
     if (any_overlap(outs, ins)) return KDA_ERR_OVERLAP;
     if (p.seqs.n == 0) return KDA_OK;
@@ -281,11 +281,11 @@ kda_status kda_conv_bwd(const void *x, kda_dtype dtype, int64_t x_stride, const 
     KDA_TRY(check_stride(p.rows, dx_stride, channels, e));
     const size_t need = kda_conv_bwd_workspace(p.rows, channels, taps);
     KDA_TRY(check_workspace(workspace, workspace_bytes, need));
-    const Span outs[] = {{dx, p.rows, row, dx_stride * e}, whole(dweight, channels * taps * 4LL),
+    const Span outs[] = {{dx, p.rows, row, dx_stride * e}, whole(dweight, 4LL * channels * taps),
                          whole(dbias, channels * 4LL), whole(dinitial_state, st),
                          whole(workspace, static_cast<int64_t>(need))};
     const Span ins[] = {{x, p.rows, row, x_stride * e}, {dout, p.rows, channels * ed, dout_stride * ed},
-                        whole(weight, channels * taps * 4LL), whole(bias, channels * 4LL), whole(initial_state, st),
+                        whole(weight, 4LL * channels * taps), whole(bias, channels * 4LL), whole(initial_state, st),
                         whole(dfinal_state, st)};
     if (any_overlap(outs, ins)) return KDA_ERR_OVERLAP;
     KDA_TRY(check_device());
@@ -322,7 +322,7 @@ kda_status kda_conv_decode(const void *x, kda_dtype dtype, int64_t x_stride, con
     KDA_TRY(check_stride(batch, out_stride, channels, e));
     if (state_in != state_out && overlap(whole(state_in, st), whole(state_out, st))) return KDA_ERR_STATE_OVERLAP;
     const Span outs[] = {{out, batch, row, out_stride * e}, whole(state_out, st)};
-    const Span ins[] = {{x, batch, row, x_stride * e}, whole(weight, channels * taps * 4LL), whole(bias, channels * 4LL)};
+    const Span ins[] = {{x, batch, row, x_stride * e}, whole(weight, 4LL * channels * taps), whole(bias, channels * 4LL)};
     if (any_overlap(outs, ins) || overlap(outs[0], whole(state_in, st))) return KDA_ERR_OVERLAP;
     if (batch == 0) return KDA_OK;
     KDA_TRY(check_device());

@@ -357,3 +357,10 @@ def test_scan_bwd_of_long_sequences_in_pieces(lib, name, N):
     g, again = base.call_bwd(d, lengths, softplus), base.call_bwd(d, lengths, softplus)
     assert kda.device_error() == 0 and all(g[k] is None or torch.equal(g[k], again[k]) for k in g)
     base.check_bwd(d, lengths, softplus, g)
+
+
+def test_conv_weight_of_many_channels_is_seen_whole(lib):
+    """2^30 channels x 4 taps are 16 GiB of weights: an output in the midst of them is refused."""
+    at = lambda i: ctypes.c_void_p(i << 40)  # noqa: E731
+    out = ctypes.c_void_p((5 << 40) + (1 << 33))
+    assert lib.kda_conv_decode(at(1), 1, 1 << 30, at(5), None, 1, 3, 1 << 30, 4, at(2), at(3), out, 1 << 30, None) == 16
