@@ -27,6 +27,7 @@ struct Span {
     int64_t rows, width, stride;
 };
 Span whole(const void *p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+Span offsets(const kda::Seqs &s) { return whole(s.cu, (static_cast<int64_t>(s.n) + 1) * 4); }
 
 // Whether two buffers share a byte. Rows with the same stride may be interleaved (slices of one
 // tensor's columns): those share none where their columns do not meet.
@@ -233,7 +234,7 @@ kda_status kda_conv_fwd(const void *x, kda_dtype dtype, int64_t x_stride, const 
     KDA_TRY(check_stride(p.rows, out_stride, channels, e));
     const Span outs[] = {{out, p.rows, row, out_stride * e}, whole(final_state, st)};
     const Span ins[] = {{x, p.rows, row, x_stride * e}, whole(initial_state, st), whole(weight, 4LL * channels * taps),
-                        whole(bias, channels * 4LL)};
+                        whole(bias, channels * 4LL), offsets(p.seqs)};
     if (any_overlap(outs, ins)) return KDA_ERR_OVERLAP;
     if (p.seqs.n == 0) return KDA_OK;
     KDA_TRY(check_device());
@@ -286,7 +287,7 @@ kda_status kda_conv_bwd(const void *x, kda_dtype dtype, int64_t x_stride, const 
                          whole(workspace, static_cast<int64_t>(need))};
     const Span ins[] = {{x, p.rows, row, x_stride * e}, {dout, p.rows, channels * ed, dout_stride * ed},
                         whole(weight, 4LL * channels * taps), whole(bias, channels * 4LL), whole(initial_state, st),
-                        whole(dfinal_state, st)};
+                        whole(dfinal_state, st), offsets(p.seqs)};
     if (any_overlap(outs, ins)) return KDA_ERR_OVERLAP;
     KDA_TRY(check_device());
     p.C = channels;
@@ -474,7 +475,7 @@ kda_status kda_scan_fwd(const void *x, int64_t x_stride, const float *dt, const 
     const Span outs[] = {{out, rows, wx, out_stride * 2}, ho, whole(need ? workspace : nullptr, static_cast<int64_t>(need))};
     const Span ins[] = {{x, rows, wx, x_stride * 2}, {B, rows, wb, b_stride * 2}, {C, rows, wb, c_stride * 2},
                         whole(dt, rows * num_heads * 4), whole(A, num_heads * 4LL), whole(D, num_heads * 4LL),
-                        whole(dt_bias, num_heads * 4LL)};
+                        whole(dt_bias, num_heads * 4LL), offsets(s)};
     if (any_overlap(outs, ins) || overlap(outs[0], hi) || overlap(outs[2], hi)) return KDA_ERR_OVERLAP;
     if (s.n == 0) return KDA_OK;
     KDA_TRY(check_device());
@@ -537,7 +538,7 @@ kda_status kda_scan_bwd(const void *x, int64_t x_stride, const float *dt, const 
                         {B, rows, gn * 2, b_stride * 2}, {C, rows, gn * 2, c_stride * 2},
                         whole(dt, rows * num_heads * 4), whole(A, num_heads * 4LL), whole(D, num_heads * 4LL),
                         whole(dt_bias, num_heads * 4LL), whole(initial_state, st * size_of(initial_dtype)),
-                        whole(dfinal_state, st * 4)};
+                        whole(dfinal_state, st * 4), offsets(s)};
     if (any_overlap(outs, ins)) return KDA_ERR_OVERLAP;
     KDA_TRY(check_device());
     kda::ScanParams p;

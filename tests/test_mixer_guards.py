@@ -364,3 +364,24 @@ def test_conv_weight_of_many_channels_is_seen_whole(lib):
     at = lambda i: ctypes.c_void_p(i << 40)  # noqa: E731
     out = ctypes.c_void_p((5 << 40) + (1 << 33))
     assert lib.kda_conv_decode(at(1), 1, 1 << 30, at(5), None, 1, 3, 1 << 30, 4, at(2), at(3), out, 1 << 30, None) == 16
+
+
+def test_outputs_over_the_offsets_are_refused(lib):
+    """cu_seqlens is an input like the others: a kernel that wrote over it would look its sequences up in its own results."""
+    OVERLAP, n, f = 16, 5, [ctypes.c_void_p((i + 1) << 36) for i in range(16)]   # aligned, never dereferenced
+    cu, last = f[15], ctypes.c_void_p((16 << 36) + 16)                           # the last of six offsets at + 20
+    conv = lambda **o: lib.kda_conv_fwd(f[0], 1, 64, f[1], None, 1, cu, n, 1, 100, 64, 4, None, o.get("final", f[3]),  # noqa: E731
+                                        o.get("out", f[2]), 64, None)
+    assert conv(out=last) == OVERLAP and conv(final=last) == OVERLAP
+    conv = lambda **o: lib.kda_conv_bwd(f[0], 1, 64, f[1], None, 1, cu, n, 1, 100, 64, 4, None, f[3], 1, 64, None,  # noqa: E731
+                                        o.get("dx", f[4]), 64, o.get("dw", f[5]), None, None, o.get("ws", f[6]), 1 << 30, None)
+    assert conv(dx=last) == OVERLAP and conv(dw=last) == OVERLAP
+    scan = lambda **o: lib.kda_scan_fwd(f[0], 256, f[1], f[2], f[3], 128, f[4], 128, None, None, 1, cu, n, 1, 100, 4, 1, 64,  # noqa: E731
+                                        128, None, 0, o.get("hT", f[7]), 2, o.get("out", f[5]), 256, f[6], 1 << 34, None)
+    assert scan(out=last) == OVERLAP and scan(hT=last) == OVERLAP
+    scan = lambda **o: lib.kda_scan_bwd(f[0], 256, f[1], f[2], f[3], 128, f[4], 128, None, None, 1, cu, n, 1, 100, 4, 1, 64,  # noqa: E731
+                                        128, None, 0, f[5], 256, None, f[6], 256, o.get("ddt", f[7]), f[8], f[9], 128, f[10],
+                                        128, None, None, None, o.get("ws", f[11]), 1 << 34, None)
+    assert scan(ddt=last) == OVERLAP and scan(ws=cu) == OVERLAP
+    if not torch.cuda.is_available():
+        assert conv() == 5 and scan() == 5              # let through, as far as the device query
