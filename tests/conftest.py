@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -18,3 +19,10 @@ def oracle_mod():
     import oracle
     oracle._load()
     return oracle
+
+
+@pytest.fixture(scope="module", autouse=True)
+def collected():
+    """Tensors that an earlier module's tests left in reference cycles (a caught exception's frames) go before a module's
+    tests run, not in the midst of one that counts what is allocated."""
+    gc.collect()
