@@ -385,3 +385,21 @@ def test_outputs_over_the_offsets_are_refused(lib):
     assert scan(ddt=last) == OVERLAP and scan(ws=cu) == OVERLAP
     if not torch.cuda.is_available():
         assert conv() == 5 and scan() == 5              # let through, as far as the device query
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [64, 128])
+@pytest.mark.parametrize("lengths", [[140], [290, 11]])
+def test_scan_steps_below_zero_that_let_the_state_grow(lib, monkeypatch, lengths, N):
+    """By up to 2^57 over 128 tokens, and by as much down again in other stretches."""
+    import test_scan as base
+    monkeypatch.setattr(base, "mags", terms_of_steps_of_both_signs)
+    d = base.make(lengths, 3, 1, 64, N, seed=N + 1)
+    d["bias"] = d["D"] = None
+    t = torch.arange(sum(lengths))[:, None]
+    d["A"] = -torch.tensor([1.0, 0.5, 2.0])
+    d["dt"] = torch.where(t // 130 % 2 == 0, -0.31, 0.31) * (0.9 + 0.1 * torch.rand(sum(lengths), 3)) / d["A"].abs()
+    out, hT = base.call_fwd(d, lengths, False, final_state_dtype=torch.float32)
+    base.check_fwd(d, lengths, False, out, hT)
+    base.check_bwd(d, lengths, False, base.call_bwd(d, lengths, False))
+    assert kda.device_error() == 0
